@@ -449,13 +449,16 @@ def _code_only(src):
 def kernel_source_hash(workload=None):
     """Hash of the CUDA sources a workload's kernels are built from: the SSD
     prefill's (ssd* and the three SSU headers it includes) or the SSU decode's
-    (every other source), so that a change to one leaves the other's ncu
+    (every other source but the layer_* operators', which no workload here
+    runs), so that a change to one leaves the other's ncu
     traffic record valid.  Only the code is hashed: an edit to comments or
     whitespace leaves the records valid."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mamba2_ssm_decode_gb300", "csrc")
     ssd = workload == SSD_WORKLOAD
     for f in sorted(os.listdir(csrc)):
+        if f.startswith("layer_"):
+            continue
         if f.startswith("ssd") != ssd and not (ssd and f in ("ssu_headrun.cuh", "ssu_kernel.cuh",
                                                           "ssu_bulk.cuh")):
             continue

@@ -468,6 +468,192 @@ ssu_status ssd_combined_fwd_varlen(const ssd_params* p, void* workspace, int64_t
                                    struct CUstream_st* stream);
 
 /*
+ * Depthwise causal convolution in front of the state update (what produces
+ * x, B and C of a Mamba layer from its input projection).  For channel c and
+ * row t of a sequence, xs being the rows that the sequence's slot holds
+ * followed by the call's rows:
+ *   y[t][c] = act(bias[c] + sum_{j < width} weight[c][j] xs[t - (width-1) + j][c])
+ * and the slot then holds the last width - 1 rows of xs.  Sums in fp32.
+ *
+ * conv_state  [slots, width - 1, channels], contiguous, io_dtype (the rows are
+ *             kept as given, so caching them rounds nothing); the last row is
+ *             the newest.
+ * io_dtype    F32, BF16 or F16: x, out and conv_state.
+ * x, out      [rows, channels]: element (r, c) at r * row_stride + c (strides
+ *             in elements; a column slice of a wider projection is fine).
+ * weight      [channels, width] contiguous, weight_dtype; width 2, 3 or 4.
+ * bias        [channels], weight_dtype, or NULL.
+ * weight_dtype  io_dtype or F32.
+ * activation  an ssu_activation.
+ * disable_state_update  1: no slot is written.
+ */
+typedef enum ssu_activation { SSU_ACT_NONE = 0, SSU_ACT_SILU = 1 } ssu_activation;
+
+typedef struct ssu_conv_params {
+  void* conv_state;
+  int64_t slots, channels, width;
+  ssu_dtype io_dtype;
+  const void* x;
+  int64_t x_row_stride;
+  void* out;
+  int64_t out_row_stride;
+  const void* weight;
+  const void* bias;
+  ssu_dtype weight_dtype;
+  int activation;
+  int disable_state_update;
+  int64_t pad_slot_id;
+} ssu_conv_params;
+
+/*
+ * Decode form: one or a few rows per sequence.  Sequences, rows, slot tables
+ * and num_accepted_tokens as in ssu_update_varlen (one token per sequence:
+ * cu_seqlens NULL, dense_steps 1): the rows before a sequence's first come
+ * from its read slot, and the slot of step t takes the state after row t.  A
+ * pad / out-of-range read slot runs from zero rows and writes no slot.  One
+ * launch.  out may be x itself (not an overlapping view of it).
+ */
+ssu_status ssu_conv_update(const ssu_conv_params* p, int64_t nseqs, int64_t rows,
+                           const void* cu_seqlens, int64_t dense_steps,
+                           const void* num_accepted_tokens, ssu_dtype meta_dtype,
+                           const ssu_slot_table* src, const ssu_slot_table* dst,
+                           ssu_dtype index_dtype, struct CUstream_st* stream);
+
+/*
+ * Prompt form: packed sequences of any length; each writes its slot once,
+ * after its last row.
+ *   cu_seqlens               [nseqs + 1] row starts, not decreasing
+ *                            (meta_dtype); ranges are clamped to [0, rows).
+ *   state_batch_indices      [nseqs] read slots, or NULL for slot s.
+ *   dst_state_batch_indices  [nseqs] write slots, or NULL: the read slot.
+ *   has_initial_state        [nseqs] bytes, or NULL (all 1): 0 starts the
+ *                            sequence from zeros, whatever its slot holds (not
+ *                            even infinities or NaN get through); its slot is
+ *                            written all the same.
+ * conv_state may be NULL (then there are no slots: every sequence starts from
+ * zeros and nothing is kept).  Pad / out-of-range slots as in the decode form.
+ * An empty sequence reads and writes nothing.  out must not overlap x.  One
+ * launch.
+ */
+ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* p, int64_t nseqs, int64_t rows,
+                               const void* cu_seqlens, ssu_dtype meta_dtype,
+                               const void* state_batch_indices,
+                               const void* dst_state_batch_indices, ssu_dtype index_dtype,
+                               const uint8_t* has_initial_state, struct CUstream_st* stream);
+
+/*
+ * Selective scan whose A varies along dstate (the Mamba-1 form; A that is one
+ * value per head or channel is ssu_update's and ssd_combined_fwd_varlen's).
+ * For channel c, group g = c / (channels / ngroups) and row r:
+ *   dt' = dt[r][c] + dt_bias[c];  dt' = softplus(dt') if dt_softplus
+ *   h[c][n] <- exp(A[c][n] dt') h[c][n] + dt' x[r][c] B[r][g][n]
+ *   y[r][c]  = sum_n h[c][n] C[r][g][n] + D[c] x[r][c];  y *= silu(z[r][c]) if z
+ * in fp32; a state is rounded (to nearest even) only where it is stored.
+ *
+ * state      [slots, channels, dstate], contiguous, 16-byte aligned, F32 /
+ *            BF16 / F16; dstate 16, 32, 64, 128 or 256.
+ * io_dtype   F32, BF16 or F16: x, z, B and C.
+ * x, z, dt, out  [rows, channels] with unit channel stride; dt in io_dtype or
+ *            F32, out in io_dtype or F32; z may be NULL.
+ * B, C       [rows, ngroups, dstate], unit dstate stride.
+ * A          [channels, dstate] fp32, unit dstate stride, A_row_stride between
+ *            channels.  D, dt_bias [channels] fp32 contiguous, or NULL.
+ * disable_state_update  1: no slot is written.
+ */
+typedef struct ssu_scan_params {
+  void* state;
+  ssu_dtype state_dtype;
+  int64_t slots, channels, dstate, ngroups;
+  ssu_dtype io_dtype;
+  const void* x;
+  int64_t x_row_stride;
+  const void* z;
+  int64_t z_row_stride;
+  void* out;
+  ssu_dtype out_dtype;
+  int64_t out_row_stride;
+  const void* dt;
+  ssu_dtype dt_dtype;
+  int64_t dt_row_stride;
+  const void* B;
+  int64_t B_row_stride, B_group_stride;
+  const void* C;
+  int64_t C_row_stride, C_group_stride;
+  const float* A;
+  int64_t A_row_stride;
+  const float* D;
+  const float* dt_bias;
+  int dt_softplus;
+  int disable_state_update;
+  int64_t pad_slot_id;
+} ssu_scan_params;
+
+/* Decode form; sequences, rows and slots as in ssu_conv_update.  One launch. */
+ssu_status ssu_scan_update(const ssu_scan_params* p, int64_t nseqs, int64_t rows,
+                           const void* cu_seqlens, int64_t dense_steps,
+                           const void* num_accepted_tokens, ssu_dtype meta_dtype,
+                           const ssu_slot_table* src, const ssu_slot_table* dst,
+                           ssu_dtype index_dtype, struct CUstream_st* stream);
+
+/* Prompt form; arguments and rules as in ssu_conv_fwd_varlen (state may be
+ * NULL; out must not overlap an operand).  One launch. */
+ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* p, int64_t nseqs, int64_t rows,
+                               const void* cu_seqlens, ssu_dtype meta_dtype,
+                               const void* state_batch_indices,
+                               const void* dst_state_batch_indices, ssu_dtype index_dtype,
+                               const uint8_t* has_initial_state, struct CUstream_st* stream);
+
+/*
+ * Moves of whole slots, over every pool that the slot ids index (the state and
+ * convolution pools of all layers, ring caches, trackers) in one call.  A pool
+ * is `slots` slots of slot_bytes bytes, slot_stride_bytes apart; any element
+ * type.  At most SSU_SLOTS_MAX_POOLS pools and 2^20 slots.
+ */
+typedef struct ssu_pool {
+  void* data;
+  int64_t slot_bytes, slot_stride_bytes;
+} ssu_pool;
+
+#define SSU_SLOTS_MAX_POOLS 256
+
+/*
+ * Copy slot src[i] to slot dst[i] in every pool, i < pairs (index_dtype).  One
+ * source may be copied to many slots (a fork).  A pair with a pad /
+ * out-of-range id is skipped, one that copies a slot to itself does nothing.
+ * A slot written by one pair and read or written by another races.  One
+ * launch.
+ */
+ssu_status ssu_slots_copy(const ssu_pool* pools, int npools, int64_t slots, const void* src,
+                          const void* dst, ssu_dtype index_dtype, int64_t pairs,
+                          int64_t pad_slot_id, struct CUstream_st* stream);
+
+/* Zero slot ids[i] of every pool, i < count (freed slots, or ones about to
+ * start a sequence); pad / out-of-range ids are skipped.  One launch. */
+ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, const void* ids,
+                           ssu_dtype index_dtype, int64_t count, int64_t pad_slot_id,
+                           struct CUstream_st* stream);
+
+/*
+ * Close the pools up.  The live slots are the distinct valid entries of
+ * `table` ([entries], any shape flattened; pad and out-of-range entries are
+ * not slots, and a slot may be entered more than once).  With m of them, those
+ * with ids below m stay; the k-th live slot at or beyond m (in ascending
+ * order) moves to the k-th free slot below m, in every pool; *num_live = m and
+ * table_out (may be table) holds the entries under their new ids, others
+ * unchanged.  Slots from m on are free afterwards; their bytes are left.
+ *   workspace  device memory of ssu_slots_compact_workspace_bytes(slots) bytes
+ *              (-1 for a negative size), 16-byte aligned; nothing in it need
+ *              be kept between calls.
+ * Two launches; the host learns num_live only if it reads it.
+ */
+int64_t ssu_slots_compact_workspace_bytes(int64_t slots);
+
+ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, const void* table,
+                             void* table_out, ssu_dtype index_dtype, int64_t entries,
+                             int64_t pad_slot_id, int32_t* num_live, void* workspace,
+                             int64_t workspace_bytes, struct CUstream_st* stream);
+
+/*
  * Bits of the device-side error word (values, not bit positions).
  */
 #define SSU_DEVICE_ERR_COPY_TIMEOUT 1u    /* a state tile copy never landed */

@@ -91,6 +91,41 @@ class SSDParams(ctypes.Structure):
     ]
 
 
+class ConvParams(ctypes.Structure):
+    """struct ssu_conv_params."""
+
+    _fields_ = [("conv_state", _c_p), ("slots", _c_i64), ("channels", _c_i64), ("width", _c_i64),
+                ("io_dtype", _c_int), ("x", _c_p), ("x_row_stride", _c_i64), ("out", _c_p),
+                ("out_row_stride", _c_i64), ("weight", _c_p), ("bias", _c_p),
+                ("weight_dtype", _c_int), ("activation", _c_int),
+                ("disable_state_update", _c_int), ("pad_slot_id", _c_i64)]
+
+
+class ScanParams(ctypes.Structure):
+    """struct ssu_scan_params."""
+
+    _fields_ = [
+        ("state", _c_p), ("state_dtype", _c_int),
+        ("slots", _c_i64), ("channels", _c_i64), ("dstate", _c_i64), ("ngroups", _c_i64),
+        ("io_dtype", _c_int),
+        ("x", _c_p), ("x_row_stride", _c_i64), ("z", _c_p), ("z_row_stride", _c_i64),
+        ("out", _c_p), ("out_dtype", _c_int), ("out_row_stride", _c_i64),
+        ("dt", _c_p), ("dt_dtype", _c_int), ("dt_row_stride", _c_i64),
+        ("B", _c_p), ("B_row_stride", _c_i64), ("B_group_stride", _c_i64),
+        ("C", _c_p), ("C_row_stride", _c_i64), ("C_group_stride", _c_i64),
+        ("A", _c_p), ("A_row_stride", _c_i64), ("D", _c_p), ("dt_bias", _c_p),
+        ("dt_softplus", _c_int), ("disable_state_update", _c_int), ("pad_slot_id", _c_i64),
+    ]
+
+
+class Pool(ctypes.Structure):
+    """struct ssu_pool."""
+
+    _fields_ = [("data", _c_p), ("slot_bytes", _c_i64), ("slot_stride_bytes", _c_i64)]
+
+
+SLOTS_MAX_POOLS = 256   # SSU_SLOTS_MAX_POOLS
+
 _lock = threading.Lock()
 _lib = None
 
@@ -124,6 +159,26 @@ def lib() -> ctypes.CDLL:
         L.ssd_workspace_bytes.argtypes = [_c_i64] * 6
         L.ssd_combined_fwd_varlen.restype = _c_int
         L.ssd_combined_fwd_varlen.argtypes = [ctypes.POINTER(SSDParams), _c_p, _c_i64, _c_p]
+        decode = [_c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_int, ctypes.POINTER(SlotTable),
+                  ctypes.POINTER(SlotTable), _c_int, _c_p]
+        prompt = [_c_i64, _c_i64, _c_p, _c_int, _c_p, _c_p, _c_int, _c_p, _c_p]
+        for name, params, args in (("ssu_conv_update", ConvParams, decode),
+                                   ("ssu_conv_fwd_varlen", ConvParams, prompt),
+                                   ("ssu_scan_update", ScanParams, decode),
+                                   ("ssu_scan_fwd_varlen", ScanParams, prompt)):
+            f = getattr(L, name)
+            f.restype, f.argtypes = _c_int, [ctypes.POINTER(params), *args]
+        L.ssu_slots_copy.restype = _c_int
+        L.ssu_slots_copy.argtypes = [ctypes.POINTER(Pool), _c_int, _c_i64, _c_p, _c_p, _c_int,
+                                     _c_i64, _c_i64, _c_p]
+        L.ssu_slots_clear.restype = _c_int
+        L.ssu_slots_clear.argtypes = [ctypes.POINTER(Pool), _c_int, _c_i64, _c_p, _c_int, _c_i64,
+                                      _c_i64, _c_p]
+        L.ssu_slots_compact_workspace_bytes.restype = _c_i64
+        L.ssu_slots_compact_workspace_bytes.argtypes = [_c_i64]
+        L.ssu_slots_compact.restype = _c_int
+        L.ssu_slots_compact.argtypes = [ctypes.POINTER(Pool), _c_int, _c_i64, _c_p, _c_p, _c_int,
+                                        _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p]
         L.ssu_ring_update.restype = _c_int
         L.ssu_ring_update.argtypes = [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64,
                                       _c_int, _c_i64, _c_int, _c_i32, _c_i32, _c_i64, _c_p]

@@ -1,0 +1,219 @@
+// layer_scan.cu -- argument checks and entry points of the selective scan, and
+// the checks of sequence metadata that it shares with the convolution.
+#include "layer_scan.cuh"
+
+namespace layer {
+
+static ssu_status table_args(const ssu_slot_table* t, const char* name, TableArgs* out) {
+  *out = TableArgs{nullptr, 0, 0, 0, 0};
+  if (!t || !t->indices) return SSU_OK;
+  if (t->numel < 0 || t->steps < 0)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "%s: numel and steps must be >= 0", name);
+  *out = TableArgs{t->indices, t->numel, t->seq_stride, t->step_stride, t->steps};
+  return SSU_OK;
+}
+
+static ssu_status check_counts(int64_t nseqs, int64_t rows) {
+  if (nseqs < 0 || rows < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "nseqs and rows must be >= 0");
+  if (nseqs > 0x7fffffffLL || rows > 0x7fffffffLL)
+    return fail(SSU_ERR_UNSUPPORTED, "nseqs and rows must be below 2^31");
+  return SSU_OK;
+}
+
+ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
+                        int64_t dense_steps, const void* na, ssu_dtype meta_dtype,
+                        const ssu_slot_table* src, const ssu_slot_table* dst,
+                        ssu_dtype index_dtype, VarlenArgs* out) {
+  ssu_status st = check_counts(nseqs, rows);
+  VarlenArgs a{};
+  if (st == SSU_OK) st = table_args(src, "state_batch_indices", &a.src);
+  if (st == SSU_OK) st = table_args(dst, "dst_state_batch_indices", &a.dst);
+  if (st != SSU_OK) return st;
+  if ((a.src.idx || a.dst.idx) && !is_index(index_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "slot tables must be int32 or int64");
+  if ((cu || na) && !is_index(meta_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "cu_seqlens / num_accepted_tokens must be int32 or int64");
+  if (na && !a.src.idx)
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "num_accepted_tokens selects the read slot, so it needs state_batch_indices to "
+                "read it from");
+  if (!cu && (dense_steps < 1 || nseqs * dense_steps != rows))
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "without cu_seqlens %lld rows cannot be split into %lld sequences of %lld steps",
+                (long long)rows, (long long)nseqs, (long long)dense_steps);
+  if (!a.src.idx && nseqs > slots)
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "without state_batch_indices sequence s uses slot s: %lld sequences exceed %lld "
+                "slots",
+                (long long)nseqs, (long long)slots);
+  a.rows = rows;
+  a.cu = cu;
+  a.dense_steps = dense_steps;
+  a.na = na;
+  a.meta64 = meta_dtype == SSU_I64;
+  a.idx64 = index_dtype == SSU_I64;
+  *out = a;
+  return SSU_OK;
+}
+
+ssu_status check_prompts(bool pool, int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
+                         ssu_dtype meta_dtype, const void* src, const void* dst,
+                         ssu_dtype index_dtype, VarlenArgs* out) {
+  ssu_status st = check_counts(nseqs, rows);
+  if (st != SSU_OK) return st;
+  if (!cu) return fail(SSU_ERR_INVALID_ARGUMENT, "cu_seqlens must not be NULL");
+  if (!is_index(meta_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "cu_seqlens must be int32 or int64");
+  if ((src || dst) && !is_index(index_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "state_batch_indices must be int32 or int64");
+  if ((src || dst) && !pool)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "slots need the state pool that they index");
+  if (pool && !src && nseqs > slots)
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "without state_batch_indices sequence s uses slot s: %lld sequences exceed %lld "
+                "slots",
+                (long long)nseqs, (long long)slots);
+  VarlenArgs a{};
+  a.rows = rows;
+  a.cu = cu;
+  a.meta64 = meta_dtype == SSU_I64;
+  if (src) a.src = TableArgs{src, nseqs, 1, 1, 1};
+  if (dst) a.dst = TableArgs{dst, nseqs, 1, 1, 1};
+  a.idx64 = index_dtype == SSU_I64;
+  *out = a;
+  return SSU_OK;
+}
+
+static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_needed,
+                             ScanArgs* p) {
+  if (!c) return fail(SSU_ERR_INVALID_ARGUMENT, "params must not be NULL");
+  if (!is_float(c->state_dtype))
+    return fail(SSU_ERR_UNSUPPORTED, "state dtype must be f32, bf16 or f16");
+  if (!is_float(c->io_dtype))
+    return fail(SSU_ERR_UNSUPPORTED, "x/z/B/C dtype must be f32, bf16 or f16");
+  if (c->dt_dtype != c->io_dtype && c->dt_dtype != SSU_F32)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "dt must have the x dtype or be f32");
+  if (c->out_dtype != c->io_dtype && c->out_dtype != SSU_F32)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out must have the x dtype or be f32");
+  if (c->slots < 0 || c->channels < 1 || c->dstate < 1 || c->ngroups < 1)
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "state must be [slots, channels, dstate] with positive sizes, got [%lld, %lld, "
+                "%lld], ngroups %lld",
+                (long long)c->slots, (long long)c->channels, (long long)c->dstate,
+                (long long)c->ngroups);
+  if (c->channels > (1 << 24)) return fail(SSU_ERR_UNSUPPORTED, "channels must not exceed 2^24");
+  if (c->channels % c->ngroups != 0)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "channels (%lld) must be a multiple of ngroups (%lld)",
+                (long long)c->channels, (long long)c->ngroups);
+  const int64_t n = c->dstate;
+  if (n != 16 && n != 32 && n != 64 && n != 128 && n != 256)
+    return fail(SSU_ERR_UNSUPPORTED, "dstate %lld is not one of 16, 32, 64, 128, 256",
+                (long long)n);
+  if (rows > 0 && (!c->x || !c->out || !c->dt || !c->B || !c->C || !c->A))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "x, out, dt, B, C and A must not be NULL");
+  if (rows > 1 && c->out_row_stride < c->channels)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out rows overlap: a stride of %lld for %lld channels",
+                (long long)c->out_row_stride, (long long)c->channels);
+  if (pool_needed && !c->state && c->slots > 0)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "state must not be NULL");
+  if (!aligned(c->state, 16))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "state must be 16-byte aligned");
+  const int es = size_of(c->io_dtype);
+  if (!aligned(c->x, es) || !aligned(c->z, es) || !aligned(c->B, es) || !aligned(c->C, es) ||
+      !aligned(c->dt, size_of(c->dt_dtype)) || !aligned(c->out, size_of(c->out_dtype)) ||
+      !aligned(c->A, 4) || !aligned(c->D, 4) || !aligned(c->dt_bias, 4))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "operands must be aligned to their element size");
+  *p = ScanArgs{};
+  p->state = c->state;
+  p->slots = c->state ? c->slots : 0;
+  p->C = (int)c->channels;
+  p->G = (int)c->ngroups;
+  p->per.init((uint32_t)(c->channels / c->ngroups));
+  p->x = c->x;
+  p->x_rs = c->x_row_stride;
+  p->z = c->z;
+  p->z_rs = c->z_row_stride;
+  p->out = c->out;
+  p->o_rs = c->out_row_stride;
+  p->out_f32 = c->out_dtype == SSU_F32;
+  p->dt = c->dt;
+  p->dt_rs = c->dt_row_stride;
+  p->dt_f32 = c->dt_dtype == SSU_F32;
+  p->B = c->B;
+  p->B_rs = c->B_row_stride;
+  p->B_gs = c->B_group_stride;
+  p->Cm = c->C;
+  p->C_rs = c->C_row_stride;
+  p->C_gs = c->C_group_stride;
+  p->bc_vec = aligned(c->B, 16) && aligned(c->C, 16) && c->B_row_stride * es % 16 == 0 &&
+              c->C_row_stride * es % 16 == 0 &&
+              (c->ngroups == 1 ||
+               (c->B_group_stride * es % 16 == 0 && c->C_group_stride * es % 16 == 0));
+  p->A = c->A;
+  p->A_rs = c->A_row_stride;
+  p->a_vec = aligned(c->A, 16) && c->A_row_stride % 4 == 0;
+  p->D = c->D;
+  p->bias = c->dt_bias;
+  p->softplus = c->dt_softplus != 0;
+  p->disable = c->disable_state_update != 0;
+  p->pad = c->pad_slot_id;
+  return SSU_OK;
+}
+
+static cudaError_t launch_scan(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
+                               int64_t nseqs, cudaStream_t stream) {
+  const int N = (int)c->dstate;
+  switch (c->io_dtype) {
+    case SSU_F32: return launch_scan_f32(c->state_dtype, N, p, a, nseqs, stream);
+    case SSU_BF16: return launch_scan_bf16(c->state_dtype, N, p, a, nseqs, stream);
+    case SSU_F16: return launch_scan_f16(c->state_dtype, N, p, a, nseqs, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace layer
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+ssu_status ssu_scan_update(const ssu_scan_params* c, int64_t nseqs, int64_t rows,
+                           const void* cu_seqlens, int64_t dense_steps,
+                           const void* num_accepted_tokens, ssu_dtype meta_dtype,
+                           const ssu_slot_table* src, const ssu_slot_table* dst,
+                           ssu_dtype index_dtype, struct CUstream_st* stream) {
+  using namespace layer;
+  ScanArgs p;
+  VarlenArgs a;
+  ssu_status st = check_scan(c, rows, true, &p);
+  if (st == SSU_OK)
+    st = check_packed(c->slots, nseqs, rows, cu_seqlens, dense_steps, num_accepted_tokens,
+                      meta_dtype, src, dst, index_dtype, &a);
+  if (st != SSU_OK) return st;
+  if (nseqs == 0 || rows == 0) return ok();
+  return launched(launch_scan(c, p, a, nseqs, (cudaStream_t)stream));
+}
+
+ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t rows,
+                               const void* cu_seqlens, ssu_dtype meta_dtype,
+                               const void* state_batch_indices,
+                               const void* dst_state_batch_indices, ssu_dtype index_dtype,
+                               const uint8_t* has_initial_state, struct CUstream_st* stream) {
+  using namespace layer;
+  ScanArgs p;
+  VarlenArgs a;
+  ssu_status st = check_scan(c, rows, false, &p);
+  if (st == SSU_OK)
+    st = check_prompts(c->state != nullptr, c->slots, nseqs, rows, cu_seqlens, meta_dtype,
+                       state_batch_indices, dst_state_batch_indices, index_dtype, &a);
+  if (st != SSU_OK) return st;
+  if (rows > 0 && (c->out == c->x || c->out == c->dt || c->out == c->z))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not be an operand");
+  if (nseqs == 0 || rows == 0) return ok();
+  p.has_init = has_initial_state;
+  p.final_only = 1;
+  return launched(launch_scan(c, p, a, nseqs, (cudaStream_t)stream));
+}
+
+}  // extern "C"
+#pragma GCC visibility pop

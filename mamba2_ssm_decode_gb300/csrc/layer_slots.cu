@@ -1,0 +1,298 @@
+// layer_slots.cu -- moves of whole slots inside the pools that the other calls
+// index: copies (a sequence forked, a beam step), clears, and the compaction
+// that closes a pool up, over any number of pools (every layer's state,
+// convolution rows, ring caches and trackers) in one call.
+//
+// Pure data movement: a slot is read once and written once.
+#include "layer_common.cuh"
+
+namespace layer {
+
+constexpr int kMaxPools = SSU_SLOTS_MAX_POOLS;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;
+constexpr int kChunk = kCopyThreads * kCopyUnroll * 16;  // bytes of a slot per work item
+
+struct Pool {
+  uint8_t* data;
+  int64_t bytes, stride;
+};
+
+// Pools by value in the launch's parameters: nothing has to be copied to the
+// device before the kernel, and nothing kept alive after the call.
+struct Pools {
+  Pool pool[kMaxPools];
+  int first[kMaxPools + 1];  // first chunk of each pool within a slot; the total at the end
+  uint32_t wide[(kMaxPools + 31) / 32];  // bit set: 16-byte accesses
+  int n;
+  int64_t slots;
+};
+
+enum class Fill { kCopy, kZero };
+
+template <class T, Fill F>
+__device__ __forceinline__ void move_bytes(uint8_t* dst, const uint8_t* src, int bytes) {
+  const int n = bytes / (int)sizeof(T);
+  T* d = reinterpret_cast<T*>(dst);
+  const T* s = reinterpret_cast<const T*>(src);
+  for (int i0 = threadIdx.x; i0 < n; i0 += kCopyThreads * kCopyUnroll) {
+    T v[kCopyUnroll];
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k) {
+      const int i = i0 + k * kCopyThreads;
+      v[k] = T{};
+      if (F == Fill::kCopy && i < n) v[k] = s[i];
+    }
+#pragma unroll
+    for (int k = 0; k < kCopyUnroll; ++k) {
+      const int i = i0 + k * kCopyThreads;
+      if (i < n) d[i] = v[k];
+    }
+  }
+}
+
+// Chunk `chunk` of a slot: which pool's bytes, from where.
+template <Fill F>
+__device__ __forceinline__ void move_chunk(const Pools& ps, int chunk, int64_t from, int64_t to) {
+  int lo = 0, hi = ps.n - 1;  // the pool with first[lo] <= chunk < first[lo + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (ps.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  const Pool& p = ps.pool[lo];
+  const int64_t at = (int64_t)(chunk - ps.first[lo]) * kChunk;
+  const int64_t left = p.bytes - at;
+  const int bytes = left < kChunk ? (int)left : kChunk;
+  uint8_t* d = p.data + to * p.stride + at;
+  const uint8_t* s = p.data + from * p.stride + at;
+  if (ps.wide[lo >> 5] >> (lo & 31) & 1) move_bytes<uint4, F>(d, s, bytes);
+  else if (((uintptr_t)p.data | (uintptr_t)p.bytes | (uintptr_t)p.stride) % 4 == 0)
+    move_bytes<uint32_t, F>(d, s, bytes);
+  else move_bytes<uint8_t, F>(d, s, bytes);
+}
+
+// grid: x = pairs (several CTAs that copy the same piece of one source run side
+// by side, so a fork reads it from HBM once), y = chunks of a slot.
+template <Fill F>
+__global__ void __launch_bounds__(kCopyThreads)
+    slots_copy_kernel(const __grid_constant__ Pools ps, const void* src, const void* dst,
+                      int idx64, int64_t pad) {
+  const int64_t to = load_int(dst, blockIdx.x, idx64);
+  const int64_t from = F == Fill::kCopy ? load_int(src, blockIdx.x, idx64) : to;
+  if (!slot_ok(to, pad, ps.slots) || !slot_ok(from, pad, ps.slots)) return;
+  if (F == Fill::kCopy && from == to) return;
+  for (int chunk = blockIdx.y; chunk < ps.first[ps.n]; chunk += gridDim.y)
+    move_chunk<F>(ps, chunk, from, to);
+}
+
+// The moves of a compaction, listed on the device: as many CTAs as fit walk
+// them, the pieces of one slot side by side.
+__global__ void __launch_bounds__(kCopyThreads)
+    slots_move_kernel(const __grid_constant__ Pools ps, const int* moves, const int* src,
+                      const int* dst) {
+  const int64_t chunks = ps.first[ps.n];
+  const int64_t items = *moves * chunks;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int64_t m = i / chunks;
+    move_chunk<Fill::kCopy>(ps, (int)(i - m * chunks), src[m], dst[m]);
+  }
+}
+
+// Which slots are live, and where each that lies beyond the first `live` goes:
+// the k-th of them to the k-th free slot below.  One CTA: a bitmap of the
+// slots in shared memory, a running count per 64 slots, then ranks.
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+    slots_plan_kernel(const void* table, void* table_out, int idx64, int64_t n, int64_t pad,
+                      int slots, int* num_live, int* moves, int* src, int* dst) {
+  extern __shared__ unsigned long long bits[];
+  const int words = (slots + 63) / 64;
+  int* before = reinterpret_cast<int*>(bits + words);  // live slots in front of word w
+  __shared__ int warp_sum[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int w = tid; w < words; w += kPlanThreads) bits[w] = 0;
+  __syncthreads();
+  for (int64_t i = tid; i < n; i += kPlanThreads) {
+    const int64_t v = load_int(table, i, idx64);
+    if (slot_ok(v, pad, slots)) atomicOr(&bits[v >> 6], 1ull << (v & 63));
+  }
+  __syncthreads();
+  // exclusive prefix of the words' counts: a run of words for each thread
+  const int run = (words + kPlanThreads - 1) / kPlanThreads;
+  const int w0 = tid * run < words ? tid * run : words;
+  const int w1 = w0 + run < words ? w0 + run : words;
+  int sum = 0;
+  for (int w = w0; w < w1; ++w) sum += __popcll(bits[w]);
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sum[lane] = v;
+  }
+  __syncthreads();
+  const int live = warp_sum[kPlanThreads / 32 - 1];
+  int at = inc - sum + (warp ? warp_sum[warp - 1] : 0);
+  for (int w = w0; w < w1; ++w) {
+    before[w] = at;
+    at += __popcll(bits[w]);
+  }
+  __syncthreads();
+  // live slots in front of slot id (id < slots)
+  auto rank = [&](int id) {
+    return before[id >> 6] + __popcll(bits[id >> 6] & ((1ull << (id & 63)) - 1));
+  };
+  const int kept = live < slots ? rank(live) : live;  // live slots that stay where they are
+  for (int id = tid; id < slots; id += kPlanThreads) {
+    const bool is_live = bits[id >> 6] >> (id & 63) & 1;
+    if (id < live && !is_live) dst[id - rank(id)] = id;
+    if (id >= live && is_live) src[rank(id) - kept] = id;
+  }
+  if (tid == 0) {
+    *moves = live - kept;
+    *num_live = live;
+  }
+  __syncthreads();  // dst is read by other threads than wrote it
+  for (int64_t i = tid; i < n; i += kPlanThreads) {
+    const int64_t v = load_int(table, i, idx64);
+    int64_t to = v;
+    if (slot_ok(v, pad, slots) && v >= live) to = dst[rank((int)v) - kept];
+    if (idx64) static_cast<int64_t*>(table_out)[i] = to;
+    else static_cast<int32_t*>(table_out)[i] = (int32_t)to;
+  }
+}
+
+static ssu_status check_pools(const ssu_pool* pools, int npools, int64_t slots, Pools* ps) {
+  if (npools < 0 || slots < 0)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "npools and slots must be >= 0");
+  if (npools > kMaxPools)
+    return fail(SSU_ERR_UNSUPPORTED, "at most %d pools per call, got %d", kMaxPools, npools);
+  if (slots > (1 << 20)) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
+  if (npools > 0 && !pools) return fail(SSU_ERR_INVALID_ARGUMENT, "pools must not be NULL");
+  *ps = Pools{};
+  int64_t chunks = 0;
+  int n = 0;
+  for (int i = 0; i < npools; ++i) {
+    const ssu_pool& p = pools[i];
+    if (p.slot_bytes < 0 || (slots > 1 && p.slot_stride_bytes < p.slot_bytes))
+      return fail(SSU_ERR_INVALID_ARGUMENT,
+                  "pool %d: a slot of %lld bytes does not fit a stride of %lld", i,
+                  (long long)p.slot_bytes, (long long)p.slot_stride_bytes);
+    if (p.slot_bytes == 0 || slots == 0) continue;
+    if (!p.data) return fail(SSU_ERR_INVALID_ARGUMENT, "pool %d must not be NULL", i);
+    ps->pool[n] = Pool{static_cast<uint8_t*>(p.data), p.slot_bytes, p.slot_stride_bytes};
+    if (aligned(p.data, 16) && p.slot_bytes % 16 == 0 && p.slot_stride_bytes % 16 == 0)
+      ps->wide[n >> 5] |= 1u << (n & 31);
+    ps->first[n] = (int)chunks;
+    chunks += (p.slot_bytes + kChunk - 1) / kChunk;
+    if (chunks > 0x3fffffffLL)
+      return fail(SSU_ERR_UNSUPPORTED, "a slot of all pools must stay below 2^45 bytes");
+    ++n;
+  }
+  ps->first[n] = (int)chunks;
+  ps->n = n;
+  ps->slots = slots;
+  return SSU_OK;
+}
+
+template <Fill F>
+static ssu_status move_slots(const ssu_pool* pools, int npools, int64_t slots, const void* src,
+                             const void* dst, ssu_dtype index_dtype, int64_t pairs, int64_t pad,
+                             cudaStream_t stream) {
+  Pools ps;
+  ssu_status st = check_pools(pools, npools, slots, &ps);
+  if (st != SSU_OK) return st;
+  if (!is_index(index_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "slot ids must be int32 or int64");
+  if (pairs < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "the number of slot ids must be >= 0");
+  if (pairs > 0x7fffffffLL) return fail(SSU_ERR_UNSUPPORTED, "at most 2^31 - 1 slot ids per call");
+  if (pairs > 0 && (!dst || (F == Fill::kCopy && !src)))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "slot ids must not be NULL");
+  if (pairs == 0 || ps.n == 0) return ok();
+  const int chunks = ps.first[ps.n];
+  const dim3 grid((unsigned)pairs, (unsigned)(chunks < 65535 ? chunks : 65535));
+  slots_copy_kernel<F><<<grid, kCopyThreads, 0, stream>>>(ps, src, dst, index_dtype == SSU_I64,
+                                                         pad);
+  return launched(cudaGetLastError());
+}
+
+static int plan_smem(int64_t slots) { return (int)((slots + 63) / 64 * 12); }
+
+}  // namespace layer
+
+#pragma GCC visibility push(default)
+extern "C" {
+
+ssu_status ssu_slots_copy(const ssu_pool* pools, int npools, int64_t slots, const void* src,
+                          const void* dst, ssu_dtype index_dtype, int64_t pairs,
+                          int64_t pad_slot_id, struct CUstream_st* stream) {
+  return layer::move_slots<layer::Fill::kCopy>(pools, npools, slots, src, dst, index_dtype, pairs,
+                                               pad_slot_id, (cudaStream_t)stream);
+}
+
+ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, const void* ids,
+                           ssu_dtype index_dtype, int64_t count, int64_t pad_slot_id,
+                           struct CUstream_st* stream) {
+  return layer::move_slots<layer::Fill::kZero>(pools, npools, slots, nullptr, ids, index_dtype,
+                                               count, pad_slot_id, (cudaStream_t)stream);
+}
+
+int64_t ssu_slots_compact_workspace_bytes(int64_t slots) {
+  // the number of moves, and the two slots of each (at most half the pool moves)
+  return slots < 0 ? -1 : 16 + 2 * 4 * ((slots + 1) / 2);
+}
+
+ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, const void* table,
+                             void* table_out, ssu_dtype index_dtype, int64_t entries,
+                             int64_t pad_slot_id, int32_t* num_live, void* workspace,
+                             int64_t workspace_bytes, struct CUstream_st* stream) {
+  using namespace layer;
+  Pools ps;
+  ssu_status st = check_pools(pools, npools, slots, &ps);
+  if (st != SSU_OK) return st;
+  if (!is_index(index_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "the slot table must be int32 or int64");
+  if (entries < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "entries must be >= 0");
+  if ((entries > 0 && (!table || !table_out)) || !num_live)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "table, table_out and num_live must not be NULL");
+  const int64_t need = ssu_slots_compact_workspace_bytes(slots);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "ssu_slots_compact needs a 16-byte aligned workspace of %lld bytes, got %lld",
+                (long long)need, (long long)workspace_bytes);
+  int* moves = static_cast<int*>(workspace);
+  int* src = moves + 4;
+  int* dst = src + (slots + 1) / 2;
+  const int smem = plan_smem(slots);
+  cudaError_t e = cudaFuncSetAttribute(slots_plan_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return launched(e);
+  slots_plan_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(
+      table, table_out, index_dtype == SSU_I64, entries, pad_slot_id, (int)slots, num_live, moves,
+      src, dst);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ps.n == 0) return launched(e);
+  // at most half the slots move, and no more than the table has entries
+  const int64_t most = slots / 2 < entries ? slots / 2 : entries;
+  const int64_t items = most * ps.first[ps.n];
+  if (items == 0) return ok();
+  const int64_t fit = 8LL * ssu::sm_count();
+  slots_move_kernel<<<(unsigned)(items < fit ? items : fit), kCopyThreads, 0,
+                      (cudaStream_t)stream>>>(ps, moves, src, dst);
+  return launched(cudaGetLastError());
+}
+
+}  // extern "C"
+#pragma GCC visibility pop
