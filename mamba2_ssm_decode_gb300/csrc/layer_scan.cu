@@ -126,6 +126,7 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
     return fail(SSU_ERR_INVALID_ARGUMENT, "operands must be aligned to their element size");
   *p = ScanArgs{};
   p->state = c->state;
+  p->state_dtype = c->state_dtype;
   p->slots = c->state ? c->slots : 0;
   p->C = (int)c->channels;
   p->G = (int)c->ngroups;
@@ -150,6 +151,15 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
               c->C_row_stride * es % 16 == 0 &&
               (c->ngroups == 1 ||
                (c->B_group_stride * es % 16 == 0 && c->C_group_stride * es % 16 == 0));
+  // ... and so do a group's channels, at which a CTA may begin
+  const int64_t per = c->ngroups > 1 ? c->channels / c->ngroups : 0;
+  auto rows_on_16 = [&](const void* ptr, int64_t stride, ssu_dtype d) {
+    return aligned(ptr, 16) && stride * size_of(d) % 16 == 0 && per * size_of(d) % 16 == 0;
+  };
+  p->x_vec = rows_on_16(c->x, c->x_row_stride, c->io_dtype);
+  p->z_vec = rows_on_16(c->z, c->z_row_stride, c->io_dtype);
+  p->dt_vec = rows_on_16(c->dt, c->dt_row_stride, c->dt_dtype);
+  p->o_vec = rows_on_16(c->out, c->out_row_stride, c->out_dtype);
   p->A = c->A;
   p->A_rs = c->A_row_stride;
   p->a_vec = aligned(c->A, 16) && c->A_row_stride % 4 == 0;
@@ -161,13 +171,24 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
   return SSU_OK;
 }
 
-static cudaError_t launch_scan(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
+static cudaError_t launch_step(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
                                int64_t nseqs, cudaStream_t stream) {
   const int N = (int)c->dstate;
   switch (c->io_dtype) {
-    case SSU_F32: return launch_scan_f32(c->state_dtype, N, p, a, nseqs, stream);
-    case SSU_BF16: return launch_scan_bf16(c->state_dtype, N, p, a, nseqs, stream);
-    case SSU_F16: return launch_scan_f16(c->state_dtype, N, p, a, nseqs, stream);
+    case SSU_F32: return launch_scan_f32(N, p, a, nseqs, stream);
+    case SSU_BF16: return launch_scan_bf16(N, p, a, nseqs, stream);
+    case SSU_F16: return launch_scan_f16(N, p, a, nseqs, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+static cudaError_t launch_prompt(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
+                                 int64_t nseqs, cudaStream_t stream) {
+  const int N = (int)c->dstate;
+  switch (c->io_dtype) {
+    case SSU_F32: return launch_prompt_f32(N, p, a, nseqs, stream);
+    case SSU_BF16: return launch_prompt_bf16(N, p, a, nseqs, stream);
+    case SSU_F16: return launch_prompt_f16(N, p, a, nseqs, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -191,7 +212,7 @@ ssu_status ssu_scan_update(const ssu_scan_params* c, int64_t nseqs, int64_t rows
                       meta_dtype, src, dst, index_dtype, &a);
   if (st != SSU_OK) return st;
   if (nseqs == 0 || rows == 0) return ok();
-  return launched(launch_scan(c, p, a, nseqs, (cudaStream_t)stream));
+  return launched(launch_step(c, p, a, nseqs, (cudaStream_t)stream));
 }
 
 ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t rows,
@@ -212,7 +233,7 @@ ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t 
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
   p.final_only = 1;
-  return launched(launch_scan(c, p, a, nseqs, (cudaStream_t)stream));
+  return launched(launch_prompt(c, p, a, nseqs, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -13,6 +13,7 @@ namespace layer {
 
 struct ScanArgs {
   void* state;
+  int state_dtype;  // ssu_dtype
   int64_t slots;
   int C, G;
   ssu::FastDiv per;  // channels per group
@@ -26,6 +27,7 @@ struct ScanArgs {
   const void* dt;
   int64_t dt_rs;
   int dt_f32;
+  int x_vec, z_vec, dt_vec, o_vec;  // every row starts on a 16-byte boundary
   const void* B;
   int64_t B_rs, B_gs;
   const void* Cm;
@@ -217,9 +219,9 @@ cudaError_t launch_scan_n(int N, const ScanArgs& p, const VarlenArgs& a, int64_t
 }
 
 template <class IT>
-cudaError_t launch_scan_io(ssu_dtype state, int N, const ScanArgs& p, const VarlenArgs& a,
-                           int64_t nseqs, cudaStream_t stream) {
-  switch (state) {
+cudaError_t launch_scan_io(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                           cudaStream_t stream) {
+  switch (p.state_dtype) {
     case SSU_F32: return launch_scan_n<float, IT>(N, p, a, nseqs, stream);
     case SSU_BF16: return launch_scan_n<__nv_bfloat16, IT>(N, p, a, nseqs, stream);
     case SSU_F16: return launch_scan_n<__half, IT>(N, p, a, nseqs, stream);
@@ -228,11 +230,17 @@ cudaError_t launch_scan_io(ssu_dtype state, int N, const ScanArgs& p, const Varl
 }
 
 // one translation unit for each element type of the rows
-cudaError_t launch_scan_f32(ssu_dtype state, int N, const ScanArgs& p, const VarlenArgs& a,
-                            int64_t nseqs, cudaStream_t stream);
-cudaError_t launch_scan_bf16(ssu_dtype state, int N, const ScanArgs& p, const VarlenArgs& a,
-                             int64_t nseqs, cudaStream_t stream);
-cudaError_t launch_scan_f16(ssu_dtype state, int N, const ScanArgs& p, const VarlenArgs& a,
-                            int64_t nseqs, cudaStream_t stream);
+cudaError_t launch_scan_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
+cudaError_t launch_prompt_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
+cudaError_t launch_scan_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
+cudaError_t launch_prompt_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
+cudaError_t launch_scan_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
+cudaError_t launch_prompt_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                         cudaStream_t stream);
 
 }  // namespace layer
