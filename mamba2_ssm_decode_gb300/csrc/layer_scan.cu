@@ -156,10 +156,10 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
   auto rows_on_16 = [&](const void* ptr, int64_t stride, ssu_dtype d) {
     return aligned(ptr, 16) && stride * size_of(d) % 16 == 0 && per * size_of(d) % 16 == 0;
   };
-  p->x_vec = rows_on_16(c->x, c->x_row_stride, c->io_dtype);
-  p->z_vec = rows_on_16(c->z, c->z_row_stride, c->io_dtype);
-  p->dt_vec = rows_on_16(c->dt, c->dt_row_stride, c->dt_dtype);
-  p->o_vec = rows_on_16(c->out, c->out_row_stride, c->out_dtype);
+  p->rows_vec = rows_on_16(c->x, c->x_row_stride, c->io_dtype) &&
+                rows_on_16(c->dt, c->dt_row_stride, c->dt_dtype) &&
+                rows_on_16(c->out, c->out_row_stride, c->out_dtype) &&
+                (!c->z || rows_on_16(c->z, c->z_row_stride, c->io_dtype)) && p->bc_vec;
   p->A = c->A;
   p->A_rs = c->A_row_stride;
   p->a_vec = aligned(c->A, 16) && c->A_row_stride % 4 == 0;

@@ -27,7 +27,7 @@ struct ScanArgs {
   const void* dt;
   int64_t dt_rs;
   int dt_f32;
-  int x_vec, z_vec, dt_vec, o_vec;  // every row starts on a 16-byte boundary
+  int rows_vec;  // every row of x, z, dt, out, B and C (and its groups) starts on a 16-byte boundary
   const void* B;
   int64_t B_rs, B_gs;
   const void* Cm;

@@ -19,27 +19,59 @@ namespace layer {
 
 constexpr int kPromptThreads = 128;
 
-template <int N>
+// R channels of NPT state columns per thread.
+template <int N, int R, int NPT>
 struct PromptTile {
-  static constexpr int NPT = N == 16 ? 4 : 8;           // state columns per thread
-  static constexpr int LPC = N / NPT;                   // lanes per channel
-  static constexpr int CH = kPromptThreads / LPC;       // channels per CTA
-  static constexpr int TT = N <= 128 ? 32 : 16;         // rows per tile
-  static constexpr int TPR = kPromptThreads / TT;       // staging threads per row
-  static constexpr int SV = CH >= TPR ? CH / TPR : 1;   // channels per staging thread
-  static constexpr int BV = N / TPR;                    // B (and C) columns per staging thread
-  static constexpr int TG = LPC < 8 ? LPC : 8;          // rows whose sums are reduced together
-  static constexpr int YS = CH + 32 / TG;               // row stride of the sums
+  static constexpr int LPC = N / NPT;                        // lanes per channel
+  static constexpr int LG = kPromptThreads / LPC;            // groups of such lanes
+  static constexpr int CH = R * LG;                          // channels per CTA
+  static constexpr int WANT = 8 * N / (R * NPT);             // rows for 8 values a staging thread
+  static constexpr int TT = WANT > 32 ? (N > 128 ? 16 : 32) : WANT;  // rows per tile
+  static constexpr int TPR = kPromptThreads / TT;            // staging threads per row
+  static constexpr int SV = CH >= TPR ? CH / TPR : 1;        // channels per staging thread
+  static constexpr int BV = N / TPR;                         // B (and C) columns per staging thread
+  static constexpr int TG = LPC < 8 ? LPC : 8;               // rows whose sums are reduced together
+  static constexpr int YS = CH + 32 / TG;                    // row stride of the sums
+  static constexpr int CPW = 32 / LPC;                       // lane groups per warp
 };
 
-template <int N>
+template <class K, int N>
 struct alignas(16) PromptSmem {
-  using K = PromptTile<N>;
   float d[K::TT][K::CH];    // dt'
   float dx[K::TT][K::CH];   // dt' x
   float B[K::TT][N];
   float C[K::TT][N];
   float y[K::TT][K::YS];    // sums over dstate
+  float D[K::CH];
+  float bias[K::CH];
+};
+
+// Sums of G rows over the LPC lanes that share a channel (lanes STRIDE apart,
+// the lane's index among them q): at each level a lane keeps half of its rows
+// and sends the others, so that it ends up with row `base` alone; levels left
+// over once it has one row are plain sums, equal in the lanes that differ in
+// the bits of `plain`.
+template <int G, int OFF, int STRIDE>
+struct GroupSum {
+  __device__ static __forceinline__ void run(float* v, int q, int& base, int& plain) {
+    if constexpr (OFF > 0) {
+      if constexpr (G > 1) {
+        const bool upper = (q & OFF) != 0;
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) {
+          const float send = upper ? v[i] : v[G / 2 + i];
+          const float keep = upper ? v[G / 2 + i] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, OFF * STRIDE);
+        }
+        if (upper) base += G / 2;
+        GroupSum<G / 2, OFF / 2, STRIDE>::run(v, q, base, plain);
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], OFF * STRIDE);
+        plain |= OFF;
+        GroupSum<1, OFF / 2, STRIDE>::run(v, q, base, plain);
+      }
+    }
+  }
 };
 
 // Four state columns from or to a slot, in the state's type.
@@ -66,217 +98,478 @@ __device__ __forceinline__ void store_state4(const ScanArgs& p, int64_t at, floa
   else store_as4<__half>(p.state, at, a, b);
 }
 
-// V elements as stored: one access where `vec`, else those in [0, n) one by one, zeros beyond.
+// V elements as stored, in 32-bit words.
 template <class T, int V>
-__device__ __forceinline__ Pack<T, V> fetch(const T* p, bool vec, int n) {
-  if (vec && n >= V) return load_pack<T, V>(p);
-  Pack<T, V> r = zero_pack<T, V>();
+struct Words {
+  static constexpr int BYTES = V * (int)sizeof(T), NW = (BYTES + 3) / 4;
+  uint32_t w[NW];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else return __half2float(__ushort_as_half((unsigned short)(w[i >> 1] >> (i & 1 ? 16 : 0))));
+  }
+  __device__ __forceinline__ void load(const T* p) {  // from a multiple of 16 bytes, or of BYTES
+    if constexpr (BYTES % 16 == 0) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < n) r.v[i] = p[i];
-  return r;
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void load_some(const T* p, int n) {  // elements [0, n), zeros beyond
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (i & 1 ? 16 : 0);
+      }
+  }
+};
+
+// V floats of shared memory
+template <int V>
+__device__ __forceinline__ void shared_floats(const float* p, float* f) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(p)[i];
+      f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = p[i];
+  }
 }
 
-template <class IT, class DT, int N>
-__global__ void __launch_bounds__(kPromptThreads)
-    scan_prompt_kernel(const ScanArgs p, const VarlenArgs a, int64_t nseqs) {
-  using K = PromptTile<N>;
-  constexpr int NPT = K::NPT, LPC = K::LPC, TT = K::TT, SV = K::SV, BV = K::BV, TG = K::TG;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  PromptSmem<N>& sm = *reinterpret_cast<PromptSmem<N>*>(smem_raw);
-
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int per = p.C / p.G, tiles = (per + K::CH - 1) / K::CH;
-  const int g = blockIdx.x / tiles;                       // the CTA's channels are of one group
-  const int c0 = g * per + (blockIdx.x - g * tiles) * K::CH;
-  const int c_end = (g + 1) * per;
-
-  // the chain's part: channel cc, columns n(j, i) = (j LPC + q) 4 + i
-  const int q = lane % LPC;
-  const int ch = tid / LPC;
-  const int cc = c0 + ch;
-  float2 A2[NPT / 2], h[NPT / 2];
+template <int V>
+__device__ __forceinline__ void to_shared(float* p, const float* f) {
+  if constexpr (V % 4 == 0) {
 #pragma unroll
-  for (int j = 0; j < NPT / 4; ++j) {
-    float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (cc < c_end) load_floats<float, 4>(p.A + cc * p.A_rs + (j * LPC + q) * 4, p.a_vec, f);
-    A2[2 * j] = make_float2(f[0] * kLog2e, f[1] * kLog2e);
-    A2[2 * j + 1] = make_float2(f[2] * kLog2e, f[3] * kLog2e);
+    for (int i = 0; i < V / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] =
+          make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = f[i];
   }
+}
 
-  // the staging part: row tr of the tile, channels sc .. sc + SV
+// FAST: every row of x, z, dt, B, C and out can be moved in whole vectors.  A
+// load is then one instruction that nothing waits for until the next tile is
+// staged; a choice between the two kinds of load would be waited for at once.
+template <class IT, class DT, int N, int R, int NPT, bool FAST, bool OUT>
+struct PromptRows {
+  using K = PromptTile<N, R, NPT>;
+  static constexpr int SV = K::SV, BV = K::BV;
+  Words<IT, SV> x, z;
+  Words<DT, SV> dt;
+  Words<IT, BV> B, C;
+  const IT *xp, *zp, *Bp, *Cp;
+  const DT* dp;
+  int sn;  // the thread's channels
+
+  // row r of [r0, r_end)
+  __device__ __forceinline__ void load(const ScanArgs& p, int64_t r, int64_t r_end) {
+    if constexpr (FAST) {
+      if (r >= r_end) r = r_end - 1;  // staged as a step that changes nothing
+      x.load(xp + r * p.x_rs);
+      if (OUT && p.z) z.load(zp + r * p.z_rs);
+      dt.load(dp + r * p.dt_rs);
+      B.load(Bp + r * p.B_rs);
+      if (OUT) C.load(Cp + r * p.C_rs);
+    } else {
+      const bool in = r < r_end;
+      x.load_some(xp + r * p.x_rs, in ? sn : 0);
+      if (OUT && p.z) z.load_some(zp + r * p.z_rs, in ? sn : 0);
+      dt.load_some(dp + r * p.dt_rs, in ? sn : 0);
+      B.load_some(Bp + r * p.B_rs, in ? BV : 0);
+      if (OUT) C.load_some(Cp + r * p.C_rs, in ? BV : 0);
+    }
+  }
+};
+
+template <class T, int SV, bool FAST>
+__device__ __forceinline__ void store_row(T* o, const float* y, int n) {
+  Pack<T, SV> v;
+#pragma unroll
+  for (int i = 0; i < SV; ++i) v.v[i] = from_f<T>(y[i]);
+  if constexpr (FAST) {
+    store_pack<T, SV>(o, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < SV; ++i)
+      if (i < n) o[i] = v.v[i];
+  }
+}
+
+// The chain over rows [r0, r_end), its state in h.  OUT false: no sums and no
+// outputs, only the state and dsum, the sum of dt' over the rows.
+template <class IT, class DT, int N, int R, int NPT, bool FAST, bool OUT>
+__device__ __forceinline__ void scan_rows(const ScanArgs& p,
+                                          PromptSmem<PromptTile<N, R, NPT>, N>& sm, int g, int c0,
+                                          int cn, int64_t r0, int64_t r_end,
+                                          const float2 (&A2)[R][NPT / 2],
+                                          float2 (&h)[R][NPT / 2], float (&dsum)[R]) {
+  using K = PromptTile<N, R, NPT>;
+  constexpr int LPC = K::LPC, TT = K::TT, SV = K::SV, BV = K::BV, TG = K::TG;
+  constexpr int UG = TT % (2 * TG) == 0 && TG < 8 ? 2 : 1;  // reduction groups per pass
+  // neighbouring lanes take neighbouring channels and the same columns: a load
+  // of B or C then asks for the same 16 bytes in runs of lanes, which shared
+  // memory serves in 1.7 cycles (runs of 8) where it takes 4 when every lane's
+  // neighbour asks for other ones
+  const int tid = threadIdx.x;
+  const int q = (tid & 31) / K::CPW, ch = tid / 32 * K::CPW + (tid & 31) % K::CPW;
+
+  // staging: row tr of the tile, channels s0 .. s0 + SV, columns b0 .. b0 + BV
   const int tr = tid / K::TPR, tp = tid % K::TPR;
-  const int sc = c0 + tp * SV;
-  const int sn = tp * SV < K::CH ? (c_end - sc < SV ? c_end - sc : SV) : 0;
-  const int b0 = tp * BV;
-  float Dv[SV], bias[SV];
+  const int s0 = tp * SV, b0 = tp * BV;
+  PromptRows<IT, DT, N, R, NPT, FAST, OUT> rows;
+  rows.sn = s0 < K::CH ? (cn - s0 < SV ? cn - s0 : SV) : 0;
+  const int cs = c0 + (rows.sn > 0 ? s0 : 0);  // threads without channels read the CTA's first
+  rows.xp = static_cast<const IT*>(p.x) + cs;
+  rows.zp = static_cast<const IT*>(p.z) + cs;
+  rows.dp = static_cast<const DT*>(p.dt) + cs;
+  rows.Bp = static_cast<const IT*>(p.B) + g * p.B_gs + b0;
+  rows.Cp = static_cast<const IT*>(p.Cm) + g * p.C_gs + b0;
+  rows.load(p, r0 + tr, r_end);
+
+  for (int64_t rt = r0; rt < r_end; rt += TT) {
+    const int n = r_end - rt < TT ? (int)(r_end - rt) : TT;
+    const bool in = tr < n;
+    const Words<IT, SV> xk = rows.x, zk = rows.z;
+    // rows beyond the sequence get dt' = 0 and zeros: a step that changes nothing
+    if (s0 < K::CH) {
+      float bias[SV], d[SV], dx[SV];
+      shared_floats<SV>(&sm.bias[s0], bias);
 #pragma unroll
-  for (int i = 0; i < SV; ++i) {
-    Dv[i] = p.D && i < sn ? p.D[sc + i] : 0.0f;
-    bias[i] = p.bias && i < sn ? p.bias[sc + i] : 0.0f;
+      for (int i = 0; i < SV; i += 2) {
+        const int k = i + 1 < SV ? i + 1 : i;
+        float2 v = make_float2(rows.dt.at(i), rows.dt.at(k));
+        const float2 bi = make_float2(bias[i], bias[k]);
+        v = p.softplus ? softplus_sum2(v, bi) : __fadd2_rn(v, bi);
+        float2 vx = __fmul2_rn(v, make_float2(xk.at(i), xk.at(k)));
+        if (!in) v = vx = make_float2(0.0f, 0.0f);
+        d[i] = v.x, d[k] = k > i ? v.y : v.x;
+        dx[i] = vx.x, dx[k] = k > i ? vx.y : vx.x;
+      }
+      to_shared<SV>(&sm.d[tr][s0], d);
+      to_shared<SV>(&sm.dx[tr][s0], dx);
+    }
+    {
+      float f[BV];
+#pragma unroll
+      for (int i = 0; i < BV; ++i) f[i] = in ? rows.B.at(i) : 0.0f;
+      to_shared<BV>(&sm.B[tr][b0], f);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int i = 0; i < BV; ++i) f[i] = in ? rows.C.at(i) : 0.0f;
+        to_shared<BV>(&sm.C[tr][b0], f);
+      }
+    }
+    __syncthreads();
+    if (rt + TT < r_end) rows.load(p, rt + TT + tr, r_end);
+
+    for (int t = 0; t < n; t += TG * UG) {
+#pragma unroll
+      for (int u = 0; u < UG; ++u) {
+        float acc[R][TG];
+#pragma unroll
+        for (int k = 0; k < TG; ++k) {
+          const int row = t + u * TG + k;
+          float2 sum[R];
+          float d[R], dx[R];
+#pragma unroll
+          for (int m = 0; m < R; ++m) {
+            d[m] = sm.d[row][ch + m * K::LG];
+            dx[m] = sm.dx[row][ch + m * K::LG];
+          }
+#pragma unroll
+          for (int j = 0; j < NPT / 4; ++j) {
+            const float4 b = *reinterpret_cast<const float4*>(&sm.B[row][(j * LPC + q) * 4]);
+            float4 c;
+            if constexpr (OUT) c = *reinterpret_cast<const float4*>(&sm.C[row][(j * LPC + q) * 4]);
+#pragma unroll
+            for (int m = 0; m < R; ++m) {
+              const float2 d2 = make_float2(d[m], d[m]), dx2 = make_float2(dx[m], dx[m]);
+              const float2 e0 = __fmul2_rn(A2[m][2 * j], d2), e1 = __fmul2_rn(A2[m][2 * j + 1], d2);
+              h[m][2 * j] = __ffma2_rn(h[m][2 * j], make_float2(ex2(e0.x), ex2(e0.y)),
+                                       __fmul2_rn(dx2, make_float2(b.x, b.y)));
+              h[m][2 * j + 1] = __ffma2_rn(h[m][2 * j + 1], make_float2(ex2(e1.x), ex2(e1.y)),
+                                           __fmul2_rn(dx2, make_float2(b.z, b.w)));
+              if constexpr (!OUT) continue;
+              sum[m] = j == 0 ? __fmul2_rn(h[m][0], make_float2(c.x, c.y))
+                              : __ffma2_rn(h[m][2 * j], make_float2(c.x, c.y), sum[m]);
+              sum[m] = __ffma2_rn(h[m][2 * j + 1], make_float2(c.z, c.w), sum[m]);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < R; ++m) {
+            if constexpr (OUT) acc[m][k] = sum[m].x + sum[m].y;
+            else dsum[m] += d[m];
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < R && OUT; ++m) {
+          int base = 0, plain = 0;
+          GroupSum<TG, LPC / 2, K::CPW>::run(acc[m], q, base, plain);
+          if ((q & plain) == 0) sm.y[t + u * TG + base][ch + m * K::LG] = acc[m][0];
+        }
+      }
+    }
+    __syncthreads();
+
+    if (OUT && in && rows.sn > 0) {
+      float y[SV], D[SV];
+      shared_floats<SV>(&sm.y[tr][s0], y);
+      shared_floats<SV>(&sm.D[s0], D);
+#pragma unroll
+      for (int i = 0; i < SV; ++i) y[i] = fmaf(D[i], xk.at(i), y[i]);
+      if (p.z) {
+#pragma unroll
+        for (int i = 0; i < SV; ++i) y[i] *= silu(zk.at(i));
+      }
+      const int64_t o = (rt + tr) * p.o_rs + c0 + s0;
+      if (p.out_f32) store_row<float, SV, FAST>(static_cast<float*>(p.out) + o, y, rows.sn);
+      else store_row<IT, SV, FAST>(static_cast<IT*>(p.out) + o, y, rows.sn);
+    }
   }
-  const IT* xp = static_cast<const IT*>(p.x) + sc;
-  const IT* zp = static_cast<const IT*>(p.z) + sc;
-  const DT* dp = static_cast<const DT*>(p.dt) + sc;
-  const IT* Bp = static_cast<const IT*>(p.B) + g * p.B_gs + b0;
-  const IT* Cp = static_cast<const IT*>(p.Cm) + g * p.C_gs + b0;
+}
+
+// A long sequence of few channels leaves most of the GPU idle, so its rows are
+// split over the K CTAs of a cluster.  Every CTA but the first carries zeros
+// through its piece (no outputs), which with the sum of its dt' says what the
+// piece does to any state that enters:
+//     h_leave = exp(A sum dt') h_enter + h_from_zero;
+// the first meanwhile finishes its piece from the true state.  Then each CTA
+// folds the pieces in front of its own, read from its neighbours' shared
+// memory, and runs its piece for the outputs.  The exponentials are paid twice
+// over (K - 1) / K of the rows.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// float at the address `p` of this CTA's shared memory, in the CTA of rank `rank`
+__device__ __forceinline__ float peer_float(const float* p, int rank) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(p);
+  uint32_t there;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
+  return v;
+}
+
+// What a CTA's piece does, for the CTAs behind it.
+template <int R, int NPT>
+struct PromptPiece {
+  float h[R * NPT][kPromptThreads];
+  float dsum[R][kPromptThreads];
+};
+
+// First row of piece k of K, in tiles: the first piece is shorter by the work
+// that the others do twice (a pass without outputs costs about 0.7 of one with).
+__device__ __forceinline__ int64_t piece_start(int64_t tiles, int k, int K) {
+  if (k == 0) return 0;
+  if (k == K) return tiles;
+  return (int64_t)(((k - 1) + 0.7f) / ((K - 1) + 0.7f) * (float)tiles);
+}
+
+template <class IT, class DT, int N, int R, int NPT, bool SPLIT>
+__global__ void __launch_bounds__(kPromptThreads, 4)
+    scan_prompt_kernel(const ScanArgs p, const VarlenArgs a, int64_t nseqs, int K_) {
+  using K = PromptTile<N, R, NPT>;
+  constexpr int LPC = K::LPC, TT = K::TT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  PromptSmem<K, N>& sm = *reinterpret_cast<PromptSmem<K, N>*>(smem_raw);
+  PromptPiece<R, NPT>& piece = *reinterpret_cast<PromptPiece<R, NPT>*>(smem_raw + sizeof sm);
+
+  const int tid = threadIdx.x;
+  const int pieces = SPLIT ? K_ : 1, rank = SPLIT ? (int)(blockIdx.x % pieces) : 0;
+  const int tile = blockIdx.x / pieces;
+  const int per = p.C / p.G, tiles = (per + K::CH - 1) / K::CH;
+  const int g = tile / tiles;                             // the CTA's channels are of one group
+  const int c0 = g * per + (tile - g * tiles) * K::CH;
+  const int cn = (g + 1) * per - c0;                      // channels from c0 to the group's end
+  const int q = (tid & 31) / K::CPW;                      // which of a channel's lanes
+  const int ch = tid / 32 * K::CPW + (tid & 31) % K::CPW;  // channels c0 + ch + k LG, k < R
+  float2 A2[R][NPT / 2];                                  // columns (j LPC + q) 4 + i; A log2 e
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int c = ch + k * K::LG;
+#pragma unroll
+    for (int j = 0; j < NPT / 4; ++j) {
+      float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (c < cn)
+        load_floats<float, 4>(p.A + (int64_t)(c0 + c) * p.A_rs + (j * LPC + q) * 4, p.a_vec, f);
+      A2[k][2 * j] = make_float2(f[0] * kLog2e, f[1] * kLog2e);
+      A2[k][2 * j + 1] = make_float2(f[2] * kLog2e, f[3] * kLog2e);
+    }
+  }
+  for (int c = tid; c < K::CH; c += kPromptThreads) {
+    sm.D[c] = p.D && c < cn ? p.D[c0 + c] : 0.0f;
+    sm.bias[c] = p.bias && c < cn ? p.bias[c0 + c] : 0.0f;
+  }
+  __syncthreads();
+  const bool fast = p.rows_vec && cn % K::SV == 0;
 
   for (int64_t s = blockIdx.y; s < nseqs; s += gridDim.y) {
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
     const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
-#pragma unroll
-    for (int j = 0; j < NPT / 4; ++j) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (from && cc < c_end)
-        v = load_state4(p, (it.src * p.C + cc) * N + (j * LPC + q) * 4);
-      h[2 * j] = make_float2(v.x, v.y);
-      h[2 * j + 1] = make_float2(v.z, v.w);
+    // a sequence of few tiles is left whole to the cluster's first CTA
+    const int64_t row_tiles = (it.len + TT - 1) / TT;
+    const bool split = SPLIT && row_tiles >= 4 * pieces;
+    if (SPLIT && !split && rank > 0) continue;
+    int64_t r0 = it.r0, r_end = it.r0 + it.len;
+    if (split) {
+      if (rank < pieces - 1) r_end = r0 + piece_start(row_tiles, rank + 1, pieces) * TT;
+      r0 += piece_start(row_tiles, rank, pieces) * TT;
     }
-
-    Pack<IT, SV> x, z;
-    Pack<DT, SV> dt;
-    Pack<IT, BV> B, C;
-    const int64_t r_end = it.r0 + it.len;
-    auto load = [&](int64_t r) {
-      const bool in = r < r_end;
-      x = fetch<IT, SV>(xp + r * p.x_rs, p.x_vec, in ? sn : 0);
-      if (p.z) z = fetch<IT, SV>(zp + r * p.z_rs, p.z_vec, in ? sn : 0);
-      dt = fetch<DT, SV>(dp + r * p.dt_rs, p.dt_vec, in ? sn : 0);
-      B = fetch<IT, BV>(Bp + r * p.B_rs, p.bc_vec, in ? BV : 0);
-      C = fetch<IT, BV>(Cp + r * p.C_rs, p.bc_vec, in ? BV : 0);
+    float2 h[R][NPT / 2];
+    float dsum[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      dsum[k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NPT / 4; ++j) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int c = ch + k * K::LG;
+        if (from && c < cn && rank == 0)
+          v = load_state4(p, (it.src * p.C + c0 + c) * N + (j * LPC + q) * 4);
+        h[k][2 * j] = make_float2(v.x, v.y);
+        h[k][2 * j + 1] = make_float2(v.z, v.w);
+      }
+    }
+    auto rows = [&](auto out) {
+      constexpr bool OUT = decltype(out)::value;
+      if (fast) scan_rows<IT, DT, N, R, NPT, true, OUT>(p, sm, g, c0, cn, r0, r_end, A2, h, dsum);
+      else scan_rows<IT, DT, N, R, NPT, false, OUT>(p, sm, g, c0, cn, r0, r_end, A2, h, dsum);
     };
-    load(it.r0 + tr);
-
-    for (int64_t t0 = 0; t0 < it.len; t0 += TT) {
-      const int64_t r = it.r0 + t0 + tr;
-      const int n = it.len - t0 < TT ? (int)(it.len - t0) : TT;
-      // stage: rows beyond the sequence get dt' = 0 and zeros, a step that changes nothing
-      const bool in = tr < n;
-      Pack<IT, SV> xk = x, zk = z;
-      if (tp * SV < K::CH) {
+    if constexpr (SPLIT) {
+      if (split) {
+        if (rank > 0 && rank < pieces - 1) rows(std::false_type{});
+        if (rank == 0) rows(std::true_type{});
+        if (rank < pieces - 1) {
 #pragma unroll
-        for (int i = 0; i < SV; i += 2) {
-          const int k = i + 1 < SV ? i + 1 : i;
-          float2 d = make_float2(to_f(dt.v[i]), to_f(dt.v[k]));
-          const float2 bi = make_float2(bias[i], bias[k]);
-          d = p.softplus ? softplus_sum2(d, bi) : __fadd2_rn(d, bi);
-          if (!in) d = make_float2(0.0f, 0.0f);
-          const float2 dx = __fmul2_rn(d, make_float2(to_f(x.v[i]), to_f(x.v[k])));
-          sm.d[tr][tp * SV + i] = d.x;
-          sm.dx[tr][tp * SV + i] = dx.x;
-          if (k > i) {
-            sm.d[tr][tp * SV + k] = d.y;
-            sm.dx[tr][tp * SV + k] = dx.y;
+          for (int k = 0; k < R; ++k) {
+            piece.dsum[k][tid] = dsum[k];
+#pragma unroll
+            for (int j = 0; j < NPT / 2; ++j) {
+              piece.h[k * NPT + 2 * j][tid] = h[k][j].x;
+              piece.h[k * NPT + 2 * j + 1][tid] = h[k][j].y;
+            }
           }
         }
-      }
+        cluster_arrive();
+        cluster_wait();
+        if (rank > 0) {
 #pragma unroll
-      for (int i = 0; i < BV; ++i) {
-        sm.B[tr][b0 + i] = to_f(B.v[i]);
-        sm.C[tr][b0 + i] = to_f(C.v[i]);
-      }
-      __syncthreads();
-      if (t0 + TT < it.len) load(r + TT);
-
-      for (int t = 0; t < n; t += TG) {
-        float acc[TG];
+          for (int k = 0; k < R; ++k)
 #pragma unroll
-        for (int k = 0; k < TG; ++k) {
-          const float d = sm.d[t + k][ch], dx = sm.dx[t + k][ch];
-          const float2 d2 = make_float2(d, d), dx2 = make_float2(dx, dx);
-          float2 sum = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < NPT / 2; ++j)
+              h[k][j] = make_float2(peer_float(&piece.h[k * NPT + 2 * j][tid], 0),
+                                    peer_float(&piece.h[k * NPT + 2 * j + 1][tid], 0));
+          for (int b = 1; b < rank; ++b) {
 #pragma unroll
-          for (int j = 0; j < NPT / 4; ++j) {
-            const float4 b = *reinterpret_cast<const float4*>(&sm.B[t + k][(j * LPC + q) * 4]);
-            const float4 c = *reinterpret_cast<const float4*>(&sm.C[t + k][(j * LPC + q) * 4]);
-            const float2 e0 = __fmul2_rn(A2[2 * j], d2), e1 = __fmul2_rn(A2[2 * j + 1], d2);
-            h[2 * j] = __ffma2_rn(h[2 * j], make_float2(ex2(e0.x), ex2(e0.y)),
-                                  __fmul2_rn(dx2, make_float2(b.x, b.y)));
-            h[2 * j + 1] = __ffma2_rn(h[2 * j + 1], make_float2(ex2(e1.x), ex2(e1.y)),
-                                      __fmul2_rn(dx2, make_float2(b.z, b.w)));
-            sum = __ffma2_rn(h[2 * j], make_float2(c.x, c.y), sum);
-            sum = __ffma2_rn(h[2 * j + 1], make_float2(c.z, c.w), sum);
-          }
-          acc[k] = sum.x + sum.y;
-        }
-        int base = 0, plain = 0;
-        ssu::RowScatter<TG, LPC / 2>::run(acc, q, base, plain);
-        if ((q & plain) == 0) sm.y[t + base][ch] = acc[0];
-      }
-      __syncthreads();
-
-      if (in && sn > 0) {
-        float y[SV];
+            for (int k = 0; k < R; ++k) {
+              const float d = peer_float(&piece.dsum[k][tid], b);
 #pragma unroll
-        for (int i = 0; i < SV; ++i) {
-          y[i] = fmaf(Dv[i], to_f(xk.v[i]), sm.y[tr][tp * SV + i]);
-          if (p.z) y[i] *= silu(to_f(zk.v[i]));
-        }
-        if (p.out_f32) {
-          float* o = static_cast<float*>(p.out) + r * p.o_rs + sc;
-          if (p.o_vec && sn == SV) {
-            Pack<float, SV> v;
-#pragma unroll
-            for (int i = 0; i < SV; ++i) v.v[i] = y[i];
-            store_pack<float, SV>(o, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < SV; ++i)
-              if (i < sn) o[i] = y[i];
-          }
-        } else {
-          IT* o = static_cast<IT*>(p.out) + r * p.o_rs + sc;
-          Pack<IT, SV> v;
-#pragma unroll
-          for (int i = 0; i < SV; ++i) v.v[i] = from_f<IT>(y[i]);
-          if (p.o_vec && sn == SV) {
-            store_pack<IT, SV>(o, v);
-          } else {
-#pragma unroll
-            for (int i = 0; i < SV; ++i)
-              if (i < sn) o[i] = v.v[i];
+              for (int j = 0; j < NPT / 2; ++j) {
+                h[k][j].x = fmaf(h[k][j].x, ex2(A2[k][j].x * d),
+                                 peer_float(&piece.h[k * NPT + 2 * j][tid], b));
+                h[k][j].y = fmaf(h[k][j].y, ex2(A2[k][j].y * d),
+                                 peer_float(&piece.h[k * NPT + 2 * j + 1][tid], b));
+              }
+            }
           }
         }
+        cluster_arrive();  // the neighbours' pieces have been read
+        if (rank > 0) rows(std::true_type{});
+        cluster_wait();    // ... by all: this CTA's may be written again, and the CTA may end
+      } else {
+        rows(std::true_type{});
       }
+    } else {
+      rows(std::true_type{});
     }
-
     int64_t slot;
-    if (it.read_ok && !p.disable && cc < c_end && write_slot(a, s, 0, p.pad, p.slots, &slot)) {
+    if ((!split || rank == pieces - 1) && it.read_ok && !p.disable &&
+        write_slot(a, s, 0, p.pad, p.slots, &slot)) {
 #pragma unroll
-      for (int j = 0; j < NPT / 4; ++j)
-        store_state4(p, (slot * p.C + cc) * N + (j * LPC + q) * 4, h[2 * j], h[2 * j + 1]);
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int j = 0; j < NPT / 4; ++j) {
+          const int c = ch + k * K::LG;
+          if (c < cn)
+            store_state4(p, (slot * p.C + c0 + c) * N + (j * LPC + q) * 4, h[k][2 * j],
+                         h[k][2 * j + 1]);
+        }
     }
   }
 }
 
-template <class IT, class DT, int N>
-cudaError_t launch_scan_prompt(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
-                               cudaStream_t stream) {
-  using K = PromptTile<N>;
-  const int per = p.C / p.G;
-  const int64_t gx = (int64_t)p.G * ((per + K::CH - 1) / K::CH);
-  const int64_t gy = nseqs < 65535 ? nseqs : 65535;
-  auto kern = scan_prompt_kernel<IT, DT, N>;
-  const int smem = (int)sizeof(PromptSmem<N>);
+template <class IT, class DT, int N, int R, int NPT, bool SPLIT>
+cudaError_t launch_prompt_as(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs, int64_t tiles,
+                             int pieces, cudaStream_t stream) {
+  using K = PromptTile<N, R, NPT>;
+  auto kern = scan_prompt_kernel<IT, DT, N, R, NPT, SPLIT>;
+  const int smem = (int)(sizeof(PromptSmem<K, N>) + (SPLIT ? sizeof(PromptPiece<R, NPT>) : 0));
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<dim3((unsigned)gx, (unsigned)gy), kPromptThreads, smem, stream>>>(p, a, nseqs);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * pieces), (unsigned)(nseqs < 65535 ? nseqs : 65535));
+  cfg.blockDim = dim3(kPromptThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = pieces;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, a, nseqs, pieces);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <class IT, class DT, int N, int R, int NPT>
+cudaError_t launch_scan_prompt(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+                               cudaStream_t stream) {
+  using K = PromptTile<N, R, NPT>;
+  const int per = p.C / p.G;
+  const int64_t tiles = (int64_t)p.G * ((per + K::CH - 1) / K::CH);
+  if (tiles * 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  // fewer CTAs than SMs: 12289 x 5120 rows in one sequence, 80 CTAs, take 1014
+  // us whole and 713 us in 8 pieces; 9001 x 4096 rows in 16 sequences, 1024
+  // CTAs, 238 us whole and 390 us in pieces
+  if (tiles * nseqs < ssu::sm_count())
+    return launch_prompt_as<IT, DT, N, R, NPT, true>(p, a, nseqs, tiles, 8, stream);
+  return launch_prompt_as<IT, DT, N, R, NPT, false>(p, a, nseqs, tiles, 1, stream);
 }
 
 template <class IT, class DT>
 cudaError_t launch_scan_prompt_n(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
                                  cudaStream_t stream) {
   switch (N) {
-    case 16: return launch_scan_prompt<IT, DT, 16>(p, a, nseqs, stream);
-    case 32: return launch_scan_prompt<IT, DT, 32>(p, a, nseqs, stream);
-    case 64: return launch_scan_prompt<IT, DT, 64>(p, a, nseqs, stream);
-    case 128: return launch_scan_prompt<IT, DT, 128>(p, a, nseqs, stream);
-    case 256: return launch_scan_prompt<IT, DT, 256>(p, a, nseqs, stream);
+    case 16: return launch_scan_prompt<IT, DT, 16, 2, 4>(p, a, nseqs, stream);
+    case 32: return launch_scan_prompt<IT, DT, 32, 2, 4>(p, a, nseqs, stream);
+    case 64: return launch_scan_prompt<IT, DT, 64, 2, 4>(p, a, nseqs, stream);
+    case 128: return launch_scan_prompt<IT, DT, 128, 2, 8>(p, a, nseqs, stream);
+    case 256: return launch_scan_prompt<IT, DT, 256, 2, 8>(p, a, nseqs, stream);
   }
   return cudaErrorInvalidValue;
 }
