@@ -81,10 +81,11 @@ __device__ __forceinline__ __half from_f<__half>(float v) {
   return __float2half_rn(v);
 }
 
-// V consecutive elements of type T, moved as one access of up to 16 bytes
-// (several for more); `raw` keeps them as stored.
+// V consecutive elements of type T, moved in accesses of the largest power of
+// two up to 16 bytes that divides their size.
 template <class T, int V>
-struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+struct alignas((sizeof(T) * V & -(sizeof(T) * V)) < 16 ? (sizeof(T) * V & -(sizeof(T) * V)) : 16)
+    Pack {
   T v[V];
 };
 

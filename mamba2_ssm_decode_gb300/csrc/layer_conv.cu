@@ -20,21 +20,30 @@ struct ConvArgs {
   int64_t o_rs;
   const void* weight;
   const void* bias;
+  int w_vec;                // weight starts on a 16-byte boundary
   int silu;
   int disable;
   int64_t pad;
   const uint8_t* has_init;  // per sequence, or NULL: every valid slot is read
-  int final_only;           // the state is written after a sequence's last row only
+  int final_only;           // prompts: the state is written after a sequence's last row only
 };
 
 template <class WT, int W, int V>
 __device__ __forceinline__ void load_weights(const ConvArgs& p, int64_t c, float (&w)[W][V],
                                              float (&bias)[V]) {
   const WT* wp = static_cast<const WT*>(p.weight) + c * W;
+  // a thread's V W weights are side by side: whole 16 bytes where V channels are
+  Pack<WT, V * W> raw;
+  if (V > 1 && p.w_vec) {
+    raw = load_pack<WT, V * W>(wp);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) raw.v[i] = wp[i];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = to_f(wp[i * W + j]);
+    for (int j = 0; j < W; ++j) w[j][i] = to_f(raw.v[i * W + j]);
 #pragma unroll
   for (int i = 0; i < V; ++i)
     bias[i] = p.bias ? to_f(static_cast<const WT*>(p.bias)[c + i]) : 0.0f;
@@ -71,23 +80,127 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs p, const 
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
     Pack<IT, V> xs[W];
-    const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      xs[j] = from ? load_pack<IT, V>(state + (it.src * (W - 1) + j) * p.C) : zero_pack<IT, V>();
+      xs[j] = it.read_ok ? load_pack<IT, V>(state + (it.src * (W - 1) + j) * p.C) : zero_pack<IT, V>();
     for (int64_t t = 0; t < it.len; ++t) {
       xs[W - 1] = load_pack<IT, V>(x + (it.r0 + t) * p.x_rs);
       store_pack<IT, V>(out + (it.r0 + t) * p.o_rs, conv_row<IT, W, V>(xs, w, bias, p.silu));
       int64_t slot;
-      const bool now = !p.final_only || t == it.len - 1;
-      if (now && it.read_ok && !p.disable &&
-          write_slot(a, s, p.final_only ? 0 : t, p.pad, p.slots, &slot)) {
+      if (it.read_ok && !p.disable && write_slot(a, s, t, p.pad, p.slots, &slot)) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
           store_pack<IT, V>(state + (slot * (W - 1) + j) * p.C, xs[j + 1]);
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) xs[j] = xs[j + 1];
+    }
+  }
+}
+
+// First sequence s with cu[s + 1] > row (nseqs if there is none): the warp's
+// lanes probe 32 places at a time.
+__device__ __forceinline__ int64_t find_sequence(const VarlenArgs& a, int64_t nseqs, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, n = nseqs;
+  while (n > 0) {
+    const int64_t step = (n + 31) / 32;
+    const int64_t last = (lane + 1) * step - 1;  // of this lane's block
+    const bool before = last < n && load_int(a.cu, lo + last + 1, a.meta64) <= row;
+    const int64_t skip = __popc(__ballot_sync(0xffffffffu, before)) * step;
+    lo += skip;
+    n = n - skip < step - 1 ? n - skip : step - 1;
+  }
+  return lo;
+}
+
+// Prompts: a thread owns V channels of a tile of rows, whatever sequences they
+// belong to, and takes them kConvRows at a time: that many loads in flight,
+// then the sliding window of W - 1 rows in fp32 registers.  Rows that reach
+// back to a sequence's slot (its first W - 1) are all done by the tile that
+// holds the sequence's first row, which also writes the slot afterwards: no
+// other CTA reads a slot, so it may be written in place.
+constexpr int kConvRows = 8;
+
+template <class IT, class WT, int W, int V>
+__global__ void __launch_bounds__(128) conv_prompt_kernel(const ConvArgs p, const VarlenArgs a,
+                                                          int64_t nseqs, int tile_rows,
+                                                          int ctiles) {
+  const int64_t tile = blockIdx.x / ctiles;
+  const int64_t c = ((int64_t)(blockIdx.x - tile * ctiles) * blockDim.x + threadIdx.x) * V;
+  const int64_t t0 = tile * tile_rows;
+  const int64_t t1 = t0 + tile_rows < a.rows ? t0 + tile_rows : a.rows;
+  int64_t s = find_sequence(a, nseqs, t0);
+  if (c >= p.C) return;
+  float w[W][V], bias[V];
+  load_weights<WT, W, V>(p, c, w, bias);
+  const IT* x = static_cast<const IT*>(p.x) + c;
+  IT* out = static_cast<IT*>(p.out) + c;
+  IT* state = static_cast<IT*>(p.state) + c;
+
+  for (; s < nseqs; ++s) {
+    const Item it = packed_item(a, s, p.pad, p.slots);
+    if (it.r0 >= t1) break;
+    if (it.len == 0) continue;
+    const int64_t end = it.r0 + it.len;
+    const int64_t reach = it.r0 + W - 1 < end ? it.r0 + W - 1 : end;  // rows that see the slot
+    const bool owner = it.r0 >= t0;
+    int64_t r = owner ? it.r0 : (t0 > reach ? t0 : reach);
+    const int64_t stop = end < t1 ? end : (owner && reach > t1 ? reach : t1);
+    if (!owner && r >= stop) continue;
+    const bool from = owner && it.read_ok && (!p.has_init || p.has_init[s]);
+    Pack<IT, V> first[W - 1];  // the rows in front of r
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      if (!owner) first[j] = load_pack<IT, V>(x + (r - (W - 1) + j) * p.x_rs);
+      else if (from) first[j] = load_pack<IT, V>(state + (it.src * (W - 1) + j) * p.C);
+      else first[j] = zero_pack<IT, V>();
+    }
+    float xs[W][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) xs[j][i] = to_f(first[j].v[i]);
+    auto row = [&](const Pack<IT, V>& in, int64_t at) {
+      Pack<IT, V> y;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        xs[W - 1][i] = to_f(in.v[i]);
+        float acc = bias[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], xs[j][i], acc);
+        y.v[i] = from_f<IT>(p.silu ? silu(acc) : acc);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) xs[j][i] = xs[j + 1][i];
+      }
+      store_pack<IT, V>(out + at * p.o_rs, y);
+    };
+    for (; r + kConvRows <= stop; r += kConvRows) {
+      Pack<IT, V> in[kConvRows];
+#pragma unroll
+      for (int k = 0; k < kConvRows; ++k) in[k] = load_pack<IT, V>(x + (r + k) * p.x_rs);
+#pragma unroll
+      for (int k = 0; k < kConvRows; ++k) row(in[k], r + k);
+    }
+    for (; r < stop; ++r) row(load_pack<IT, V>(x + r * p.x_rs), r);
+
+    int64_t slot;
+    if (owner && it.read_ok && !p.disable && write_slot(a, s, 0, p.pad, p.slots, &slot)) {
+      Pack<IT, V> last[W - 1];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        last[j] = zero_pack<IT, V>();
+        if (it.len + j >= W - 1) {
+          last[j] = load_pack<IT, V>(x + (end - (W - 1) + j) * p.x_rs);
+        } else {  // shorter than the window: rows of the slot are left in it
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k)
+            if (k == it.len + j) last[j] = first[k];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+        store_pack<IT, V>(state + (slot * (W - 1) + j) * p.C, last[j]);
     }
   }
 }
@@ -105,6 +218,20 @@ cudaError_t launch_step(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
   return cudaGetLastError();
 }
 
+template <class IT, class WT, int W, int V>
+cudaError_t launch_prompt(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
+                          cudaStream_t stream) {
+  const int64_t ctiles = (p.C / V + kStepThreads - 1) / kStepThreads;
+  // rows per thread: fewer than 64 while the SMs are not full (16 CTAs each)
+  int rows = 64;
+  while (rows > kConvRows && a.rows / rows * ctiles < 16LL * ssu::sm_count()) rows /= 2;
+  const int64_t grid = ctiles * ((a.rows + rows - 1) / rows);
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  conv_prompt_kernel<IT, WT, W, V>
+      <<<(unsigned)grid, kStepThreads, 0, stream>>>(p, a, nseqs, rows, (int)ctiles);
+  return cudaGetLastError();
+}
+
 // Channels per thread: 16 bytes of a row where every row starts on a 16-byte
 // boundary, 4 bytes (two 16-bit channels) on 4-byte boundaries, else one.
 template <class IT, class WT, int W>
@@ -115,11 +242,16 @@ cudaError_t launch_width(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
     return aligned(p.x, bytes) && aligned(p.out, bytes) && aligned(p.state, bytes) &&
            p.x_rs * B % bytes == 0 && p.o_rs * B % bytes == 0 && p.C * B % bytes == 0;
   };
-  if (rows_on(16)) return launch_step<IT, WT, W, 16 / B>(p, a, nseqs, stream);
+  auto launch = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    return p.final_only ? launch_prompt<IT, WT, W, V>(p, a, nseqs, stream)
+                        : launch_step<IT, WT, W, V>(p, a, nseqs, stream);
+  };
+  if (rows_on(16)) return launch(std::integral_constant<int, 16 / B>{});
   if constexpr (B == 2) {
-    if (rows_on(4)) return launch_step<IT, WT, W, 2>(p, a, nseqs, stream);
+    if (rows_on(4)) return launch(std::integral_constant<int, 2>{});
   }
-  return launch_step<IT, WT, W, 1>(p, a, nseqs, stream);
+  return launch(std::integral_constant<int, 1>{});
 }
 
 template <class IT, class WT>
@@ -184,6 +316,7 @@ ssu_status check_conv(const ssu_conv_params* c, int64_t rows, bool pool_needed, 
   p->o_rs = c->out_row_stride;
   p->weight = c->weight;
   p->bias = c->bias;
+  p->w_vec = aligned(c->weight, 16);
   p->silu = c->activation == SSU_ACT_SILU;
   p->disable = c->disable_state_update != 0;
   p->pad = c->pad_slot_id;
