@@ -17,8 +17,23 @@ int sm_count();                                                  // ssu_abi.cu
 namespace layer {
 using ssu::load_int;
 using ssu::slot_ok;
-using ssu::TableArgs;
-using ssu::VarlenArgs;
+
+// A slot table: entry (s, t) is idx[s ss + t ts], 0 <= t < steps, below numel.
+struct Table {
+  const void* idx;  // nullptr: slot s
+  int64_t numel;
+  int ss, ts, steps;
+};
+
+// The sequences of a call.
+struct Seqs {
+  int rows, n;
+  const void* cu;  // nullptr: `steps` rows each
+  int steps;
+  const void* na;  // nullptr: the read table's entry 0
+  int meta64, idx64;
+  Table src, dst;  // slots read, slots written
+};
 
 // ---------------------------------------------------------------------------
 // host: errors and checks
@@ -52,12 +67,12 @@ inline bool aligned(const void* p, int64_t bytes) {
 ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
                         int64_t dense_steps, const void* na, ssu_dtype meta_dtype,
                         const ssu_slot_table* src, const ssu_slot_table* dst,
-                        ssu_dtype index_dtype, VarlenArgs* out);
+                        ssu_dtype index_dtype, Seqs* out);
 
 // ... and by the prompt-form calls (ssu_conv_fwd_varlen, ssu_scan_fwd_varlen).
 ssu_status check_prompts(bool pool, int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
                          ssu_dtype meta_dtype, const void* src, const void* dst,
-                         ssu_dtype index_dtype, VarlenArgs* out);
+                         ssu_dtype index_dtype, Seqs* out);
 
 // ---------------------------------------------------------------------------
 // device: elements
@@ -107,6 +122,83 @@ __device__ __forceinline__ Pack<T, V> zero_pack() {
   return z;
 }
 
+// V elements as stored, in 32-bit words.
+template <class T, int V>
+struct Words {
+  static constexpr int BYTES = V * (int)sizeof(T), NW = (BYTES + 3) / 4;
+  uint32_t w[NW];
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else return __half2float(__ushort_as_half((unsigned short)(w[i >> 1] >> (i & 1 ? 16 : 0))));
+  }
+  // elements 2 i and 2 i + 1 (zero beyond V)
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2(at(2 * i), 2 * i + 1 < V ? at(2 * i + 1) : 0.0f);
+  }
+  // all V, from (V + 1) / 2 pairs, rounded to nearest even
+  __device__ __forceinline__ void set(const float2* f) {
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[2 * i] = __float_as_uint(f[i].x);
+        if (2 * i + 1 < V) w[2 * i + 1] = __float_as_uint(f[i].y);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 v = __float22bfloat162_rn(f[i]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __float22half2_rn(f[i]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    }
+  }
+  __device__ __forceinline__ void load(const T* p) {  // from a multiple of 16 bytes, or of BYTES
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void load_some(const T* p, int n) {  // elements [0, n), zeros beyond
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (i & 1 ? 16 : 0);
+      }
+  }
+};
+
 // V consecutive elements as fp32: one vector access where `vec` says that the
 // address allows it, else element by element.
 template <class T, int V>
@@ -132,6 +224,15 @@ __device__ __forceinline__ float ex2(float v) {
 
 __device__ __forceinline__ float silu(float v) {
   return __fdividef(v, 1.0f + ex2(-v * kLog2e));
+}
+
+__device__ __forceinline__ float2 silu2(float2 v) {
+  const float2 e = __fmul2_rn(v, make_float2(-kLog2e, -kLog2e));
+  const float2 s = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.0f, 1.0f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(s.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(s.y));
+  return __fmul2_rn(v, r);
 }
 
 // softplus(a + b) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|), v = a + b, for
@@ -175,47 +276,83 @@ __device__ __forceinline__ float softplus_sum(float a, float b) {
 // ---------------------------------------------------------------------------
 // device: rows and slots of packed sequence s
 // ---------------------------------------------------------------------------
-struct Item {
-  int64_t r0;      // first row
-  int64_t len;     // rows (0: an empty sequence, nothing to do)
-  int64_t src;     // slot read
-  bool read_ok;    // ... when it is a valid one; else the sequence runs from zeros and writes none
+// An index as stored: two 32-bit words (one twice where indices are 32 bits
+// wide).  Absent arrays read zeros.  Loading and looking at it are apart, with
+// no choice between kinds of load in between, so that the loads of a call's
+// metadata wait for each other only where one needs the other's value.
+__device__ const int kNoIndex[2] = {0, 0};
+
+struct RawIndex {
+  int lo, hi;
+  __device__ __forceinline__ int64_t value(int is64) const {
+    return is64 ? (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo) : (int64_t)lo;
+  }
 };
 
-__device__ __forceinline__ Item packed_item(const VarlenArgs& a, int64_t s, int64_t pad,
-                                            int64_t slots) {
+__device__ __forceinline__ RawIndex load_index(const void* p, int64_t i, int is64) {
+  const int* w = p ? static_cast<const int*>(p) + (i << is64) : kNoIndex;
+  return RawIndex{w[0], w[is64]};
+}
+
+// Entry (s, pos) of a slot table, as stored; `found` is false where the table
+// has no such entry.  Without a table the slot is s itself.
+struct Slot {
+  RawIndex raw;
+  bool found, table;
+  __device__ __forceinline__ int64_t id(int s, int is64) const {
+    return table ? raw.value(is64) : s;
+  }
+};
+
+__device__ __forceinline__ Slot load_slot(const Table& t, int s, int pos, int is64) {
+  const int64_t e = (int64_t)s * t.ss + (int64_t)pos * t.ts;
+  Slot slot;
+  slot.table = t.idx != nullptr;
+  const bool inside = (unsigned)pos < (unsigned)t.steps && e < t.numel;
+  slot.found = inside || !slot.table;
+  slot.raw = load_index(inside ? t.idx : nullptr, e, is64);
+  return slot;
+}
+
+struct Item {
+  int r0, len;   // first row, rows (0: an empty sequence, nothing to do)
+  int64_t src;   // slot read
+  bool read_ok;  // ... when it is a valid one; else the sequence runs from zeros and writes none
+};
+
+__device__ __forceinline__ int clamped(int64_t v, int most) {
+  return v < 0 ? 0 : v < most ? (int)v : most;
+}
+
+// ONE: every sequence is one row and reads entry 0 of its table.
+template <bool ONE = false>
+__device__ __forceinline__ Item packed_item(const Seqs& a, int s, int64_t pad, int64_t slots) {
   Item it;
-  int64_t begin, end;
-  if (a.cu) {
-    begin = load_int(a.cu, s, a.meta64);
-    end = load_int(a.cu, s + 1, a.meta64);
+  Slot read;
+  if constexpr (ONE) {
+    read = load_slot(a.src, s, 0, a.idx64);
+    it.r0 = s;
+    it.len = 1;
   } else {
-    begin = s * a.dense_steps;
-    end = begin + a.dense_steps;
+    const RawIndex b = load_index(a.cu, s, a.meta64), e = load_index(a.cu, s + 1, a.meta64);
+    const RawIndex n = load_index(a.na, s, a.meta64);
+    const int64_t pos = a.na ? n.value(a.meta64) - 1 : 0;
+    read = load_slot(a.src, s, pos < 0 || pos > 0x7fffffff ? -1 : (int)pos, a.idx64);
+    it.r0 = clamped(a.cu ? b.value(a.meta64) : (int64_t)s * a.steps, a.rows);
+    const int end = clamped(a.cu ? e.value(a.meta64) : (int64_t)(s + 1) * a.steps, a.rows);
+    it.len = end > it.r0 ? end - it.r0 : 0;
   }
-  if (begin < 0) begin = 0;
-  if (end > a.rows) end = a.rows;
-  it.r0 = begin;
-  it.len = end > begin ? end - begin : 0;
-  it.src = s;
-  bool found = true;
-  if (a.src.idx) {
-    const int64_t col = a.na ? load_int(a.na, s, a.meta64) - 1 : 0;
-    found = ssu::table_entry(a.src, s, col, a.idx64, &it.src);
-  }
-  it.read_ok = found && slot_ok(it.src, pad, slots);
+  it.src = read.id(s, a.idx64);
+  it.read_ok = read.found && slot_ok(it.src, pad, slots);
   return it;
 }
 
-// Slot that takes the state after row t of sequence s: entry t of the write
-// table, of the read table without one, slot s without either.
-__device__ __forceinline__ bool write_slot(const VarlenArgs& a, int64_t s, int64_t t, int64_t pad,
-                                           int64_t slots, int64_t* slot) {
-  bool found = true;
-  if (a.dst.idx) found = ssu::table_entry(a.dst, s, t, a.idx64, slot);
-  else if (a.src.idx) found = ssu::table_entry(a.src, s, t, a.idx64, slot);
-  else *slot = s;
-  return found && slot_ok(*slot, pad, slots);
+// Slot that takes the state after row t of sequence s.
+__device__ __forceinline__ bool write_slot(const Seqs& a, int s, int t, int64_t pad, int64_t slots,
+                                           int64_t* slot) {
+  const Slot to = load_slot(a.dst, s, t, a.idx64);
+  *slot = to.id(s, a.idx64);
+  return to.found && slot_ok(*slot, pad, slots);
 }
 
 }  // namespace layer

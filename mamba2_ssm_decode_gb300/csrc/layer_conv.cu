@@ -20,96 +20,139 @@ struct ConvArgs {
   int64_t o_rs;
   const void* weight;
   const void* bias;
-  int w_vec;                // weight starts on a 16-byte boundary
+  int w_vec;                // weight and bias start on 16-byte boundaries
   int silu;
   int disable;
   int64_t pad;
   const uint8_t* has_init;  // per sequence, or NULL: every valid slot is read
-  int final_only;           // prompts: the state is written after a sequence's last row only
+  int prompt;               // the prompt form: the state is written after a sequence's last row only
 };
 
+// A thread's V W weights and V biases are side by side: whole vectors where V
+// channels are, fp32 pairs of neighbouring channels in registers.
 template <class WT, int W, int V>
-__device__ __forceinline__ void load_weights(const ConvArgs& p, int64_t c, float (&w)[W][V],
-                                             float (&bias)[V]) {
+__device__ __forceinline__ void load_weights(const ConvArgs& p, int64_t c,
+                                             float2 (&w)[W][(V + 1) / 2],
+                                             float2 (&bias)[(V + 1) / 2]) {
   const WT* wp = static_cast<const WT*>(p.weight) + c * W;
-  // a thread's V W weights are side by side: whole 16 bytes where V channels are
+  const WT* bp = static_cast<const WT*>(p.bias) + c;
   Pack<WT, V * W> raw;
+  Pack<WT, V> b = zero_pack<WT, V>();
   if (V > 1 && p.w_vec) {
     raw = load_pack<WT, V * W>(wp);
+    if (p.bias) b = load_pack<WT, V>(bp);
   } else {
 #pragma unroll
     for (int i = 0; i < V * W; ++i) raw.v[i] = wp[i];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (p.bias) b.v[i] = bp[i];
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < (V + 1) / 2; ++i) {
+    const int k = 2 * i + 1 < V ? 2 * i + 1 : 2 * i;
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = to_f(raw.v[i * W + j]);
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    bias[i] = p.bias ? to_f(static_cast<const WT*>(p.bias)[c + i]) : 0.0f;
+    for (int j = 0; j < W; ++j)
+      w[j][i] = make_float2(to_f(raw.v[2 * i * W + j]), to_f(raw.v[k * W + j]));
+    bias[i] = make_float2(to_f(b.v[2 * i]), to_f(b.v[k]));
+  }
 }
 
 // One row: xs holds the W rows that its taps read, oldest first.
 template <class IT, int W, int V>
-__device__ __forceinline__ Pack<IT, V> conv_row(const Pack<IT, V>* xs, const float (&w)[W][V],
-                                                const float (&bias)[V], int act) {
-  Pack<IT, V> y;
+__device__ __forceinline__ void conv_row(IT* out, const float2 (&xs)[W][(V + 1) / 2],
+                                         const float2 (&w)[W][(V + 1) / 2],
+                                         const float2 (&bias)[(V + 1) / 2], int act) {
+  float2 y[(V + 1) / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float acc = bias[i];
+  for (int i = 0; i < (V + 1) / 2; ++i) {
+    y[i] = bias[i];
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], to_f(xs[j].v[i]), acc);
-    y.v[i] = from_f<IT>(act ? silu(acc) : acc);
+    for (int j = 0; j < W; ++j) y[i] = __ffma2_rn(w[j][i], xs[j][i], y[i]);
+    if (act) y[i] = silu2(y[i]);
   }
-  return y;
+  Words<IT, V> r;
+  r.set(y);
+  r.store(out);
 }
 
 // Decode: a thread owns V channels of one sequence after another and walks the
-// sequence's rows with the window of W - 1 rows in registers.
-template <class IT, class WT, int W, int V>
-__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs p, const VarlenArgs a,
-                                                        int64_t nseqs) {
-  const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
+// sequence's rows with the window of W - 1 rows in registers.  What it needs
+// of up to ROWS rows (the rows, and the slots that take the state after them)
+// is asked for at once, beside the slot's rows.  ROWS 1: one row a sequence.
+constexpr int kStepThreads = 128;
+
+template <class IT, class WT, int W, int V, int ROWS>
+__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvArgs p, const Seqs a) {
+  const int64_t c = ((int64_t)blockIdx.x * kStepThreads + threadIdx.x) * V;
   if (c >= p.C) return;
-  float w[W][V], bias[V];
+  constexpr int P = (V + 1) / 2;
+  float2 w[W][P], bias[P];
   load_weights<WT, W, V>(p, c, w, bias);
   const IT* x = static_cast<const IT*>(p.x) + c;
   IT* out = static_cast<IT*>(p.out) + c;
   IT* state = static_cast<IT*>(p.state) + c;
-  for (int64_t s = blockIdx.y; s < nseqs; s += gridDim.y) {
-    const Item it = packed_item(a, s, p.pad, p.slots);
+  for (int s = blockIdx.y; s < a.n; s += gridDim.y) {
+    const Item it = packed_item<ROWS == 1>(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
-    Pack<IT, V> xs[W];
+    Words<IT, V> in[W - 1 + ROWS];  // the window, then the rows, as stored
+    float2 xs[W][P];
+    for (int t0 = 0; t0 < it.len; t0 += ROWS) {
+      const int n = it.len - t0 < ROWS ? it.len - t0 : ROWS;
+      Slot to[ROWS];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-      xs[j] = it.read_ok ? load_pack<IT, V>(state + (it.src * (W - 1) + j) * p.C) : zero_pack<IT, V>();
-    for (int64_t t = 0; t < it.len; ++t) {
-      xs[W - 1] = load_pack<IT, V>(x + (it.r0 + t) * p.x_rs);
-      store_pack<IT, V>(out + (it.r0 + t) * p.o_rs, conv_row<IT, W, V>(xs, w, bias, p.silu));
-      int64_t slot;
-      if (it.read_ok && !p.disable && write_slot(a, s, t, p.pad, p.slots, &slot)) {
+      for (int k = 0; k < ROWS; ++k) {
+        if (k < n) {
+          in[W - 1 + k].load(x + (it.r0 + t0 + k) * p.x_rs);
+          to[k] = load_slot(a.dst, s, t0 + k, a.idx64);
+        }
+      }
+      if (t0 == 0) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          if (it.read_ok) in[j].load(state + (it.src * (W - 1) + j) * p.C);
+          else in[j].zero();
+        }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-          store_pack<IT, V>(state + (slot * (W - 1) + j) * p.C, xs[j + 1]);
+#pragma unroll
+          for (int i = 0; i < P; ++i) xs[j][i] = in[j].pair(i);
       }
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j) xs[j] = xs[j + 1];
+      for (int k = 0; k < ROWS; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int i = 0; i < P; ++i) xs[W - 1][i] = in[W - 1 + k].pair(i);
+        conv_row<IT, W, V>(out + (it.r0 + t0 + k) * p.o_rs, xs, w, bias, p.silu);
+        const int64_t slot = to[k].id(s, a.idx64);
+        if (it.read_ok && !p.disable && to[k].found && slot_ok(slot, p.pad, p.slots)) {
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+            in[k + 1 + j].store(state + (slot * (W - 1) + j) * p.C);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < P; ++i) xs[j][i] = xs[j + 1][i];
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) in[j] = in[ROWS + j];
     }
   }
 }
 
-// First sequence s with cu[s + 1] > row (nseqs if there is none): the warp's
+// First sequence s with cu[s + 1] > row (a.n if there is none): the warp's
 // lanes probe 32 places at a time.
-__device__ __forceinline__ int64_t find_sequence(const VarlenArgs& a, int64_t nseqs, int64_t row) {
+__device__ __forceinline__ int find_sequence(const Seqs& a, int row) {
   const int lane = threadIdx.x & 31;
-  int64_t lo = 0, n = nseqs;
+  int lo = 0, n = a.n;
   while (n > 0) {
-    const int64_t step = (n + 31) / 32;
-    const int64_t last = (lane + 1) * step - 1;  // of this lane's block
+    const int step = (n + 31) / 32;
+    const int64_t last = (int64_t)(lane + 1) * step - 1;  // of this lane's block
     const bool before = last < n && load_int(a.cu, lo + last + 1, a.meta64) <= row;
-    const int64_t skip = __popc(__ballot_sync(0xffffffffu, before)) * step;
-    lo += skip;
-    n = n - skip < step - 1 ? n - skip : step - 1;
+    const int64_t skip = (int64_t)__popc(__ballot_sync(0xffffffffu, before)) * step;
+    lo += (int)skip;
+    n = n - skip < step - 1 ? (int)(n - skip) : step - 1;
   }
   return lo;
 }
@@ -120,134 +163,147 @@ __device__ __forceinline__ int64_t find_sequence(const VarlenArgs& a, int64_t ns
 // back to a sequence's slot (its first W - 1) are all done by the tile that
 // holds the sequence's first row, which also writes the slot afterwards: no
 // other CTA reads a slot, so it may be written in place.
-constexpr int kConvRows = 8;
+template <class IT>
+constexpr int kRowsInFlight = sizeof(IT) == 2 ? 8 : 4;
+constexpr int kPromptThreads = 128;
 
 template <class IT, class WT, int W, int V>
-__global__ void __launch_bounds__(128) conv_prompt_kernel(const ConvArgs p, const VarlenArgs a,
-                                                          int64_t nseqs, int tile_rows,
-                                                          int ctiles) {
-  const int64_t tile = blockIdx.x / ctiles;
-  const int64_t c = ((int64_t)(blockIdx.x - tile * ctiles) * blockDim.x + threadIdx.x) * V;
-  const int64_t t0 = tile * tile_rows;
-  const int64_t t1 = t0 + tile_rows < a.rows ? t0 + tile_rows : a.rows;
-  int64_t s = find_sequence(a, nseqs, t0);
+__global__ void __launch_bounds__(kPromptThreads, sizeof(IT) == 2 ? 6 : 4)
+    conv_prompt_kernel(const ConvArgs p, const Seqs a, int tile_rows,
+                       int ctiles) {
+  constexpr int kConvRows = kRowsInFlight<IT>;
+  const int tile = blockIdx.x / ctiles;
+  const int64_t c = ((int64_t)(blockIdx.x - tile * ctiles) * kPromptThreads + threadIdx.x) * V;
+  const int t0 = tile * tile_rows;  // below a.rows
+  const int t1 = a.rows - t0 < tile_rows ? a.rows : t0 + tile_rows;
+  int s = find_sequence(a, t0);
   if (c >= p.C) return;
-  float w[W][V], bias[V];
+  constexpr int P = (V + 1) / 2;
+  float2 w[W][P], bias[P];
   load_weights<WT, W, V>(p, c, w, bias);
   const IT* x = static_cast<const IT*>(p.x) + c;
   IT* out = static_cast<IT*>(p.out) + c;
   IT* state = static_cast<IT*>(p.state) + c;
 
-  for (; s < nseqs; ++s) {
+  for (; s < a.n; ++s) {
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.r0 >= t1) break;
     if (it.len == 0) continue;
-    const int64_t end = it.r0 + it.len;
-    const int64_t reach = it.r0 + W - 1 < end ? it.r0 + W - 1 : end;  // rows that see the slot
+    const int end = it.r0 + it.len;
+    const int reach = it.len > W - 1 ? it.r0 + W - 1 : end;  // rows that see the slot
     const bool owner = it.r0 >= t0;
-    int64_t r = owner ? it.r0 : (t0 > reach ? t0 : reach);
-    const int64_t stop = end < t1 ? end : (owner && reach > t1 ? reach : t1);
+    int r = owner ? it.r0 : (t0 > reach ? t0 : reach);
+    const int stop = end < t1 ? end : (owner && reach > t1 ? reach : t1);
     if (!owner && r >= stop) continue;
     const bool from = owner && it.read_ok && (!p.has_init || p.has_init[s]);
-    Pack<IT, V> first[W - 1];  // the rows in front of r
+    Words<IT, V> first[W - 1];  // the rows in front of r
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      if (!owner) first[j] = load_pack<IT, V>(x + (r - (W - 1) + j) * p.x_rs);
-      else if (from) first[j] = load_pack<IT, V>(state + (it.src * (W - 1) + j) * p.C);
-      else first[j] = zero_pack<IT, V>();
+      if (!owner) first[j].load(x + (r - (W - 1) + j) * p.x_rs);
+      else if (from) first[j].load(state + (it.src * (W - 1) + j) * p.C);
+      else first[j].zero();
     }
-    float xs[W][V];
+    float2 xs[W][P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) xs[j][i] = to_f(first[j].v[i]);
-    auto row = [&](const Pack<IT, V>& in, int64_t at) {
-      Pack<IT, V> y;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        xs[W - 1][i] = to_f(in.v[i]);
-        float acc = bias[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], xs[j][i], acc);
-        y.v[i] = from_f<IT>(p.silu ? silu(acc) : acc);
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) xs[j][i] = xs[j + 1][i];
-      }
-      store_pack<IT, V>(out + at * p.o_rs, y);
+      for (int i = 0; i < P; ++i) xs[j][i] = first[j].pair(i);
+    // kConvRows loads are always in flight: a row's place takes the row
+    // kConvRows on (the last one again beyond the end) as soon as it is in xs
+    Words<IT, V> in[kConvRows];
+    auto fetch = [&](int k, int at) {
+      in[k].load(x + at * p.x_rs);
     };
-    for (; r + kConvRows <= stop; r += kConvRows) {
-      Pack<IT, V> in[kConvRows];
+    auto row = [&](int k, int at) {
 #pragma unroll
-      for (int k = 0; k < kConvRows; ++k) in[k] = load_pack<IT, V>(x + (r + k) * p.x_rs);
+      for (int i = 0; i < P; ++i) xs[W - 1][i] = in[k].pair(i);
+      fetch(k, stop - at > kConvRows ? at + kConvRows : stop - 1);
+      conv_row<IT, W, V>(out + at * p.o_rs, xs, w, bias, p.silu);
 #pragma unroll
-      for (int k = 0; k < kConvRows; ++k) row(in[k], r + k);
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int i = 0; i < P; ++i) xs[j][i] = xs[j + 1][i];
+    };
+#pragma unroll
+    for (int k = 0; k < kConvRows; ++k) fetch(k, stop - r > k ? r + k : stop - 1);
+    for (; stop - r >= kConvRows; r += kConvRows) {
+#pragma unroll
+      for (int k = 0; k < kConvRows; ++k) row(k, r + k);
     }
-    for (; r < stop; ++r) row(load_pack<IT, V>(x + r * p.x_rs), r);
+#pragma unroll
+    for (int k = 0; k < kConvRows - 1; ++k)
+      if (stop - r > k) row(k, r + k);
 
     int64_t slot;
     if (owner && it.read_ok && !p.disable && write_slot(a, s, 0, p.pad, p.slots, &slot)) {
-      Pack<IT, V> last[W - 1];
+      Words<IT, V> last[W - 1];
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) {
-        last[j] = zero_pack<IT, V>();
         if (it.len + j >= W - 1) {
-          last[j] = load_pack<IT, V>(x + (end - (W - 1) + j) * p.x_rs);
+          last[j].load(x + (end - (W - 1) + j) * p.x_rs);
         } else {  // shorter than the window: rows of the slot are left in it
+          last[j].zero();
 #pragma unroll
           for (int k = 0; k < W - 1; ++k)
             if (k == it.len + j) last[j] = first[k];
         }
       }
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        store_pack<IT, V>(state + (slot * (W - 1) + j) * p.C, last[j]);
+      for (int j = 0; j < W - 1; ++j) last[j].store(state + (slot * (W - 1) + j) * p.C);
     }
   }
 }
 
-constexpr int kStepThreads = 128;
-
-template <class IT, class WT, int W, int V>
-cudaError_t launch_step(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
-                        cudaStream_t stream) {
+template <class IT, class WT, int W, int V, int ROWS>
+cudaError_t launch_step_as(const ConvArgs& p, const Seqs& a, cudaStream_t stream) {
   const int64_t gx = (p.C / V + kStepThreads - 1) / kStepThreads;
-  const int64_t gy = nseqs < 65535 ? nseqs : 65535;
   if (gx > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  conv_step_kernel<IT, WT, W, V>
-      <<<dim3((unsigned)gx, (unsigned)gy), kStepThreads, 0, stream>>>(p, a, nseqs);
+  // a CTA keeps its weights over several sequences once the SMs are full
+  int64_t gy = (16LL * ssu::sm_count() + gx - 1) / gx;
+  if (gy > a.n) gy = a.n;
+  if (gy > 65535) gy = 65535;
+  conv_step_kernel<IT, WT, W, V, ROWS>
+      <<<dim3((unsigned)gx, (unsigned)gy), kStepThreads, 0, stream>>>(p, a);
   return cudaGetLastError();
 }
 
 template <class IT, class WT, int W, int V>
-cudaError_t launch_prompt(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_step(const ConvArgs& p, const Seqs& a, cudaStream_t stream) {
+  if (!a.cu && !a.na && a.steps == 1) return launch_step_as<IT, WT, W, V, 1>(p, a, stream);
+  return launch_step_as<IT, WT, W, V, 4>(p, a, stream);
+}
+
+template <class IT, class WT, int W, int V>
+cudaError_t launch_prompt(const ConvArgs& p, const Seqs& a,
                           cudaStream_t stream) {
-  const int64_t ctiles = (p.C / V + kStepThreads - 1) / kStepThreads;
+  const int64_t ctiles = (p.C / V + kPromptThreads - 1) / kPromptThreads;
   // rows per thread: fewer than 64 while the SMs are not full (16 CTAs each)
   int rows = 64;
-  while (rows > kConvRows && a.rows / rows * ctiles < 16LL * ssu::sm_count()) rows /= 2;
-  const int64_t grid = ctiles * ((a.rows + rows - 1) / rows);
+  while (rows > kRowsInFlight<IT> && a.rows / rows * ctiles < 16LL * ssu::sm_count()) rows /= 2;
+  const int64_t grid = ctiles * (((int64_t)a.rows + rows - 1) / rows);
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   conv_prompt_kernel<IT, WT, W, V>
-      <<<(unsigned)grid, kStepThreads, 0, stream>>>(p, a, nseqs, rows, (int)ctiles);
+      <<<(unsigned)grid, kPromptThreads, 0, stream>>>(p, a, rows, (int)ctiles);
   return cudaGetLastError();
 }
 
-// Channels per thread: 16 bytes of a row where every row starts on a 16-byte
-// boundary, 4 bytes (two 16-bit channels) on 4-byte boundaries, else one.
+// Channels per thread: four where every row starts on a multiple of four (at
+// 20634 x 5376 bf16 rows they leave 24 warps an SM and take 84 us; eight take
+// 128 registers, 16 warps and 100 us; two fp32 ones 191 us where four take
+// 171), two 16-bit ones on 4 bytes, else one.
 template <class IT, class WT, int W>
-cudaError_t launch_width(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
-                         cudaStream_t stream) {
+cudaError_t launch_width(const ConvArgs& p, const Seqs& a, cudaStream_t stream) {
   constexpr int B = (int)sizeof(IT);
+  auto launch = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    return p.prompt ? launch_prompt<IT, WT, W, V>(p, a, stream)
+                    : launch_step<IT, WT, W, V>(p, a, stream);
+  };
   auto rows_on = [&](int64_t bytes) {
     return aligned(p.x, bytes) && aligned(p.out, bytes) && aligned(p.state, bytes) &&
            p.x_rs * B % bytes == 0 && p.o_rs * B % bytes == 0 && p.C * B % bytes == 0;
   };
-  auto launch = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    return p.final_only ? launch_prompt<IT, WT, W, V>(p, a, nseqs, stream)
-                        : launch_step<IT, WT, W, V>(p, a, nseqs, stream);
-  };
-  if (rows_on(16)) return launch(std::integral_constant<int, 16 / B>{});
+  if (rows_on(4 * B)) return launch(std::integral_constant<int, 4>{});
   if constexpr (B == 2) {
     if (rows_on(4)) return launch(std::integral_constant<int, 2>{});
   }
@@ -255,28 +311,27 @@ cudaError_t launch_width(const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
 }
 
 template <class IT, class WT>
-cudaError_t launch_types(int W, const ConvArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_types(int W, const ConvArgs& p, const Seqs& a,
                          cudaStream_t stream) {
   switch (W) {
-    case 2: return launch_width<IT, WT, 2>(p, a, nseqs, stream);
-    case 3: return launch_width<IT, WT, 3>(p, a, nseqs, stream);
-    case 4: return launch_width<IT, WT, 4>(p, a, nseqs, stream);
+    case 2: return launch_width<IT, WT, 2>(p, a, stream);
+    case 3: return launch_width<IT, WT, 3>(p, a, stream);
+    case 4: return launch_width<IT, WT, 4>(p, a, stream);
   }
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_conv(const ssu_conv_params* c, const ConvArgs& p, const VarlenArgs& a,
-                        int64_t nseqs, cudaStream_t stream) {
+cudaError_t launch_conv(const ssu_conv_params* c, const ConvArgs& p, const Seqs& a, cudaStream_t stream) {
   const int W = (int)c->width;
   const bool f32w = c->weight_dtype == SSU_F32;
   switch (c->io_dtype) {
-    case SSU_F32: return launch_types<float, float>(W, p, a, nseqs, stream);
+    case SSU_F32: return launch_types<float, float>(W, p, a, stream);
     case SSU_BF16:
-      return f32w ? launch_types<__nv_bfloat16, float>(W, p, a, nseqs, stream)
-                  : launch_types<__nv_bfloat16, __nv_bfloat16>(W, p, a, nseqs, stream);
+      return f32w ? launch_types<__nv_bfloat16, float>(W, p, a, stream)
+                  : launch_types<__nv_bfloat16, __nv_bfloat16>(W, p, a, stream);
     case SSU_F16:
-      return f32w ? launch_types<__half, float>(W, p, a, nseqs, stream)
-                  : launch_types<__half, __half>(W, p, a, nseqs, stream);
+      return f32w ? launch_types<__half, float>(W, p, a, stream)
+                  : launch_types<__half, __half>(W, p, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -316,7 +371,7 @@ ssu_status check_conv(const ssu_conv_params* c, int64_t rows, bool pool_needed, 
   p->o_rs = c->out_row_stride;
   p->weight = c->weight;
   p->bias = c->bias;
-  p->w_vec = aligned(c->weight, 16);
+  p->w_vec = aligned(c->weight, 16) && aligned(c->bias, 16);
   p->silu = c->activation == SSU_ACT_SILU;
   p->disable = c->disable_state_update != 0;
   p->pad = c->pad_slot_id;
@@ -335,14 +390,14 @@ ssu_status ssu_conv_update(const ssu_conv_params* c, int64_t nseqs, int64_t rows
                            ssu_dtype index_dtype, struct CUstream_st* stream) {
   using namespace layer;
   ConvArgs p;
-  VarlenArgs a;
+  Seqs a;
   ssu_status st = check_conv(c, rows, true, &p);
   if (st == SSU_OK)
     st = check_packed(c->slots, nseqs, rows, cu_seqlens, dense_steps, num_accepted_tokens,
                       meta_dtype, src, dst, index_dtype, &a);
   if (st != SSU_OK) return st;
   if (nseqs == 0 || rows == 0) return ok();
-  return launched(launch_conv(c, p, a, nseqs, (cudaStream_t)stream));
+  return launched(launch_conv(c, p, a, (cudaStream_t)stream));
 }
 
 ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* c, int64_t nseqs, int64_t rows,
@@ -352,7 +407,7 @@ ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* c, int64_t nseqs, int64_t 
                                const uint8_t* has_initial_state, struct CUstream_st* stream) {
   using namespace layer;
   ConvArgs p;
-  VarlenArgs a;
+  Seqs a;
   ssu_status st = check_conv(c, rows, false, &p);
   if (st == SSU_OK)
     st = check_prompts(c->conv_state != nullptr, c->slots, nseqs, rows, cu_seqlens, meta_dtype,
@@ -362,8 +417,8 @@ ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* c, int64_t nseqs, int64_t 
     return fail(SSU_ERR_INVALID_ARGUMENT, "out must not be x: rows are read by several blocks");
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
-  p.final_only = 1;
-  return launched(launch_conv(c, p, a, nseqs, (cudaStream_t)stream));
+  p.prompt = 1;
+  return launched(launch_conv(c, p, a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -4,12 +4,16 @@
 
 namespace layer {
 
-static ssu_status table_args(const ssu_slot_table* t, const char* name, TableArgs* out) {
-  *out = TableArgs{nullptr, 0, 0, 0, 0};
+static ssu_status table_args(const ssu_slot_table* t, const char* name, Table* out) {
+  *out = Table{};
   if (!t || !t->indices) return SSU_OK;
-  if (t->numel < 0 || t->steps < 0)
-    return fail(SSU_ERR_INVALID_ARGUMENT, "%s: numel and steps must be >= 0", name);
-  *out = TableArgs{t->indices, t->numel, t->seq_stride, t->step_stride, t->steps};
+  if (t->numel < 0 || t->steps < 0 || t->seq_stride < 0 || t->step_stride < 0)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "%s: numel, steps and strides must be >= 0", name);
+  const int64_t most = 0x7fffffff;
+  if (t->seq_stride > most || t->step_stride > most)
+    return fail(SSU_ERR_UNSUPPORTED, "%s: strides must be below 2^31", name);
+  *out = Table{t->indices, t->numel, (int)t->seq_stride, (int)t->step_stride,
+               (int)(t->steps < most ? t->steps : most)};
   return SSU_OK;
 }
 
@@ -23,9 +27,9 @@ static ssu_status check_counts(int64_t nseqs, int64_t rows) {
 ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
                         int64_t dense_steps, const void* na, ssu_dtype meta_dtype,
                         const ssu_slot_table* src, const ssu_slot_table* dst,
-                        ssu_dtype index_dtype, VarlenArgs* out) {
+                        ssu_dtype index_dtype, Seqs* out) {
   ssu_status st = check_counts(nseqs, rows);
-  VarlenArgs a{};
+  Seqs a{};
   if (st == SSU_OK) st = table_args(src, "state_batch_indices", &a.src);
   if (st == SSU_OK) st = table_args(dst, "dst_state_batch_indices", &a.dst);
   if (st != SSU_OK) return st;
@@ -38,7 +42,7 @@ ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* 
     return fail(SSU_ERR_INVALID_ARGUMENT,
                 "num_accepted_tokens selects the read slot, so it needs state_batch_indices to "
                 "read it from");
-  if (!cu && (dense_steps < 1 || nseqs * dense_steps != rows))
+  if (!cu && (dense_steps < 1 || dense_steps > 0x7fffffff || nseqs * dense_steps != rows))
     return fail(SSU_ERR_INVALID_ARGUMENT,
                 "without cu_seqlens %lld rows cannot be split into %lld sequences of %lld steps",
                 (long long)rows, (long long)nseqs, (long long)dense_steps);
@@ -47,9 +51,11 @@ ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* 
                 "without state_batch_indices sequence s uses slot s: %lld sequences exceed %lld "
                 "slots",
                 (long long)nseqs, (long long)slots);
-  a.rows = rows;
+  if (!a.dst.idx) a.dst = a.src;
+  a.rows = (int)rows;
+  a.n = (int)nseqs;
   a.cu = cu;
-  a.dense_steps = dense_steps;
+  a.steps = cu ? 0 : (int)dense_steps;
   a.na = na;
   a.meta64 = meta_dtype == SSU_I64;
   a.idx64 = index_dtype == SSU_I64;
@@ -59,7 +65,7 @@ ssu_status check_packed(int64_t slots, int64_t nseqs, int64_t rows, const void* 
 
 ssu_status check_prompts(bool pool, int64_t slots, int64_t nseqs, int64_t rows, const void* cu,
                          ssu_dtype meta_dtype, const void* src, const void* dst,
-                         ssu_dtype index_dtype, VarlenArgs* out) {
+                         ssu_dtype index_dtype, Seqs* out) {
   ssu_status st = check_counts(nseqs, rows);
   if (st != SSU_OK) return st;
   if (!cu) return fail(SSU_ERR_INVALID_ARGUMENT, "cu_seqlens must not be NULL");
@@ -74,12 +80,13 @@ ssu_status check_prompts(bool pool, int64_t slots, int64_t nseqs, int64_t rows, 
                 "without state_batch_indices sequence s uses slot s: %lld sequences exceed %lld "
                 "slots",
                 (long long)nseqs, (long long)slots);
-  VarlenArgs a{};
-  a.rows = rows;
+  Seqs a{};
+  a.rows = (int)rows;
+  a.n = (int)nseqs;
   a.cu = cu;
   a.meta64 = meta_dtype == SSU_I64;
-  if (src) a.src = TableArgs{src, nseqs, 1, 1, 1};
-  if (dst) a.dst = TableArgs{dst, nseqs, 1, 1, 1};
+  if (src) a.src = Table{src, nseqs, 1, 1, 1};
+  a.dst = dst ? Table{dst, nseqs, 1, 1, 1} : a.src;
   a.idx64 = index_dtype == SSU_I64;
   *out = a;
   return SSU_OK;
@@ -171,24 +178,22 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
   return SSU_OK;
 }
 
-static cudaError_t launch_step(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
-                               int64_t nseqs, cudaStream_t stream) {
+static cudaError_t launch_step(const ssu_scan_params* c, const ScanArgs& p, const Seqs& a, cudaStream_t stream) {
   const int N = (int)c->dstate;
   switch (c->io_dtype) {
-    case SSU_F32: return launch_scan_f32(N, p, a, nseqs, stream);
-    case SSU_BF16: return launch_scan_bf16(N, p, a, nseqs, stream);
-    case SSU_F16: return launch_scan_f16(N, p, a, nseqs, stream);
+    case SSU_F32: return launch_scan_f32(N, p, a, stream);
+    case SSU_BF16: return launch_scan_bf16(N, p, a, stream);
+    case SSU_F16: return launch_scan_f16(N, p, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
-static cudaError_t launch_prompt(const ssu_scan_params* c, const ScanArgs& p, const VarlenArgs& a,
-                                 int64_t nseqs, cudaStream_t stream) {
+static cudaError_t launch_prompt(const ssu_scan_params* c, const ScanArgs& p, const Seqs& a, cudaStream_t stream) {
   const int N = (int)c->dstate;
   switch (c->io_dtype) {
-    case SSU_F32: return launch_prompt_f32(N, p, a, nseqs, stream);
-    case SSU_BF16: return launch_prompt_bf16(N, p, a, nseqs, stream);
-    case SSU_F16: return launch_prompt_f16(N, p, a, nseqs, stream);
+    case SSU_F32: return launch_prompt_f32(N, p, a, stream);
+    case SSU_BF16: return launch_prompt_bf16(N, p, a, stream);
+    case SSU_F16: return launch_prompt_f16(N, p, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -205,14 +210,14 @@ ssu_status ssu_scan_update(const ssu_scan_params* c, int64_t nseqs, int64_t rows
                            ssu_dtype index_dtype, struct CUstream_st* stream) {
   using namespace layer;
   ScanArgs p;
-  VarlenArgs a;
+  Seqs a;
   ssu_status st = check_scan(c, rows, true, &p);
   if (st == SSU_OK)
     st = check_packed(c->slots, nseqs, rows, cu_seqlens, dense_steps, num_accepted_tokens,
                       meta_dtype, src, dst, index_dtype, &a);
   if (st != SSU_OK) return st;
   if (nseqs == 0 || rows == 0) return ok();
-  return launched(launch_step(c, p, a, nseqs, (cudaStream_t)stream));
+  return launched(launch_step(c, p, a, (cudaStream_t)stream));
 }
 
 ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t rows,
@@ -222,7 +227,7 @@ ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t 
                                const uint8_t* has_initial_state, struct CUstream_st* stream) {
   using namespace layer;
   ScanArgs p;
-  VarlenArgs a;
+  Seqs a;
   ssu_status st = check_scan(c, rows, false, &p);
   if (st == SSU_OK)
     st = check_prompts(c->state != nullptr, c->slots, nseqs, rows, cu_seqlens, meta_dtype,
@@ -233,7 +238,7 @@ ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t 
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
   p.final_only = 1;
-  return launched(launch_prompt(c, p, a, nseqs, (cudaStream_t)stream));
+  return launched(launch_prompt(c, p, a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -65,7 +65,7 @@ struct ScanStep {
 
 template <class ST, class IT, int N>
 __global__ void __launch_bounds__(kScanWarps * 32)
-    scan_step_kernel(const ScanArgs p, const VarlenArgs a, int64_t nseqs) {
+    scan_step_kernel(const ScanArgs p, const Seqs a) {
   using K = ScanStep<ST, N>;
   using L = typename K::L;
   constexpr int U = K::U;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kScanWarps * 32)
   const IT* Bp = static_cast<const IT*>(p.B);
   const IT* Cp = static_cast<const IT*>(p.Cm);
 
-  for (int64_t s = blockIdx.y; s < nseqs; s += gridDim.y) {
+  for (int s = blockIdx.y; s < a.n; s += gridDim.y) {
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
     const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
@@ -192,55 +192,55 @@ __global__ void __launch_bounds__(kScanWarps * 32)
 }
 
 template <class ST, class IT, int N>
-cudaError_t launch_scan_step(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_step(const ScanArgs& p, const Seqs& a,
                              cudaStream_t stream) {
   using K = ScanStep<ST, N>;
   const int64_t gx = (p.C + K::CH - 1) / K::CH;
   // eight CTAs an SM walk the sequences of one tile of channels each
   int64_t gy = (8LL * ssu::sm_count() + gx - 1) / gx;
-  if (gy > nseqs) gy = nseqs;
+  if (gy > a.n) gy = a.n;
   if (gy > 65535) gy = 65535;
   scan_step_kernel<ST, IT, N>
-      <<<dim3((unsigned)gx, (unsigned)gy), kScanWarps * 32, 0, stream>>>(p, a, nseqs);
+      <<<dim3((unsigned)gx, (unsigned)gy), kScanWarps * 32, 0, stream>>>(p, a);
   return cudaGetLastError();
 }
 
 template <class ST, class IT>
-cudaError_t launch_scan_n(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_n(int N, const ScanArgs& p, const Seqs& a,
                           cudaStream_t stream) {
   switch (N) {
-    case 16: return launch_scan_step<ST, IT, 16>(p, a, nseqs, stream);
-    case 32: return launch_scan_step<ST, IT, 32>(p, a, nseqs, stream);
-    case 64: return launch_scan_step<ST, IT, 64>(p, a, nseqs, stream);
-    case 128: return launch_scan_step<ST, IT, 128>(p, a, nseqs, stream);
-    case 256: return launch_scan_step<ST, IT, 256>(p, a, nseqs, stream);
+    case 16: return launch_scan_step<ST, IT, 16>(p, a, stream);
+    case 32: return launch_scan_step<ST, IT, 32>(p, a, stream);
+    case 64: return launch_scan_step<ST, IT, 64>(p, a, stream);
+    case 128: return launch_scan_step<ST, IT, 128>(p, a, stream);
+    case 256: return launch_scan_step<ST, IT, 256>(p, a, stream);
   }
   return cudaErrorInvalidValue;
 }
 
 template <class IT>
-cudaError_t launch_scan_io(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_io(int N, const ScanArgs& p, const Seqs& a,
                            cudaStream_t stream) {
   switch (p.state_dtype) {
-    case SSU_F32: return launch_scan_n<float, IT>(N, p, a, nseqs, stream);
-    case SSU_BF16: return launch_scan_n<__nv_bfloat16, IT>(N, p, a, nseqs, stream);
-    case SSU_F16: return launch_scan_n<__half, IT>(N, p, a, nseqs, stream);
+    case SSU_F32: return launch_scan_n<float, IT>(N, p, a, stream);
+    case SSU_BF16: return launch_scan_n<__nv_bfloat16, IT>(N, p, a, stream);
+    case SSU_F16: return launch_scan_n<__half, IT>(N, p, a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 // one translation unit for each element type of the rows
-cudaError_t launch_scan_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_f32(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
-cudaError_t launch_prompt_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_f32(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
-cudaError_t launch_scan_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_bf16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
-cudaError_t launch_prompt_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_bf16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
-cudaError_t launch_scan_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_f16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
-cudaError_t launch_prompt_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_f16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream);
 
 }  // namespace layer

@@ -3,15 +3,15 @@
 
 namespace layer {
 
-cudaError_t launch_scan_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_bf16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream) {
-  return launch_scan_io<__nv_bfloat16>(N, p, a, nseqs, stream);
+  return launch_scan_io<__nv_bfloat16>(N, p, a, stream);
 }
 
-cudaError_t launch_prompt_bf16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_bf16(int N, const ScanArgs& p, const Seqs& a,
                            cudaStream_t stream) {
-  if (!p.dt_f32) return launch_scan_prompt_n<__nv_bfloat16, __nv_bfloat16>(N, p, a, nseqs, stream);
-  return launch_scan_prompt_n<__nv_bfloat16, float>(N, p, a, nseqs, stream);
+  if (!p.dt_f32) return launch_scan_prompt_n<__nv_bfloat16, __nv_bfloat16>(N, p, a, stream);
+  return launch_scan_prompt_n<__nv_bfloat16, float>(N, p, a, stream);
 }
 
 }  // namespace layer

@@ -3,15 +3,15 @@
 
 namespace layer {
 
-cudaError_t launch_scan_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_f16(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream) {
-  return launch_scan_io<__half>(N, p, a, nseqs, stream);
+  return launch_scan_io<__half>(N, p, a, stream);
 }
 
-cudaError_t launch_prompt_f16(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_f16(int N, const ScanArgs& p, const Seqs& a,
                            cudaStream_t stream) {
-  if (!p.dt_f32) return launch_scan_prompt_n<__half, __half>(N, p, a, nseqs, stream);
-  return launch_scan_prompt_n<__half, float>(N, p, a, nseqs, stream);
+  if (!p.dt_f32) return launch_scan_prompt_n<__half, __half>(N, p, a, stream);
+  return launch_scan_prompt_n<__half, float>(N, p, a, stream);
 }
 
 }  // namespace layer

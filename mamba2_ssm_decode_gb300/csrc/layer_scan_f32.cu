@@ -3,14 +3,14 @@
 
 namespace layer {
 
-cudaError_t launch_scan_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_f32(int N, const ScanArgs& p, const Seqs& a,
                          cudaStream_t stream) {
-  return launch_scan_io<float>(N, p, a, nseqs, stream);
+  return launch_scan_io<float>(N, p, a, stream);
 }
 
-cudaError_t launch_prompt_f32(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_prompt_f32(int N, const ScanArgs& p, const Seqs& a,
                            cudaStream_t stream) {
-  return launch_scan_prompt_n<float, float>(N, p, a, nseqs, stream);
+  return launch_scan_prompt_n<float, float>(N, p, a, stream);
 }
 
 }  // namespace layer

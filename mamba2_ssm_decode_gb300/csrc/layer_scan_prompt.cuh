@@ -98,45 +98,6 @@ __device__ __forceinline__ void store_state4(const ScanArgs& p, int64_t at, floa
   else store_as4<__half>(p.state, at, a, b);
 }
 
-// V elements as stored, in 32-bit words.
-template <class T, int V>
-struct Words {
-  static constexpr int BYTES = V * (int)sizeof(T), NW = (BYTES + 3) / 4;
-  uint32_t w[NW];
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
-      return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-    else return __half2float(__ushort_as_half((unsigned short)(w[i >> 1] >> (i & 1 ? 16 : 0))));
-  }
-  __device__ __forceinline__ void load(const T* p) {  // from a multiple of 16 bytes, or of BYTES
-    if constexpr (BYTES % 16 == 0) {
-#pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-      }
-    } else if constexpr (BYTES == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    } else if constexpr (BYTES == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    }
-  }
-  __device__ __forceinline__ void load_some(const T* p, int n) {  // elements [0, n), zeros beyond
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) {
-        if constexpr (sizeof(T) == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-        else w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (i & 1 ? 16 : 0);
-      }
-  }
-};
-
 // V floats of shared memory
 template <int V>
 __device__ __forceinline__ void shared_floats(const float* p, float* f) {
@@ -200,16 +161,15 @@ struct PromptRows {
 };
 
 template <class T, int SV, bool FAST>
-__device__ __forceinline__ void store_row(T* o, const float* y, int n) {
-  Pack<T, SV> v;
-#pragma unroll
-  for (int i = 0; i < SV; ++i) v.v[i] = from_f<T>(y[i]);
+__device__ __forceinline__ void store_row(T* o, const float2* y, int n) {
   if constexpr (FAST) {
-    store_pack<T, SV>(o, v);
+    Words<T, SV> v;
+    v.set(y);
+    v.store(o);
   } else {
 #pragma unroll
     for (int i = 0; i < SV; ++i)
-      if (i < n) o[i] = v.v[i];
+      if (i < n) o[i] = from_f<T>(i & 1 ? y[i >> 1].y : y[i >> 1].x);
   }
 }
 
@@ -330,14 +290,19 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
     __syncthreads();
 
     if (OUT && in && rows.sn > 0) {
-      float y[SV], D[SV];
-      shared_floats<SV>(&sm.y[tr][s0], y);
+      constexpr int P = (SV + 1) / 2;
+      float f[2 * P], D[2 * P];
+      shared_floats<SV>(&sm.y[tr][s0], f);
       shared_floats<SV>(&sm.D[s0], D);
+      if (SV & 1) f[SV] = D[SV] = 0.0f;
+      float2 y[P];
 #pragma unroll
-      for (int i = 0; i < SV; ++i) y[i] = fmaf(D[i], xk.at(i), y[i]);
+      for (int i = 0; i < P; ++i)
+        y[i] = __ffma2_rn(make_float2(D[2 * i], D[2 * i + 1]), xk.pair(i),
+                          make_float2(f[2 * i], f[2 * i + 1]));
       if (p.z) {
 #pragma unroll
-        for (int i = 0; i < SV; ++i) y[i] *= silu(zk.at(i));
+        for (int i = 0; i < P; ++i) y[i] = __fmul2_rn(y[i], silu2(zk.pair(i)));
       }
       const int64_t o = (rt + tr) * p.o_rs + c0 + s0;
       if (p.out_f32) store_row<float, SV, FAST>(static_cast<float*>(p.out) + o, y, rows.sn);
@@ -388,7 +353,7 @@ __device__ __forceinline__ int64_t piece_start(int64_t tiles, int k, int K) {
 
 template <class IT, class DT, int N, int R, int NPT, bool SPLIT>
 __global__ void __launch_bounds__(kPromptThreads, 4)
-    scan_prompt_kernel(const ScanArgs p, const VarlenArgs a, int64_t nseqs, int K_) {
+    scan_prompt_kernel(const ScanArgs p, const Seqs a, int K_) {
   using K = PromptTile<N, R, NPT>;
   constexpr int LPC = K::LPC, TT = K::TT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -424,7 +389,7 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
   __syncthreads();
   const bool fast = p.rows_vec && cn % K::SV == 0;
 
-  for (int64_t s = blockIdx.y; s < nseqs; s += gridDim.y) {
+  for (int s = blockIdx.y; s < a.n; s += gridDim.y) {
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
     const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
@@ -521,7 +486,7 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
 }
 
 template <class IT, class DT, int N, int R, int NPT, bool SPLIT>
-cudaError_t launch_prompt_as(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs, int64_t tiles,
+cudaError_t launch_prompt_as(const ScanArgs& p, const Seqs& a, int64_t tiles,
                              int pieces, cudaStream_t stream) {
   using K = PromptTile<N, R, NPT>;
   auto kern = scan_prompt_kernel<IT, DT, N, R, NPT, SPLIT>;
@@ -532,7 +497,7 @@ cudaError_t launch_prompt_as(const ScanArgs& p, const VarlenArgs& a, int64_t nse
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * pieces), (unsigned)(nseqs < 65535 ? nseqs : 65535));
+  cfg.gridDim = dim3((unsigned)(tiles * pieces), (unsigned)(a.n < 65535 ? a.n : 65535));
   cfg.blockDim = dim3(kPromptThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -542,12 +507,12 @@ cudaError_t launch_prompt_as(const ScanArgs& p, const VarlenArgs& a, int64_t nse
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   cfg.attrs = &cluster;
   cfg.numAttrs = SPLIT ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, a, nseqs, pieces);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, a, pieces);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <class IT, class DT, int N, int R, int NPT>
-cudaError_t launch_scan_prompt(const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_prompt(const ScanArgs& p, const Seqs& a,
                                cudaStream_t stream) {
   using K = PromptTile<N, R, NPT>;
   const int per = p.C / p.G;
@@ -556,20 +521,20 @@ cudaError_t launch_scan_prompt(const ScanArgs& p, const VarlenArgs& a, int64_t n
   // fewer CTAs than SMs: 12289 x 5120 rows in one sequence, 80 CTAs, take 1014
   // us whole and 713 us in 8 pieces; 9001 x 4096 rows in 16 sequences, 1024
   // CTAs, 238 us whole and 390 us in pieces
-  if (tiles * nseqs < ssu::sm_count())
-    return launch_prompt_as<IT, DT, N, R, NPT, true>(p, a, nseqs, tiles, 8, stream);
-  return launch_prompt_as<IT, DT, N, R, NPT, false>(p, a, nseqs, tiles, 1, stream);
+  if (tiles * a.n < ssu::sm_count())
+    return launch_prompt_as<IT, DT, N, R, NPT, true>(p, a, tiles, 8, stream);
+  return launch_prompt_as<IT, DT, N, R, NPT, false>(p, a, tiles, 1, stream);
 }
 
 template <class IT, class DT>
-cudaError_t launch_scan_prompt_n(int N, const ScanArgs& p, const VarlenArgs& a, int64_t nseqs,
+cudaError_t launch_scan_prompt_n(int N, const ScanArgs& p, const Seqs& a,
                                  cudaStream_t stream) {
   switch (N) {
-    case 16: return launch_scan_prompt<IT, DT, 16, 2, 4>(p, a, nseqs, stream);
-    case 32: return launch_scan_prompt<IT, DT, 32, 2, 4>(p, a, nseqs, stream);
-    case 64: return launch_scan_prompt<IT, DT, 64, 2, 4>(p, a, nseqs, stream);
-    case 128: return launch_scan_prompt<IT, DT, 128, 2, 8>(p, a, nseqs, stream);
-    case 256: return launch_scan_prompt<IT, DT, 256, 2, 8>(p, a, nseqs, stream);
+    case 16: return launch_scan_prompt<IT, DT, 16, 2, 4>(p, a, stream);
+    case 32: return launch_scan_prompt<IT, DT, 32, 2, 4>(p, a, stream);
+    case 64: return launch_scan_prompt<IT, DT, 64, 2, 4>(p, a, stream);
+    case 128: return launch_scan_prompt<IT, DT, 128, 2, 8>(p, a, stream);
+    case 256: return launch_scan_prompt<IT, DT, 256, 2, 8>(p, a, stream);
   }
   return cudaErrorInvalidValue;
 }
