@@ -19,11 +19,15 @@ struct Pool {
 };
 
 // Pools by value in the launch's parameters: nothing has to be copied to the
-// device before the kernel, and nothing kept alive after the call.
+// device before the kernel, and nothing kept alive after the call.  Calls of a
+// few pools have a smaller list to hand over.
+constexpr int kFewPools = 16;
+
+template <int MOST>
 struct Pools {
-  Pool pool[kMaxPools];
-  int first[kMaxPools + 1];  // first chunk of each pool within a slot; the total at the end
-  uint32_t wide[(kMaxPools + 31) / 32];  // bit set: 16-byte accesses
+  Pool pool[MOST];
+  int first[MOST + 1];  // first chunk of each pool within a slot; the total at the end
+  uint32_t wide[(MOST + 31) / 32];  // bit set: 16-byte accesses
   int n;
   int64_t slots;
 };
@@ -52,8 +56,8 @@ __device__ __forceinline__ void move_bytes(uint8_t* dst, const uint8_t* src, int
 }
 
 // Chunk `chunk` of a slot: which pool's bytes, from where.
-template <Fill F>
-__device__ __forceinline__ void move_chunk(const Pools& ps, int chunk, int64_t from, int64_t to) {
+template <Fill F, int MOST>
+__device__ __forceinline__ void move_chunk(const Pools<MOST>& ps, int chunk, int64_t from, int64_t to) {
   int lo = 0, hi = ps.n - 1;  // the pool with first[lo] <= chunk < first[lo + 1]
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -74,28 +78,29 @@ __device__ __forceinline__ void move_chunk(const Pools& ps, int chunk, int64_t f
 
 // grid: x = pairs (several CTAs that copy the same piece of one source run side
 // by side, so a fork reads it from HBM once), y = chunks of a slot.
-template <Fill F>
+template <Fill F, int MOST>
 __global__ void __launch_bounds__(kCopyThreads)
-    slots_copy_kernel(const __grid_constant__ Pools ps, const void* src, const void* dst,
+    slots_copy_kernel(const __grid_constant__ Pools<MOST> ps, const void* src, const void* dst,
                       int idx64, int64_t pad) {
   const int64_t to = load_int(dst, blockIdx.x, idx64);
   const int64_t from = F == Fill::kCopy ? load_int(src, blockIdx.x, idx64) : to;
   if (!slot_ok(to, pad, ps.slots) || !slot_ok(from, pad, ps.slots)) return;
   if (F == Fill::kCopy && from == to) return;
   for (int chunk = blockIdx.y; chunk < ps.first[ps.n]; chunk += gridDim.y)
-    move_chunk<F>(ps, chunk, from, to);
+    move_chunk<F, MOST>(ps, chunk, from, to);
 }
 
 // The moves of a compaction, listed on the device: as many CTAs as fit walk
 // them, the pieces of one slot side by side.
+template <int MOST>
 __global__ void __launch_bounds__(kCopyThreads)
-    slots_move_kernel(const __grid_constant__ Pools ps, const int* moves, const int* src,
+    slots_move_kernel(const __grid_constant__ Pools<MOST> ps, const int* moves, const int* src,
                       const int* dst) {
   const int64_t chunks = ps.first[ps.n];
   const int64_t items = *moves * chunks;
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int64_t m = i / chunks;
-    move_chunk<Fill::kCopy>(ps, (int)(i - m * chunks), src[m], dst[m]);
+    move_chunk<Fill::kCopy, MOST>(ps, (int)(i - m * chunks), src[m], dst[m]);
   }
 }
 
@@ -174,14 +179,15 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
 }
 
-static ssu_status check_pools(const ssu_pool* pools, int npools, int64_t slots, Pools* ps) {
+template <int MOST>
+static ssu_status check_pools(const ssu_pool* pools, int npools, int64_t slots, Pools<MOST>* ps) {
   if (npools < 0 || slots < 0)
     return fail(SSU_ERR_INVALID_ARGUMENT, "npools and slots must be >= 0");
   if (npools > kMaxPools)
     return fail(SSU_ERR_UNSUPPORTED, "at most %d pools per call, got %d", kMaxPools, npools);
   if (slots > (1 << 20)) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
   if (npools > 0 && !pools) return fail(SSU_ERR_INVALID_ARGUMENT, "pools must not be NULL");
-  *ps = Pools{};
+  *ps = Pools<MOST>{};
   int64_t chunks = 0;
   int n = 0;
   for (int i = 0; i < npools; ++i) {
@@ -207,11 +213,11 @@ static ssu_status check_pools(const ssu_pool* pools, int npools, int64_t slots, 
   return SSU_OK;
 }
 
-template <Fill F>
-static ssu_status move_slots(const ssu_pool* pools, int npools, int64_t slots, const void* src,
+template <Fill F, int MOST>
+static ssu_status move_slots_as(const ssu_pool* pools, int npools, int64_t slots, const void* src,
                              const void* dst, ssu_dtype index_dtype, int64_t pairs, int64_t pad,
                              cudaStream_t stream) {
-  Pools ps;
+  Pools<MOST> ps;
   ssu_status st = check_pools(pools, npools, slots, &ps);
   if (st != SSU_OK) return st;
   if (!is_index(index_dtype))
@@ -223,12 +229,69 @@ static ssu_status move_slots(const ssu_pool* pools, int npools, int64_t slots, c
   if (pairs == 0 || ps.n == 0) return ok();
   const int chunks = ps.first[ps.n];
   const dim3 grid((unsigned)pairs, (unsigned)(chunks < 65535 ? chunks : 65535));
-  slots_copy_kernel<F><<<grid, kCopyThreads, 0, stream>>>(ps, src, dst, index_dtype == SSU_I64,
+  slots_copy_kernel<F, MOST><<<grid, kCopyThreads, 0, stream>>>(ps, src, dst, index_dtype == SSU_I64,
                                                          pad);
   return launched(cudaGetLastError());
 }
 
+template <Fill F>
+static ssu_status move_slots(const ssu_pool* pools, int npools, int64_t slots, const void* src,
+                             const void* dst, ssu_dtype index_dtype, int64_t pairs, int64_t pad,
+                             cudaStream_t stream) {
+  return npools <= kFewPools ? move_slots_as<F, kFewPools>(pools, npools, slots, src, dst,
+                                                           index_dtype, pairs, pad, stream)
+                             : move_slots_as<F, kMaxPools>(pools, npools, slots, src, dst,
+                                                           index_dtype, pairs, pad, stream);
+}
+
 static int plan_smem(int64_t slots) { return (int)((slots + 63) / 64 * 12); }
+
+static int64_t workspace_bytes_of(int64_t slots) {
+  // the number of moves, and the two slots of each (at most half the pool moves)
+  return slots < 0 ? -1 : 16 + 2 * 4 * ((slots + 1) / 2);
+}
+
+template <int MOST>
+static ssu_status compact_as(const ssu_pool* pools, int npools, int64_t slots, const void* table,
+                             void* table_out, ssu_dtype index_dtype, int64_t entries,
+                             int64_t pad_slot_id, int32_t* num_live, void* workspace,
+                             int64_t workspace_bytes, cudaStream_t stream) {
+  Pools<MOST> ps;
+  ssu_status st = check_pools(pools, npools, slots, &ps);
+  if (st != SSU_OK) return st;
+  if (!is_index(index_dtype))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "the slot table must be int32 or int64");
+  if (entries < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "entries must be >= 0");
+  if ((entries > 0 && (!table || !table_out)) || !num_live)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "table, table_out and num_live must not be NULL");
+  const int64_t need = workspace_bytes_of(slots);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(SSU_ERR_INVALID_ARGUMENT,
+                "ssu_slots_compact needs a 16-byte aligned workspace of %lld bytes, got %lld",
+                (long long)need, (long long)workspace_bytes);
+  int* moves = static_cast<int*>(workspace);
+  int* src = moves + 4;
+  int* dst = src + (slots + 1) / 2;
+  const int smem = plan_smem(slots);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) {
+    e = cudaFuncSetAttribute(slots_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launched(e);
+  }
+  slots_plan_kernel<<<1, kPlanThreads, smem, stream>>>(
+      table, table_out, index_dtype == SSU_I64, entries, pad_slot_id, (int)slots, num_live, moves,
+      src, dst);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ps.n == 0) return launched(e);
+  // at most half the slots move, and no more than the table has entries
+  const int64_t most = slots / 2 < entries ? slots / 2 : entries;
+  const int64_t items = most * ps.first[ps.n];
+  if (items == 0) return ok();
+  const int64_t fit = 8LL * ssu::sm_count();
+  slots_move_kernel<MOST><<<(unsigned)(items < fit ? items : fit), kCopyThreads, 0,
+                      stream>>>(ps, moves, src, dst);
+  return launched(cudaGetLastError());
+}
 
 }  // namespace layer
 
@@ -250,8 +313,7 @@ ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, con
 }
 
 int64_t ssu_slots_compact_workspace_bytes(int64_t slots) {
-  // the number of moves, and the two slots of each (at most half the pool moves)
-  return slots < 0 ? -1 : 16 + 2 * 4 * ((slots + 1) / 2);
+  return layer::workspace_bytes_of(slots);
 }
 
 ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, const void* table,
@@ -259,39 +321,9 @@ ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, c
                              int64_t pad_slot_id, int32_t* num_live, void* workspace,
                              int64_t workspace_bytes, struct CUstream_st* stream) {
   using namespace layer;
-  Pools ps;
-  ssu_status st = check_pools(pools, npools, slots, &ps);
-  if (st != SSU_OK) return st;
-  if (!is_index(index_dtype))
-    return fail(SSU_ERR_INVALID_ARGUMENT, "the slot table must be int32 or int64");
-  if (entries < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "entries must be >= 0");
-  if ((entries > 0 && (!table || !table_out)) || !num_live)
-    return fail(SSU_ERR_INVALID_ARGUMENT, "table, table_out and num_live must not be NULL");
-  const int64_t need = ssu_slots_compact_workspace_bytes(slots);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
-    return fail(SSU_ERR_INVALID_ARGUMENT,
-                "ssu_slots_compact needs a 16-byte aligned workspace of %lld bytes, got %lld",
-                (long long)need, (long long)workspace_bytes);
-  int* moves = static_cast<int*>(workspace);
-  int* src = moves + 4;
-  int* dst = src + (slots + 1) / 2;
-  const int smem = plan_smem(slots);
-  cudaError_t e = cudaFuncSetAttribute(slots_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return launched(e);
-  slots_plan_kernel<<<1, kPlanThreads, smem, (cudaStream_t)stream>>>(
-      table, table_out, index_dtype == SSU_I64, entries, pad_slot_id, (int)slots, num_live, moves,
-      src, dst);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || ps.n == 0) return launched(e);
-  // at most half the slots move, and no more than the table has entries
-  const int64_t most = slots / 2 < entries ? slots / 2 : entries;
-  const int64_t items = most * ps.first[ps.n];
-  if (items == 0) return ok();
-  const int64_t fit = 8LL * ssu::sm_count();
-  slots_move_kernel<<<(unsigned)(items < fit ? items : fit), kCopyThreads, 0,
-                      (cudaStream_t)stream>>>(ps, moves, src, dst);
-  return launched(cudaGetLastError());
+  auto f = npools <= kFewPools ? compact_as<kFewPools> : compact_as<kMaxPools>;
+  return f(pools, npools, slots, table, table_out, index_dtype, entries, pad_slot_id, num_live,
+           workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
 }  // extern "C"
