@@ -639,12 +639,14 @@ ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, con
  * not slots, and a slot may be entered more than once).  With m of them, those
  * with ids below m stay; the k-th live slot at or beyond m (in ascending
  * order) moves to the k-th free slot below m, in every pool; *num_live = m and
- * table_out (may be table) holds the entries under their new ids, others
+ * table_out holds the entries under their new ids, others
  * unchanged.  Slots from m on are free afterwards; their bytes are left.
  *   workspace  device memory of ssu_slots_compact_workspace_bytes(slots) bytes
  *              (-1 for a negative size), 16-byte aligned; nothing in it need
  *              be kept between calls.
- * Two launches; the host learns num_live only if it reads it.
+ * table_out may be table or must not overlap it.  One launch (two for pools of
+ * more than 4096 slots, tables of more than 8192 entries and tables rewritten
+ * in place); the host learns num_live only if it reads it.
  */
 int64_t ssu_slots_compact_workspace_bytes(int64_t slots);
 

@@ -235,42 +235,58 @@ __device__ __forceinline__ float2 silu2(float2 v) {
   return __fmul2_rn(v, r);
 }
 
-// softplus(a + b) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|), v = a + b, for
-// two values at once (the packed fp32 pipe).  Far below zero the result is e^v
-// itself, which turns an error of v into a relative one: so the exponent's
-// product with log2 e is carried in two parts (Dekker), what the sum a + b lost
-// (Knuth's two-sum) is put back, and e^(v + d) = e^v (1 + d) to first order.
-// log1p(u) = u P(u) on [0, 1], P the degree 8 least-maximum fit of log1p(u) / u
-// (relative error 1.8e-7 in fp32).  NaN comes through `lost`; infinities have
-// none.
-__device__ __forceinline__ float2 softplus_sum2(float2 a, float2 b) {
-  const float2 minus = make_float2(-1.0f, -1.0f);
-  const float2 v = __fadd2_rn(a, b);
-  const float2 part = __ffma2_rn(a, minus, v);
-  float2 lost = __fadd2_rn(__ffma2_rn(__ffma2_rn(part, minus, v), minus, a),
-                           __ffma2_rn(part, minus, b));
-  if (fabsf(v.x) == INFINITY) lost.x = 0.0f;
-  if (fabsf(v.y) == INFINITY) lost.y = 0.0f;
-  // below -150 the exponential is zero in fp32
-  const float2 m = make_float2(fmaxf(-fabsf(v.x), -150.0f), fmaxf(-fabsf(v.y), -150.0f));
-  const float2 l2e = make_float2(1.44269502e+0f, 1.44269502e+0f);
-  const float2 hi = __fmul2_rn(m, l2e);
-  float2 d = __ffma2_rn(m, l2e, __fmul2_rn(hi, minus));
-  d = __ffma2_rn(m, make_float2(1.92596299e-8f, 1.92596299e-8f), d);  // log2 e - l2e
-  d = __ffma2_rn(d, make_float2(0.693147181f, 0.693147181f), lost);
-  float2 u = make_float2(ex2(hi.x), ex2(hi.y));
-  u = __ffma2_rn(u, d, u);
-  constexpr float P[9] = {0.9999999403953552f, -0.4999949336051941f, 0.3331909775733948f,
-                          -0.2484298199415207f, 0.19106005132198334f, -0.13663242757320404f,
-                          0.07822591066360474f, -0.029505213722586632f, 0.0052326880395412445f};
-  float2 l = make_float2(P[8], P[8]);
-#pragma unroll
-  for (int i = 7; i >= 0; --i) l = __ffma2_rn(l, u, make_float2(P[i], P[i]));
-  return __ffma2_rn(l, u, make_float2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)));
+// softplus(a + b) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|), v = a + b.  Far
+// below zero the result is e^v itself, which turns an error of v into a
+// relative one: so the exponent's product with log2 e is carried in two parts
+// (Dekker), what the sum a + b lost (Knuth's two-sum) is put back, and e^(v + d)
+// = e^v (1 + d) to first order.  log1p(u) = u P(u) on [0, 1], P the degree 8
+// least-maximum fit of log1p(u) / u (relative error 1.8e-7 in fp32).  NaN comes
+// through `lost`; infinities have none.
+__device__ __forceinline__ float softplus_from(float v, float lost) {
+  const float m = fmaxf(-fabsf(v), -150.0f);  // below, the exponential is zero in fp32
+  const float hi = m * kLog2e;
+  float d = fmaf(m, kLog2e, -hi);
+  d = fmaf(m, 1.92596299e-8f, d);  // log2 e - kLog2e
+  d = fmaf(d, 0.693147181f, lost);
+  float u = ex2(hi);
+  u = fmaf(u, d, u);
+  float l = 0.0052326880395412445f;
+  l = fmaf(l, u, -0.029505213722586632f);
+  l = fmaf(l, u, 0.07822591066360474f);
+  l = fmaf(l, u, -0.13663242757320404f);
+  l = fmaf(l, u, 0.19106005132198334f);
+  l = fmaf(l, u, -0.2484298199415207f);
+  l = fmaf(l, u, 0.3331909775733948f);
+  l = fmaf(l, u, -0.4999949336051941f);
+  l = fmaf(l, u, 0.9999999403953552f);
+  return fmaf(l, u, fmaxf(v, 0.0f));
 }
 
 __device__ __forceinline__ float softplus_sum(float a, float b) {
-  return softplus_sum2(make_float2(a, a), make_float2(b, b)).x;
+  const float v = a + b;
+  const float part = v - a;
+  const float lost = (a - (v - part)) + (b - part);
+  return softplus_from(v, fabsf(v) == INFINITY ? 0.0f : lost);
+}
+
+// ... of V sums at once.  What a sum lost is below 2^-21 of the result unless v
+// is below -16 (or not finite): then all are done with it.
+template <int V>
+__device__ __forceinline__ void softplus_sums(float* a, const float* b) {
+  float v[V];
+  bool near = true;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = a[i] + b[i];
+    near = near && v[i] > -16.0f;
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = softplus_from(v[i], 0.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = softplus_sum(a[i], b[i]);
+  }
 }
 
 // ---------------------------------------------------------------------------

@@ -33,10 +33,23 @@ struct PromptTile {
   static constexpr int TG = LPC < 8 ? LPC : 8;               // rows whose sums are reduced together
   static constexpr int YS = CH + 32 / TG;                    // row stride of the sums
   static constexpr int CPW = 32 / LPC;                       // lane groups per warp
+
+  // A staging thread owns SV neighbouring channels and moves them to and from
+  // shared memory four at a time.  With SV = 8 a row there holds the first
+  // halves of all threads' channels, then the second: threads side by side are
+  // then 16 bytes apart, on distinct banks, where 32 would collide.  The
+  // channel at place i of a row, and the place of a thread's f-th four:
+  __device__ static __forceinline__ int channel(int i) {
+    return SV == 8 ? i % (CH / 2) / 4 * 8 + i / (CH / 2) * 4 + i % 4 : i;
+  }
+  __device__ static __forceinline__ int place(int thread, int f) {
+    return SV == 8 ? f * (CH / 2) + thread * 4 : thread * SV + f * 4;
+  }
 };
 
 template <class K, int N>
 struct alignas(16) PromptSmem {
+  // rows of channels in the order of K::channel
   float d[K::TT][K::CH];    // dt'
   float dx[K::TT][K::CH];   // dt' x
   float B[K::TT][N];
@@ -98,18 +111,31 @@ __device__ __forceinline__ void store_state4(const ScanArgs& p, int64_t at, floa
   else store_as4<__half>(p.state, at, a, b);
 }
 
-// V floats of shared memory
-template <int V>
-__device__ __forceinline__ void shared_floats(const float* p, float* f) {
-  if constexpr (V % 4 == 0) {
+// A staging thread's channels in a row of shared memory
+template <class K>
+__device__ __forceinline__ void from_row(const float* row, int thread, float* f) {
+  if constexpr (K::SV % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 v = reinterpret_cast<const float4*>(p)[i];
+    for (int i = 0; i < K::SV / 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(row + K::place(thread, i));
       f[4 * i] = v.x, f[4 * i + 1] = v.y, f[4 * i + 2] = v.z, f[4 * i + 3] = v.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = p[i];
+    for (int i = 0; i < K::SV; ++i) f[i] = row[thread * K::SV + i];
+  }
+}
+
+template <class K>
+__device__ __forceinline__ void to_row(float* row, int thread, const float* f) {
+  if constexpr (K::SV % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < K::SV / 4; ++i)
+      *reinterpret_cast<float4*>(row + K::place(thread, i)) =
+          make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < K::SV; ++i) row[thread * K::SV + i] = f[i];
   }
 }
 
@@ -140,17 +166,17 @@ struct PromptRows {
   const DT* dp;
   int sn;  // the thread's channels
 
-  // row r of [r0, r_end)
-  __device__ __forceinline__ void load(const ScanArgs& p, int64_t r, int64_t r_end) {
+  // row rt + tr, below r_end
+  __device__ __forceinline__ void load(const ScanArgs& p, int rt, int tr, int r_end) {
+    const bool in = tr < r_end - rt;
+    const int r = in ? rt + tr : r_end - 1;  // beyond: staged as a step that changes nothing
     if constexpr (FAST) {
-      if (r >= r_end) r = r_end - 1;  // staged as a step that changes nothing
       x.load(xp + r * p.x_rs);
       if (OUT && p.z) z.load(zp + r * p.z_rs);
       dt.load(dp + r * p.dt_rs);
       B.load(Bp + r * p.B_rs);
       if (OUT) C.load(Cp + r * p.C_rs);
     } else {
-      const bool in = r < r_end;
       x.load_some(xp + r * p.x_rs, in ? sn : 0);
       if (OUT && p.z) z.load_some(zp + r * p.z_rs, in ? sn : 0);
       dt.load_some(dp + r * p.dt_rs, in ? sn : 0);
@@ -178,7 +204,7 @@ __device__ __forceinline__ void store_row(T* o, const float2* y, int n) {
 template <class IT, class DT, int N, int R, int NPT, bool FAST, bool OUT>
 __device__ __forceinline__ void scan_rows(const ScanArgs& p,
                                           PromptSmem<PromptTile<N, R, NPT>, N>& sm, int g, int c0,
-                                          int cn, int64_t r0, int64_t r_end,
+                                          int cn, int r0, int r_end,
                                           const float2 (&A2)[R][NPT / 2],
                                           float2 (&h)[R][NPT / 2], float (&dsum)[R]) {
   using K = PromptTile<N, R, NPT>;
@@ -202,29 +228,32 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
   rows.dp = static_cast<const DT*>(p.dt) + cs;
   rows.Bp = static_cast<const IT*>(p.B) + g * p.B_gs + b0;
   rows.Cp = static_cast<const IT*>(p.Cm) + g * p.C_gs + b0;
-  rows.load(p, r0 + tr, r_end);
+  rows.load(p, r0, tr, r_end);
 
-  for (int64_t rt = r0; rt < r_end; rt += TT) {
-    const int n = r_end - rt < TT ? (int)(r_end - rt) : TT;
+  for (int rt = r0; rt < r_end; rt += TT) {
+    const int n = r_end - rt < TT ? r_end - rt : TT;
     const bool in = tr < n;
     const Words<IT, SV> xk = rows.x, zk = rows.z;
     // rows beyond the sequence get dt' = 0 and zeros: a step that changes nothing
     if (s0 < K::CH) {
       float bias[SV], d[SV], dx[SV];
-      shared_floats<SV>(&sm.bias[s0], bias);
+      from_row<K>(sm.bias, tp, bias);
 #pragma unroll
-      for (int i = 0; i < SV; i += 2) {
-        const int k = i + 1 < SV ? i + 1 : i;
-        float2 v = make_float2(rows.dt.at(i), rows.dt.at(k));
-        const float2 bi = make_float2(bias[i], bias[k]);
-        v = p.softplus ? softplus_sum2(v, bi) : __fadd2_rn(v, bi);
-        float2 vx = __fmul2_rn(v, make_float2(xk.at(i), xk.at(k)));
-        if (!in) v = vx = make_float2(0.0f, 0.0f);
-        d[i] = v.x, d[k] = k > i ? v.y : v.x;
-        dx[i] = vx.x, dx[k] = k > i ? vx.y : vx.x;
+      for (int i = 0; i < SV; ++i) d[i] = rows.dt.at(i);
+      if (p.softplus) {
+        softplus_sums<SV>(d, bias);
+      } else {
+#pragma unroll
+        for (int i = 0; i < SV; ++i) d[i] += bias[i];
       }
-      to_shared<SV>(&sm.d[tr][s0], d);
-      to_shared<SV>(&sm.dx[tr][s0], dx);
+#pragma unroll
+      for (int i = 0; i < SV; ++i) dx[i] = d[i] * xk.at(i);
+      if (!in) {
+#pragma unroll
+        for (int i = 0; i < SV; ++i) d[i] = dx[i] = 0.0f;
+      }
+      to_row<K>(sm.d[tr], tp, d);
+      to_row<K>(sm.dx[tr], tp, dx);
     }
     {
       float f[BV];
@@ -238,7 +267,7 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
       }
     }
     __syncthreads();
-    if (rt + TT < r_end) rows.load(p, rt + TT + tr, r_end);
+    if (r_end - rt > TT) rows.load(p, rt + TT, tr, r_end);
 
     for (int t = 0; t < n; t += TG * UG) {
 #pragma unroll
@@ -292,8 +321,8 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
     if (OUT && in && rows.sn > 0) {
       constexpr int P = (SV + 1) / 2;
       float f[2 * P], D[2 * P];
-      shared_floats<SV>(&sm.y[tr][s0], f);
-      shared_floats<SV>(&sm.D[s0], D);
+      from_row<K>(sm.y[tr], tp, f);
+      from_row<K>(sm.D, tp, D);
       if (SV & 1) f[SV] = D[SV] = 0.0f;
       float2 y[P];
 #pragma unroll
@@ -304,7 +333,7 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
 #pragma unroll
         for (int i = 0; i < P; ++i) y[i] = __fmul2_rn(y[i], silu2(zk.pair(i)));
       }
-      const int64_t o = (rt + tr) * p.o_rs + c0 + s0;
+      const int64_t o = (int64_t)(rt + tr) * p.o_rs + c0 + s0;
       if (p.out_f32) store_row<float, SV, FAST>(static_cast<float*>(p.out) + o, y, rows.sn);
       else store_row<IT, SV, FAST>(static_cast<IT*>(p.out) + o, y, rows.sn);
     }
@@ -343,12 +372,39 @@ struct PromptPiece {
   float dsum[R][kPromptThreads];
 };
 
+constexpr int kMostPieces = 16, kLeastPieces = 4;
+constexpr int kPieceTiles = 3;  // tiles of rows that a piece has at least
+
 // First row of piece k of K, in tiles: the first piece is shorter by the work
 // that the others do twice (a pass without outputs costs about 0.7 of one with).
-__device__ __forceinline__ int64_t piece_start(int64_t tiles, int k, int K) {
+__device__ __forceinline__ int piece_start(int tiles, int k, int K) {
   if (k == 0) return 0;
   if (k == K) return tiles;
-  return (int64_t)(((k - 1) + 0.7f) / ((K - 1) + 0.7f) * (float)tiles);
+  return (int)(((k - 1) + 0.7f) / ((K - 1) + 0.7f) * (float)tiles);
+}
+
+// CTAs start in the order of their index: with the longest sequences first the
+// short ones fill the gaps that they leave at the end (16 sequences of 300 to
+// 900 rows x 4096 channels, 1.7 waves: 236 us in the
+// order given, 203 us so).  The sequence of rank `rank`
+// by length, where there are at most kRanked.
+constexpr int kRanked = 128;
+
+__device__ __forceinline__ int by_length(const Seqs& a, int rank, int* lens) {
+  static_assert(kRanked == kPromptThreads, "a thread per sequence");
+  const int i = threadIdx.x;
+  if (i < a.n) {
+    const RawIndex b = load_index(a.cu, i, a.meta64), e = load_index(a.cu, i + 1, a.meta64);
+    lens[i] = clamped(e.value(a.meta64), a.rows) - clamped(b.value(a.meta64), a.rows);
+  }
+  __syncthreads();
+  int before = 0;
+  if (i < a.n)
+    for (int j = 0; j < a.n; ++j) before += lens[j] > lens[i] || (lens[j] == lens[i] && j < i);
+  __shared__ int pick;
+  if (i < a.n && before == rank) pick = i;
+  __syncthreads();
+  return pick;
 }
 
 template <class IT, class DT, int N, int R, int NPT, bool SPLIT>
@@ -368,11 +424,11 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
   const int c0 = g * per + (tile - g * tiles) * K::CH;
   const int cn = (g + 1) * per - c0;                      // channels from c0 to the group's end
   const int q = (tid & 31) / K::CPW;                      // which of a channel's lanes
-  const int ch = tid / 32 * K::CPW + (tid & 31) % K::CPW;  // channels c0 + ch + k LG, k < R
+  const int ch = tid / 32 * K::CPW + (tid & 31) % K::CPW;  // places ch + k LG, k < R
   float2 A2[R][NPT / 2];                                  // columns (j LPC + q) 4 + i; A log2 e
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    const int c = ch + k * K::LG;
+    const int c = K::channel(ch + k * K::LG);
 #pragma unroll
     for (int j = 0; j < NPT / 4; ++j) {
       float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -382,25 +438,37 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
       A2[k][2 * j + 1] = make_float2(f[2] * kLog2e, f[3] * kLog2e);
     }
   }
-  for (int c = tid; c < K::CH; c += kPromptThreads) {
-    sm.D[c] = p.D && c < cn ? p.D[c0 + c] : 0.0f;
-    sm.bias[c] = p.bias && c < cn ? p.bias[c0 + c] : 0.0f;
+  for (int i = tid; i < K::CH; i += kPromptThreads) {
+    const int c = K::channel(i);
+    sm.D[i] = p.D && c < cn ? p.D[c0 + c] : 0.0f;
+    sm.bias[i] = p.bias && c < cn ? p.bias[c0 + c] : 0.0f;
   }
   __syncthreads();
   const bool fast = p.rows_vec && cn % K::SV == 0;
 
-  for (int s = blockIdx.y; s < a.n; s += gridDim.y) {
+  const bool ranked = !SPLIT && a.n > 1 && a.n <= kRanked;
+  for (int y = blockIdx.y; y < a.n; y += gridDim.y) {
+    const int s = ranked ? by_length(a, y, reinterpret_cast<int*>(sm.d)) : y;
     const Item it = packed_item(a, s, p.pad, p.slots);
     if (it.len == 0) continue;
     const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
-    // a sequence of few tiles is left whole to the cluster's first CTA
-    const int64_t row_tiles = (it.len + TT - 1) / TT;
-    const bool split = SPLIT && row_tiles >= 4 * pieces;
+    // a shorter sequence has fewer pieces; one of few tiles is left whole to the
+    // cluster's first CTA
+    const int row_tiles = (it.len + TT - 1) / TT;
+    const int use = row_tiles / kPieceTiles < pieces ? row_tiles / kPieceTiles : pieces;
+    const bool split = SPLIT && use >= kLeastPieces;
     if (SPLIT && !split && rank > 0) continue;
-    int64_t r0 = it.r0, r_end = it.r0 + it.len;
+    if (SPLIT && split && rank >= use) {  // no piece: only the cluster's two barriers
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+      continue;
+    }
+    int r0 = it.r0, r_end = it.r0 + it.len;
     if (split) {
-      if (rank < pieces - 1) r_end = r0 + piece_start(row_tiles, rank + 1, pieces) * TT;
-      r0 += piece_start(row_tiles, rank, pieces) * TT;
+      if (rank < use - 1) r_end = r0 + piece_start(row_tiles, rank + 1, use) * TT;
+      r0 += piece_start(row_tiles, rank, use) * TT;
     }
     float2 h[R][NPT / 2];
     float dsum[R];
@@ -410,7 +478,7 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
 #pragma unroll
       for (int j = 0; j < NPT / 4; ++j) {
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const int c = ch + k * K::LG;
+        const int c = K::channel(ch + k * K::LG);
         if (from && c < cn && rank == 0)
           v = load_state4(p, (it.src * p.C + c0 + c) * N + (j * LPC + q) * 4);
         h[k][2 * j] = make_float2(v.x, v.y);
@@ -424,9 +492,9 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
     };
     if constexpr (SPLIT) {
       if (split) {
-        if (rank > 0 && rank < pieces - 1) rows(std::false_type{});
+        if (rank > 0 && rank < use - 1) rows(std::false_type{});
         if (rank == 0) rows(std::true_type{});
-        if (rank < pieces - 1) {
+        if (rank < use - 1) {
 #pragma unroll
           for (int k = 0; k < R; ++k) {
             piece.dsum[k][tid] = dsum[k];
@@ -470,13 +538,13 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
       rows(std::true_type{});
     }
     int64_t slot;
-    if ((!split || rank == pieces - 1) && it.read_ok && !p.disable &&
+    if ((!split || rank == use - 1) && it.read_ok && !p.disable &&
         write_slot(a, s, 0, p.pad, p.slots, &slot)) {
 #pragma unroll
       for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int j = 0; j < NPT / 4; ++j) {
-          const int c = ch + k * K::LG;
+          const int c = K::channel(ch + k * K::LG);
           if (c < cn)
             store_state4(p, (slot * p.C + c0 + c) * N + (j * LPC + q) * 4, h[k][2 * j],
                          h[k][2 * j + 1]);
@@ -494,6 +562,11 @@ cudaError_t launch_prompt_as(const ScanArgs& p, const Seqs& a, int64_t tiles,
   if (smem > 48 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  if (pieces > 8) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -518,11 +591,16 @@ cudaError_t launch_scan_prompt(const ScanArgs& p, const Seqs& a,
   const int per = p.C / p.G;
   const int64_t tiles = (int64_t)p.G * ((per + K::CH - 1) / K::CH);
   if (tiles * 8 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // fewer CTAs than SMs: 12289 x 5120 rows in one sequence, 80 CTAs, take 1014
-  // us whole and 713 us in 8 pieces; 9001 x 4096 rows in 16 sequences, 1024
-  // CTAs, 238 us whole and 390 us in pieces
-  if (tiles * a.n < ssu::sm_count())
-    return launch_prompt_as<IT, DT, N, R, NPT, true>(p, a, tiles, 8, stream);
+  // Pieces while they fit in one wave of four CTAs an SM (12289 rows in one
+  // sequence: 5120 channels, 80 CTAs whole 1014 us, in 4 pieces 812, 7 pieces
+  // 592, 8 pieces, which do not fit, 660; 1536 channels in 8 pieces 312 us, 16
+  // pieces 253).  Three gain little (12000 rows x 5120 channels in two sequences
+  // 722 us for 740 whole), and a piece takes a few tiles to pay for the barriers
+  // (512 rows x 5120: 35 us in 16 pieces of 2 tiles, 54 us in 4 of 8).
+  const int64_t fit = 4LL * ssu::sm_count() / (tiles * a.n);
+  const int pieces = fit < kMostPieces ? (int)fit : kMostPieces;
+  if (pieces >= kLeastPieces && a.rows / a.n >= kLeastPieces * kPieceTiles * K::TT)
+    return launch_prompt_as<IT, DT, N, R, NPT, true>(p, a, tiles, pieces, stream);
   return launch_prompt_as<IT, DT, N, R, NPT, false>(p, a, tiles, 1, stream);
 }
 

@@ -632,7 +632,9 @@ def test_each_call_is_its_stated_launches():
     assert graph_kernel_nodes(lambda: ssu.slots_copy([pool, cp], t[:1], t[1:])) == 1
     assert graph_kernel_nodes(lambda: ssu.slots_clear([pool, cp], t)) == 1
     assert graph_kernel_nodes(
-        lambda: ssu.slots_compact([pool, cp], t, out=to, num_live=n, workspace=ws)) == 2
+        lambda: ssu.slots_compact([pool, cp], t, out=to, num_live=n, workspace=ws)) == 1
+    assert graph_kernel_nodes(
+        lambda: ssu.slots_compact([pool, cp], t, out=t, num_live=n, workspace=ws)) == 2   # in place
 
 
 def test_calls_run_on_the_given_stream():
