@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libssu_gb300.so")
@@ -128,13 +127,6 @@ class Pool(ctypes.Structure):
 SLOTS_MAX_POOLS = 256   # SSU_SLOTS_MAX_POOLS
 
 
-def packer(cls):
-    """``pack`` of a struct.Struct with the layout of a ctypes Structure: its
-    fields in order, as bytes (several times quicker than setting them)."""
-    code = {_c_p: "P", _c_i64: "q", _c_int: "i", _c_i32: "i"}
-    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
-
-
 _lock = threading.Lock()
 _lib = None
 
@@ -168,7 +160,7 @@ def lib() -> ctypes.CDLL:
         L.ssd_workspace_bytes.argtypes = [_c_i64] * 6
         L.ssd_combined_fwd_varlen.restype = _c_int
         L.ssd_combined_fwd_varlen.argtypes = [ctypes.POINTER(SSDParams), _c_p, _c_i64, _c_p]
-        # structs of these calls are passed by address: a ctypes one, or its packed bytes
+        # structs of these calls are passed by address
         decode = [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_int, _c_p, _c_p, _c_int, _c_p]
         prompt = [_c_p, _c_i64, _c_i64, _c_p, _c_int, _c_p, _c_p, _c_int, _c_p, _c_p]
         for name, args in (("ssu_conv_update", decode), ("ssu_conv_fwd_varlen", prompt),

@@ -3,6 +3,8 @@
 Each translation unit under csrc/ is compiled by nvcc in parallel into
 _build/, then linked into mamba2_ssm_decode_gb300/libssu_gb300.so.  No cmake,
 no torch extension machinery: the library is plain C ABI (include/ssu.h).
+The argument checks of the layer calls are a small CPython module beside it
+(_layer_binding.so, csrc/layer_binding.cpp: g++ with torch's headers).
 
     python -m mamba2_ssm_decode_gb300.build [--force] [--ptxas-info]
 """
@@ -12,8 +14,10 @@ import argparse
 import concurrent.futures as cf
 import os
 import shutil
+import importlib.util
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssu_gb300.so")
 HEADER = os.path.join(ROOT, "include", "ssu.h")
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
+BINDING = os.path.join(PKG, "_layer_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -63,6 +69,32 @@ def _compile(src, ptxas_info):
     return obj, r.stderr
 
 
+def _compile_binding():
+    """csrc/layer_binding.cpp to an object file (linked once the library is there)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "layer_binding.o")
+    include = [os.path.join(torch, "include"), os.path.join(cuda, "include"),
+               sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
+           *(f"-isystem{p}" for p in include), "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libssu_gb300.so", "-Wl,-rpath,$ORIGIN",
+           f"-L{os.path.join(torch, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _layer_binding.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) -> str:
     """Compile (if anything changed) and return the path of libssu_gb300.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -70,11 +102,17 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     deps = _deps()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     todo = [s for s, o in zip(srcs, objs) if force or ptxas_info or _stale(o, [s, *deps])]
-    if todo:
-        with cf.ThreadPoolExecutor(max_workers=min(len(todo), os.cpu_count() or 4)) as ex:
+    binding = os.path.join(BUILD, "layer_binding.o")
+    bind = force or _stale(binding, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+    if todo or bind:
+        jobs = len(todo) + bind
+        with cf.ThreadPoolExecutor(max_workers=min(jobs, os.cpu_count() or 4)) as ex:
+            bound = ex.submit(_compile_binding) if bind else None
             for obj, log in ex.map(lambda s: _compile(s, ptxas_info), todo):
                 if verbose or ptxas_info:
                     print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
+            if bound:
+                bound.result()
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *LINK_FLAGS, "-o", tmp, *objs]
@@ -82,6 +120,8 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force or bind or not os.path.exists(BINDING):
+        _link_binding(binding)
     return LIB
 
 
