@@ -245,6 +245,8 @@ def slots_compact(pools, table, pad_slot_id=-1, out=None, num_live=None, workspa
         n = pools[0].shape[0] if len(pools) and pools[0].dim() else 0
         workspace = torch.empty(slots_compact_workspace_bytes(n), dtype=torch.uint8,
                                 device=table.device)
+        if stream is not None:   # not handed out again while that stream uses it
+            workspace.record_stream(stream)
     (_module or _binding()).slots_compact(pools, table, out, num_live, workspace, pad_slot_id,
                                           _raw(stream))
     return out, num_live

@@ -470,6 +470,71 @@ def test_scan_prompt_then_tokens_is_one_prompt():
                src=torch.tensor([1]), prompt=True)
 
 
+def test_many_short_sequences():
+    """More sequences than one probe finds, than are ranked by length, and than
+    CTAs walk at once; several of a CTA's own one after another."""
+    S, dim, N = 3000, 24, 16
+    g = gen(8)
+    lens = torch.randint(0, 4, (S,), generator=g).tolist()
+    T = sum(lens)
+    cu = cu_of(lens)
+    slots = torch.randperm(S + 5, generator=g)[:S]
+    slots[::9] = -1
+    init = torch.rand(S, generator=g) < 0.5
+    c = conv_inputs(T, dim, 4, S + 5, seed=1)
+    x, w, b, pool = cuda(c, "x", "weight", "bias", "pool")
+    got = ssu.conv_fwd_varlen(x, w, cu.to(DEV), bias=b, conv_state=pool, has_initial_state=init.to(DEV),
+                              state_batch_indices=slots.to(DEV))
+    conv_check(c, got, pool, "silu", "prompts", pool=c["pool"], nseqs=S, cu=cu, src=slots, init=init,
+               prompt=True)
+    i = scan_inputs(T, dim, N, S + 5, seed=1)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    got, pool = scan_prompt(i, lens, slots, init)
+    scan_check(i, got, pool, "prompts", pool=i["pool"], nseqs=S, cu=cu, src=slots, init=init,
+               prompt=True)
+    # one token each: a row for every sequence
+    c, i = conv_inputs(S, dim, 4, S + 5, seed=2), scan_inputs(S, dim, N, S + 5, seed=2)
+    x, w, b, pool = cuda(c, "x", "weight", "bias", "pool")
+    got = ssu.conv_update(pool, x, w, bias=b, state_batch_indices=slots.to(DEV))
+    conv_check(c, got, pool, "silu", "tokens", pool=c["pool"], nseqs=S, src=slots[:, None])
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_update(pool, d["x"], d["dt"], d["A"], d["B"], d["C"], D=d["D"], z=d["z"],
+                          dt_bias=d["dt_bias"], dt_softplus=True, state_batch_indices=slots.to(DEV))
+    scan_check(i, got, pool, "tokens", pool=i["pool"], nseqs=S, src=slots[:, None])
+
+
+def test_conv_many_rows():
+    """Enough rows for the largest row tiles; sequences that begin, end and lie
+    inside them, and one of a single row at a tile's last."""
+    C, lens = 2048, [63, 1, 20000, 2, 5, 40, 130, 18000, 7, 64, 3000]
+    i = conv_inputs(sum(lens), C, 4, len(lens), seed=9)
+    x, w, b, pool = cuda(i, "x", "weight", "bias", "pool")
+    got = ssu.conv_fwd_varlen(x, w, cu_of(lens).to(DEV), bias=b, conv_state=pool)
+    conv_check(i, got, pool, "silu", "many rows", pool=i["pool"], nseqs=len(lens), cu=cu_of(lens),
+               prompt=True)
+
+
+def test_operands_off_their_vectors():
+    """weight, bias, B, C and A that do not start on 16 bytes."""
+    c = conv_inputs(30, 64, 4, 2, seed=4)
+    x, w, b, pool = cuda(c, "x", "weight", "bias", "pool")
+    off = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
+    got = ssu.conv_fwd_varlen(x, off(w), cu_of([30]).to(DEV), bias=off(b), conv_state=pool)
+    conv_check(c, got, pool, "silu", "offset", pool=c["pool"], nseqs=1, cu=cu_of([30]), prompt=True)
+    i = scan_inputs(30, 64, 16, 30, seed=4)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    d = {k: off(v) for k, v in d.items()}
+    kw = dict(D=d["D"], z=d["z"], dt_bias=d["dt_bias"], dt_softplus=True)
+    args = [d[k] for k in ("x", "dt", "A", "B", "C")]
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_fwd_varlen(*args, cu_of([30]).to(DEV), state=pool, **kw)
+    scan_check(i, got, pool, "offset", pool=i["pool"], nseqs=1, cu=cu_of([30]), prompt=True)
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_update(pool, *args, **kw)
+    scan_check(i, got, pool, "offset", pool=i["pool"], nseqs=30)
+
+
 # ---------------------------------------------------------------------------
 # slots
 # ---------------------------------------------------------------------------
