@@ -19,8 +19,8 @@ static ssu_status table_args(const ssu_slot_table* t, const char* name, Table* o
 
 static ssu_status check_counts(int64_t nseqs, int64_t rows) {
   if (nseqs < 0 || rows < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "nseqs and rows must be >= 0");
-  if (nseqs > 0x7fffffffLL || rows > 0x7fffffffLL)
-    return fail(SSU_ERR_UNSUPPORTED, "nseqs and rows must be below 2^31");
+  if (nseqs >= 1LL << 30 || rows > 0x7fffffffLL)  // the kernels count in 32 bits, with strides
+    return fail(SSU_ERR_UNSUPPORTED, "nseqs must be below 2^30 and rows below 2^31");
   return SSU_OK;
 }
 
@@ -137,7 +137,6 @@ static ssu_status check_scan(const ssu_scan_params* c, int64_t rows, bool pool_n
   p->slots = c->state ? c->slots : 0;
   p->C = (int)c->channels;
   p->G = (int)c->ngroups;
-  p->per.init((uint32_t)(c->channels / c->ngroups));
   p->x = c->x;
   p->x_rs = c->x_row_stride;
   p->z = c->z;

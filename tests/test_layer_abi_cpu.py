@@ -97,7 +97,7 @@ def test_sequence_refusals(lib, update, fwd, make):
     assert decode(lib, update, p, src=_abi.SlotTable(FAKE, -1, 4, 1, 4)) == INVALID
     assert decode(lib, update, p, nseqs=9, rows=18) == INVALID and "exceed 8 slots" in err()
     assert decode(lib, update, p, nseqs=-1) == INVALID
-    assert decode(lib, update, p, nseqs=1 << 31, rows=1 << 31, dense=1) == UNSUPPORTED
+    assert decode(lib, update, p, nseqs=1 << 30, rows=1 << 30, dense=1) == UNSUPPORTED
     assert decode(lib, update, p, nseqs=0, rows=0) == _abi.SSU_OK and err() == ""
     assert prompt(lib, fwd, p, cu=None) == INVALID and "cu_seqlens" in err()
     assert prompt(lib, fwd, p, meta=_abi.SSU_F16) == INVALID
