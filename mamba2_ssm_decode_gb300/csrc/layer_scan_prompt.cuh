@@ -209,7 +209,7 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
                                           float2 (&h)[R][NPT / 2], float (&dsum)[R]) {
   using K = PromptTile<N, R, NPT>;
   constexpr int LPC = K::LPC, TT = K::TT, SV = K::SV, BV = K::BV, TG = K::TG;
-  constexpr int UG = TT % (2 * TG) == 0 && TG < 8 ? 2 : 1;  // reduction groups per pass
+  constexpr int UG = TG < 8 ? 16 / TG < TT / TG ? 16 / TG : TT / TG : 1;  // groups of TG per pass
   // neighbouring lanes take neighbouring channels and the same columns: a load
   // of B or C then asks for the same 16 bytes in runs of lanes, which shared
   // memory serves in 1.7 cycles (runs of 8) where it takes 4 when every lane's
