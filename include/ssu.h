@@ -641,14 +641,16 @@ ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, con
  * order) moves to the k-th free slot below m, in every pool; *num_live = m and
  * table_out holds the entries under their new ids, others
  * unchanged.  Slots from m on are free afterwards; their bytes are left.
- *   workspace  device memory of ssu_slots_compact_workspace_bytes(slots) bytes
- *              (-1 for a negative size), 16-byte aligned; nothing in it need
- *              be kept between calls.
- * table_out may be table or must not overlap it.  One launch (two for pools of
- * more than 4096 slots, tables of more than 8192 entries and tables rewritten
- * in place); the host learns num_live only if it reads it.
+ *   workspace  device memory of ssu_slots_compact_workspace_bytes(slots,
+ *              entries, table_out == table) bytes, 16-byte aligned; nothing in
+ *              it need be kept between calls.  0 (pass NULL) for pools of up
+ *              to 4096 slots and tables of up to 8192 entries that are not
+ *              rewritten in place, which take one launch; else two.  -1 for
+ *              negative sizes.
+ * table_out may be table or must not overlap it.  The host learns num_live
+ * only if it reads it.
  */
-int64_t ssu_slots_compact_workspace_bytes(int64_t slots);
+int64_t ssu_slots_compact_workspace_bytes(int64_t slots, int64_t entries, int in_place);
 
 ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, const void* table,
                              void* table_out, ssu_dtype index_dtype, int64_t entries,

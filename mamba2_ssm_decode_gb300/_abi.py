@@ -174,7 +174,7 @@ def lib() -> ctypes.CDLL:
         L.ssu_slots_clear.argtypes = [_c_p, _c_int, _c_i64, _c_p, _c_int, _c_i64,
                                       _c_i64, _c_p]
         L.ssu_slots_compact_workspace_bytes.restype = _c_i64
-        L.ssu_slots_compact_workspace_bytes.argtypes = [_c_i64]
+        L.ssu_slots_compact_workspace_bytes.argtypes = [_c_i64, _c_i64, _c_int]
         L.ssu_slots_compact.restype = _c_int
         L.ssu_slots_compact.argtypes = [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_int,
                                         _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p]

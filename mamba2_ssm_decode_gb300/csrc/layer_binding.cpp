@@ -413,19 +413,21 @@ void slots_clear(PyObject* const* a) {
 // slots_compact(pools, table, out, num_live, workspace, pad, stream)
 void slots_compact(PyObject* const* a) {
   const Tensor &t = needed(a[1], "table"), &out = needed(a[2], "out");
-  const Tensor &live = needed(a[3], "num_live"), &ws = needed(a[4], "workspace");
-  const Pools p(a[0], {&t, &out, &live, &ws});
+  const Tensor& live = needed(a[3], "num_live");
+  const Tensor* ws = tensor(a[4], "workspace");
+  const Pools p(a[0], {&t, &out, &live, ws});
   const ssu_dtype d = index_of(t, "table");
   value_if(!t.is_contiguous(), "table must be contiguous");
   value_if(out.sizes() != t.sizes() || out.scalar_type() != t.scalar_type() ||
                !out.is_contiguous(),
            "out must match table's shape and dtype");
   value_if(live.scalar_type() != at::kInt || live.numel() != 1, "num_live must be one int32");
-  value_if(!ws.is_contiguous(), "workspace must be contiguous");
+  value_if(ws && !ws->is_contiguous(), "workspace must be contiguous");
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)p.device));
   done(ssu_slots_compact(p.pool.data(), (int)p.pool.size(), p.slots, t.data_ptr(), out.data_ptr(),
                          d, t.numel(), integer(a[5]), static_cast<int32_t*>(live.data_ptr()),
-                         ws.data_ptr(), (int64_t)ws.nbytes(), stream_of(a[6], p.device)));
+                         ws ? ws->data_ptr() : nullptr, ws ? (int64_t)ws->nbytes() : 0,
+                         stream_of(a[6], p.device)));
 }
 
 template <void (*F)(PyObject* const*), int ARGS>

@@ -64,8 +64,16 @@ constexpr int kScanWarps = 4;
 template <class ST, int N>
 struct ScanStep {
   using L = ssu::RowLayout<ST, N>;
-  static constexpr int FIT = 32 / L::EPL > 1 ? 32 / L::EPL : 1;  // 32 state values per thread
+  // State values per thread: 16 of the short rows, 32 of those whose lanes own
+  // more (64 tokens x 5120 channels x 128, fp32: 74 us with 32, 95 us with 16),
+  // and the CTAs an SM that they leave room for (512 tokens x 5120 channels x
+  // 16: fp32 state 65 us with four, bf16 47 us; three take 70 and 70, five 67
+  // and 53.  32 tokens x 5120 x 256: 90 us with three, some registers spilled;
+  // two take 109).
+  static constexpr int MOST = L::EPL > 4 ? 32 : 16;
+  static constexpr int FIT = MOST / L::EPL > 1 ? MOST / L::EPL : 1;
   static constexpr int U = L::LPR < FIT ? L::LPR : FIT;
+  static constexpr int CTAS = U * L::EPL > 16 ? 3 : 4;
   static constexpr int CH = kScanWarps * L::RPW * U;  // channels per CTA
 };
 
@@ -102,7 +110,7 @@ struct Ahead {
 };
 
 template <class ST, class IT, int N, bool ONE>
-__global__ void __launch_bounds__(kScanWarps * 32, ScanStep<ST, N>::L::EPL > 16 ? 2 : 3)
+__global__ void __launch_bounds__(kScanWarps * 32, ScanStep<ST, N>::CTAS)
     scan_walk_kernel(const ScanArgs p, const Seqs a) {
   using K = ScanStep<ST, N>;
   using L = typename K::L;

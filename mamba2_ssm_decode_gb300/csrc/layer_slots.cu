@@ -301,9 +301,15 @@ static ssu_status move_slots(const ssu_pool* pools, int npools, int64_t slots, c
 
 static int plan_smem(int64_t slots) { return plan_words(slots) * 12; }
 
-static int64_t workspace_bytes_of(int64_t slots) {
+static bool in_one_launch(int64_t slots, int64_t entries, bool in_place) {
+  return slots <= kSmallSlots && entries <= kSmallEntries && !in_place;
+}
+
+static int64_t workspace_bytes_of(int64_t slots, int64_t entries, bool in_place) {
+  if (slots < 0 || entries < 0) return -1;
+  if (in_one_launch(slots, entries, in_place)) return 0;
   // the number of moves, and the two slots of each (at most half the pool moves)
-  return slots < 0 ? -1 : 16 + 2 * 4 * ((slots + 1) / 2);
+  return 16 + 2 * 4 * ((slots + 1) / 2);
 }
 
 template <int MOST>
@@ -319,8 +325,8 @@ static ssu_status compact_as(const ssu_pool* pools, int npools, int64_t slots, c
   if (entries < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "entries must be >= 0");
   if ((entries > 0 && (!table || !table_out)) || !num_live)
     return fail(SSU_ERR_INVALID_ARGUMENT, "table, table_out and num_live must not be NULL");
-  const int64_t need = workspace_bytes_of(slots);
-  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+  const int64_t need = workspace_bytes_of(slots, entries, table == table_out);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(SSU_ERR_INVALID_ARGUMENT,
                 "ssu_slots_compact needs a 16-byte aligned workspace of %lld bytes, got %lld",
                 (long long)need, (long long)workspace_bytes);
@@ -331,7 +337,7 @@ static ssu_status compact_as(const ssu_pool* pools, int npools, int64_t slots, c
   const int64_t ctas = items < 1 ? 1 : items < fit ? items : fit;
   // 244 of 1024 slots moved, 201 MB: 44.7 us in two launches, 41.6 us in one; 12
   // of 48, 10 MB: 16 us and 11 us
-  if (slots <= kSmallSlots && entries <= kSmallEntries && table != table_out) {
+  if (need == 0) {
     slots_compact_kernel<MOST><<<(unsigned)ctas, kCopyThreads, 0, stream>>>(
         ps, table, table_out, index_dtype == SSU_I64, (int)entries, pad_slot_id, (int)slots,
         num_live);
@@ -374,8 +380,8 @@ ssu_status ssu_slots_clear(const ssu_pool* pools, int npools, int64_t slots, con
                                                count, pad_slot_id, (cudaStream_t)stream);
 }
 
-int64_t ssu_slots_compact_workspace_bytes(int64_t slots) {
-  return layer::workspace_bytes_of(slots);
+int64_t ssu_slots_compact_workspace_bytes(int64_t slots, int64_t entries, int in_place) {
+  return layer::workspace_bytes_of(slots, entries, in_place != 0);
 }
 
 ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, const void* table,

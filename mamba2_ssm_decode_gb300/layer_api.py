@@ -220,10 +220,10 @@ def slots_clear(pools, slots, pad_slot_id=-1, stream=None):
     (_module or _binding()).slots_clear(pools, slots, pad_slot_id, _raw(stream))
 
 
-def slots_compact_workspace_bytes(slots):
-    """Bytes of workspace slots_compact needs (C ABI
-    ``ssu_slots_compact_workspace_bytes``)."""
-    return int(_abi.lib().ssu_slots_compact_workspace_bytes(slots))
+def slots_compact_workspace_bytes(slots, entries, in_place=False):
+    """Bytes of workspace slots_compact needs for a table of ``entries`` entries
+    (C ABI ``ssu_slots_compact_workspace_bytes``); 0 where it takes one launch."""
+    return int(_abi.lib().ssu_slots_compact_workspace_bytes(slots, entries, int(in_place)))
 
 
 def slots_compact(pools, table, pad_slot_id=-1, out=None, num_live=None, workspace=None,
@@ -235,18 +235,19 @@ def slots_compact(pools, table, pad_slot_id=-1, out=None, num_live=None, workspa
 
     Returns (``out``, ``num_live``): the table under the new ids (``out`` may be
     ``table``) and m as a one-element int32 CUDA tensor.  ``workspace``: a CUDA
-    uint8 tensor of slots_compact_workspace_bytes(slots), allocated when not
-    given."""
+    uint8 tensor of slots_compact_workspace_bytes(...), allocated when needed and
+    not given."""
     if out is None:
         out = torch.empty_like(table)
     if num_live is None:
         num_live = torch.empty(1, dtype=torch.int32, device=table.device)
     if workspace is None:
         n = pools[0].shape[0] if len(pools) and pools[0].dim() else 0
-        workspace = torch.empty(slots_compact_workspace_bytes(n), dtype=torch.uint8,
-                                device=table.device)
-        if stream is not None:   # not handed out again while that stream uses it
-            workspace.record_stream(stream)
+        need = slots_compact_workspace_bytes(n, table.numel(), out is table)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=table.device)
+            if stream is not None:   # not handed out again while that stream uses it
+                workspace.record_stream(stream)
     (_module or _binding()).slots_compact(pools, table, out, num_live, workspace, pad_slot_id,
                                           _raw(stream))
     return out, num_live

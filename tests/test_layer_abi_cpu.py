@@ -169,11 +169,14 @@ def test_slots_refusals(lib):
     assert copy(one, pairs=0) == _abi.SSU_OK and err() == ""
     assert copy(pools((None, 0, 0))) == _abi.SSU_OK                       # no bytes to move
     assert lib.ssu_slots_clear(one, 1, 4, None, I32, 2, -1, None) == INVALID
-    need = lib.ssu_slots_compact_workspace_bytes(4)
-    assert need > 0 and lib.ssu_slots_compact_workspace_bytes(-1) == -1
+    size = lib.ssu_slots_compact_workspace_bytes
+    need = size(4, 2, 1)
+    assert need > 0 and size(-1, 2, 0) == size(4, -1, 0) == -1
+    assert size(4096, 8192, 0) == 0                          # one launch
+    assert size(4097, 8192, 0) > 0 and size(4096, 8193, 0) > 0
     comp = lambda t=FAKE, ws=FAKE, n=need, live=FAKE, idx=I32, entries=2: (  # noqa: E731
         lib.ssu_slots_compact(one, 1, 4, t, FAKE, idx, entries, -1, live, ws, n, None))
-    assert comp(n=need - 1) == INVALID and "workspace" in err()
+    assert comp(n=need - 1) == INVALID and "workspace" in err()   # in place: two launches
     assert comp(ws=FAKE + 4) == INVALID
     assert comp(live=None) == INVALID
     assert comp(t=None) == INVALID

@@ -613,7 +613,8 @@ def test_slots_compact(slots, live, pads, idx):
         same_bits(q, ref)
     # in place, with a workspace of the caller's
     gpu, t = on_gpu(pools), table.to(DEV)
-    ws = torch.full((ssu.slots_compact_workspace_bytes(slots),), 255, dtype=torch.uint8, device=DEV)
+    need = ssu.slots_compact_workspace_bytes(slots, t.numel(), in_place=True)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
     out, _ = ssu.slots_compact(gpu, t, out=t, workspace=ws)
     assert out is t and t.cpu().tolist() == want.tolist()
 
@@ -693,7 +694,7 @@ def test_each_call_is_its_stated_launches():
         lambda: ssu.conv_update_varlen(cp, x, w, bias=b, cu_seqlens=cu, out=out)) == 1
     t = torch.tensor([3, 1], dtype=torch.int32, device=DEV)
     to, n = torch.empty_like(t), torch.empty(1, dtype=torch.int32, device=DEV)
-    ws = torch.empty(ssu.slots_compact_workspace_bytes(4), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ssu.slots_compact_workspace_bytes(4, 2, True), dtype=torch.uint8, device=DEV)
     assert graph_kernel_nodes(lambda: ssu.slots_copy([pool, cp], t[:1], t[1:])) == 1
     assert graph_kernel_nodes(lambda: ssu.slots_clear([pool, cp], t)) == 1
     assert graph_kernel_nodes(
@@ -787,7 +788,7 @@ def test_refusals():
     with pytest.raises(ValueError, match="slot must be contiguous"):
         ssu.slots_clear([sp.transpose(1, 2)], cu[:1])
     with pytest.raises(ValueError, match="workspace"):
-        ssu.slots_compact([sp], cu, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
+        ssu.slots_compact([sp], cu, out=cu, workspace=torch.empty(8, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="int32 or int64"):
         ssu.slots_compact([sp], cu.float())
     assert ssu.ssu_device_error() == 0
