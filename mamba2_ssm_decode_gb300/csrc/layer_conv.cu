@@ -211,28 +211,36 @@ __global__ void __launch_bounds__(kPromptThreads, sizeof(IT) == 2 ? 6 : 4)
     // kConvRows loads are always in flight: a row's place takes the row
     // kConvRows on (the last one again beyond the end) as soon as it is in xs
     Words<IT, V> in[kConvRows];
-    auto fetch = [&](int k, int at) {
-      in[k].load(x + at * p.x_rs);
+    const IT* xf = x + r * p.x_rs;  // the row to fetch next
+    int behind = stop - 1 - r;      // rows behind it
+    IT* o = out + r * p.o_rs;
+    auto fetch = [&](int k) {
+      in[k].load(xf);
+      if (behind > 0) {
+        xf += p.x_rs;
+        --behind;
+      }
     };
-    auto row = [&](int k, int at) {
+    auto row = [&](int k) {
 #pragma unroll
       for (int i = 0; i < P; ++i) xs[W - 1][i] = in[k].pair(i);
-      fetch(k, stop - at > kConvRows ? at + kConvRows : stop - 1);
-      conv_row<IT, W, V>(out + at * p.o_rs, xs, w, bias, p.silu);
+      fetch(k);
+      conv_row<IT, W, V>(o, xs, w, bias, p.silu);
+      o += p.o_rs;
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
 #pragma unroll
         for (int i = 0; i < P; ++i) xs[j][i] = xs[j + 1][i];
     };
 #pragma unroll
-    for (int k = 0; k < kConvRows; ++k) fetch(k, stop - r > k ? r + k : stop - 1);
+    for (int k = 0; k < kConvRows; ++k) fetch(k);
     for (; stop - r >= kConvRows; r += kConvRows) {
 #pragma unroll
-      for (int k = 0; k < kConvRows; ++k) row(k, r + k);
+      for (int k = 0; k < kConvRows; ++k) row(k);
     }
 #pragma unroll
     for (int k = 0; k < kConvRows - 1; ++k)
-      if (stop - r > k) row(k, r + k);
+      if (stop - r > k) row(k);
 
     int64_t slot;
     if (owner && it.read_ok && !p.disable && write_slot(a, s, 0, p.pad, p.slots, &slot)) {
