@@ -80,6 +80,8 @@ __device__ __forceinline__ void conv_row(IT* out, const float2 (&xs)[W][(V + 1) 
 // sequence's rows with the window of W - 1 rows in registers.  What it needs
 // of up to ROWS rows (the rows, and the slots that take the state after them)
 // is asked for at once, beside the slot's rows.  ROWS 1: one row a sequence.
+// Bound by the latency of three dependent loads (count, slot, rows) in two or
+// three waves of CTAs: 640 drafted rows x 5376 channels take 14 us for 43 MB.
 constexpr int kStepThreads = 128;
 
 template <class IT, class WT, int W, int V, int ROWS>
@@ -163,6 +165,9 @@ __device__ __forceinline__ int find_sequence(const Seqs& a, int row) {
 // back to a sequence's slot (its first W - 1) are all done by the tile that
 // holds the sequence's first row, which also writes the slot afterwards: no
 // other CTA reads a slot, so it may be written in place.
+//
+// Bound by HBM and the latency of its loads: 20634 x 5376 bf16 rows take 85 us,
+// 444 MB at 5.2 TB/s; the same walk without the arithmetic takes 73 us.
 template <class IT>
 constexpr int kRowsInFlight = sizeof(IT) == 2 ? 8 : 4;
 constexpr int kPromptThreads = 128;

@@ -19,8 +19,9 @@ static ssu_status table_args(const ssu_slot_table* t, const char* name, Table* o
 
 static ssu_status check_counts(int64_t nseqs, int64_t rows) {
   if (nseqs < 0 || rows < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "nseqs and rows must be >= 0");
-  if (nseqs >= 1LL << 30 || rows > 0x7fffffffLL)  // the kernels count in 32 bits, with strides
-    return fail(SSU_ERR_UNSUPPORTED, "nseqs must be below 2^30 and rows below 2^31");
+  // the kernels count sequences and rows in 32 bits, a tile or a stride beyond the last
+  if (nseqs >= 1LL << 30 || rows > 0x7fffffffLL - 1024)
+    return fail(SSU_ERR_UNSUPPORTED, "nseqs must be below 2^30 and rows below 2^31 - 1024");
   return SSU_OK;
 }
 
@@ -236,7 +237,6 @@ ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t 
     return fail(SSU_ERR_INVALID_ARGUMENT, "out must not be an operand");
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
-  p.final_only = 1;
   return launched(launch_prompt(c, p, a, (cudaStream_t)stream));
 }
 

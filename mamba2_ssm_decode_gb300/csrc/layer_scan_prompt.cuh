@@ -9,8 +9,13 @@
 // back through shared memory for the gate and a whole-row store.  The next
 // tile's rows are in flight in registers meanwhile.
 //
-// Bound by the exponentials (dstate per row and channel, on the special-function
-// pipe) and the packed fp32 products beside them, not by HBM.
+// Four state columns of a channel's row take 8 packed fp32 operations (about 2.3
+// cycles each: 18 to 21), 4 exponentials (16 cycles of the special-function
+// pipe), two shared memory reads of B and C for two channels and two of dt' and
+// dt' x, and a quarter of a staged value.  So neither HBM nor one pipe alone
+// bounds it: at 9001 x 4096 rows x 16 in 16 sequences, 194 us, the fp32 pipe is
+// busy 52 % of the time, the special-function pipe 39 %, shared memory 57 %, the
+// issue slots 66 %; 36 cycles a unit in the full waves, the rest is the tail.
 #pragma once
 
 #include "layer_scan.cuh"
@@ -604,6 +609,10 @@ cudaError_t launch_scan_prompt(const ScanArgs& p, const Seqs& a,
   return launch_prompt_as<IT, DT, N, R, NPT, false>(p, a, tiles, 1, stream);
 }
 
+// Two channels a thread share what is read of B and C.  Four columns of each
+// leave 126 registers and 16 warps an SM; eight (one wave of 512 CTAs for 1024)
+// take 207 us where four take 202, four channels of four 225.  The long rows
+// have eight: half the lanes to a channel, half the sums to reduce.
 template <class IT, class DT>
 cudaError_t launch_scan_prompt_n(int N, const ScanArgs& p, const Seqs& a,
                                  cudaStream_t stream) {

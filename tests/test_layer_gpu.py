@@ -323,7 +323,7 @@ def test_scan_prompts(io, dt, state, N, dim, G):
 
 @pytest.mark.parametrize("lens,dim", [([3000], 24), ([2049], 40), ([1500, 7], 16), ([700] * 3, 8),
                                       ([1023, 1, 513], 33)])
-@pytest.mark.parametrize("N", [16, 64])
+@pytest.mark.parametrize("N", [16, 32, 64, 128, 256])
 def test_scan_long_prompts(lens, dim, N):
     """Long chains of few channels, from a slot and into it."""
     i = scan_inputs(sum(lens), dim, N, len(lens), 1, BF16, BF16, F32, seed=dim)
