@@ -82,10 +82,13 @@ __device__ __forceinline__ void conv_row(IT* out, const float2 (&xs)[W][(V + 1) 
 // is asked for at once, beside the slot's rows.  ROWS 1: one row a sequence.
 // Bound by the latency of three dependent loads (count, slot, rows) in two or
 // three waves of CTAs: 640 drafted rows x 5376 channels take 14 us for 43 MB.
+// Eight CTAs an SM: 1024 one-row sequences 22.5 us where the 6 that registers
+// would leave take 26.
 constexpr int kStepThreads = 128;
 
 template <class IT, class WT, int W, int V, int ROWS>
-__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvArgs p, const Seqs a) {
+__global__ void __launch_bounds__(kStepThreads, sizeof(IT) == 2 ? 8 : 5)
+    conv_step_kernel(const ConvArgs p, const Seqs a) {
   const int64_t c = ((int64_t)blockIdx.x * kStepThreads + threadIdx.x) * V;
   if (c >= p.C) return;
   constexpr int P = (V + 1) / 2;
