@@ -557,7 +557,9 @@ ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* p, int64_t nseqs, int64_t 
  *            F32, out in io_dtype or F32; z may be NULL.
  * B, C       [rows, ngroups, dstate], unit dstate stride.
  * A          [channels, dstate] fp32, unit dstate stride, A_row_stride between
- *            channels.  D, dt_bias [channels] fp32 contiguous, or NULL.
+ *            channels; a column of -infinity forgets at once (dt' of 2^-120 or
+ *            more), and a step of exactly 0 decays nothing, whatever A.
+ * D, dt_bias [channels] fp32 contiguous, or NULL.
  * disable_state_update  1: no slot is written.
  */
 typedef struct ssu_scan_params {

@@ -222,6 +222,17 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
+// A log2 e, held to the largest finite value (NaN stays).  An infinite one would
+// turn a step of zero, which has to change nothing, into 0 x infinity; held, a
+// column with A = -infinity still forgets at once: 2^(A dt') is 0 for every dt'
+// of 2^-120 or more (a smaller one, where infinity would do, forgets in part).
+__device__ __forceinline__ float log2_rate(float a) {
+  float r = a * kLog2e;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(-3.402823466e38f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(r) : "f"(3.402823466e38f));
+  return r;
+}
+
 __device__ __forceinline__ float silu(float v) {
   return __fdividef(v, 1.0f + ex2(-v * kLog2e));
 }

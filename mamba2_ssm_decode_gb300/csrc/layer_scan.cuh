@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kScanWarps * 32, ScanStep<ST, N>::CTAS)
       if (c_ok[u]) load_floats<float, VEC>(p.A + c * p.A_rs + (q + k * L::LPR) * VEC, p.a_vec, f);
 #pragma unroll
       for (int i = 0; i < VEC / 2; ++i)
-        A2[u][k * VEC / 2 + i] = make_float2(f[2 * i] * kLog2e, f[2 * i + 1] * kLog2e);
+        A2[u][k * VEC / 2 + i] = make_float2(log2_rate(f[2 * i]), log2_rate(f[2 * i + 1]));
     }
   }
   const float Dc = p.D && cm_ok ? p.D[cm] : 0.0f;

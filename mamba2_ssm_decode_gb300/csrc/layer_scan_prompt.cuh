@@ -239,7 +239,8 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
     const int n = r_end - rt < TT ? r_end - rt : TT;
     const bool in = tr < n;
     const Words<IT, SV> xk = rows.x, zk = rows.z;
-    // rows beyond the sequence get dt' = 0 and zeros: a step that changes nothing
+    // rows beyond the sequence get dt' = 0 and zeros: a step that changes nothing,
+    // since no A2 is infinite
     if (s0 < K::CH) {
       float bias[SV], d[SV], dx[SV];
       from_row<K>(sm.bias, tp, bias);
@@ -439,8 +440,8 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
       float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (c < cn)
         load_floats<float, 4>(p.A + (int64_t)(c0 + c) * p.A_rs + (j * LPC + q) * 4, p.a_vec, f);
-      A2[k][2 * j] = make_float2(f[0] * kLog2e, f[1] * kLog2e);
-      A2[k][2 * j + 1] = make_float2(f[2] * kLog2e, f[3] * kLog2e);
+      A2[k][2 * j] = make_float2(log2_rate(f[0]), log2_rate(f[1]));
+      A2[k][2 * j + 1] = make_float2(log2_rate(f[2]), log2_rate(f[3]));
     }
   }
   for (int i = tid; i < K::CH; i += kPromptThreads) {

@@ -1,0 +1,81 @@
+"""GPU parity of the layer calls where values, memory and streams come to their
+edges: infinite and huge A, sequences split over a cluster in every form,
+operands that overlap, results on another stream than the current one.
+
+Tolerances as in test_layer_gpu.py: the oracle's running bound for the scan, and
+half a unit in the last place of what is stored in 16 bits.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import mamba2_ssm_decode_gb300 as ssu
+
+from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, cu_of, cuda, gen, scan_check,  # noqa: F401
+                             scan_inputs, scan_prompt)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# values at the edges of their range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens", [[1, 2, 7, 16, 33, 0, 61], [401], [1203]])
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("N", [16, 32, 64, 128, 256])
+def test_scan_columns_that_forget_at_once(N, io, lens):
+    """A = -inf: exp(A dt') is 0 for every dt' > 0, whatever the sequence's length.
+    The oracle has -1e30 there, whose exponentials are 0 as well."""
+    S, dim = len(lens), 24
+    i = scan_inputs(sum(lens), dim, N, S + 1, 1, io, F32, F32, seed=N)
+    forget = torch.rand(dim, N, generator=gen(1)) < 0.3
+    i["A"][forget] = -1e30
+    slots = torch.randperm(S + 1, generator=gen(2))[:S]
+    ref = dict(i, A=i["A"].clone())
+    i["A"][forget] = -math.inf
+    got, pool = scan_prompt(i, lens, slots)
+    scan_check(ref, got, pool, "prompts", pool=i["pool"], nseqs=S, cu=cu_of(lens), src=slots, prompt=True)
+    # ... and one row at a time
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    pool, cu = i["pool"].to(DEV), cu_of([min(n, 5) for n in lens])
+    T = int(cu[-1])
+    d = {k: v[:T] if k in ("x", "dt", "z", "B", "C") else v for k, v in d.items()}
+    ref.update({k: ref[k][:T] for k in ("x", "dt", "z", "B", "C")})
+    table = slots[:, None].repeat(1, 5)
+    got = ssu.scan_update_varlen(pool, d["x"], d["dt"], d["A"], d["B"], d["C"], D=d["D"], z=d["z"],
+                                 dt_bias=d["dt_bias"], dt_softplus=True, cu_seqlens=cu.to(DEV),
+                                 state_batch_indices=table.int().to(DEV))
+    scan_check(ref, got, pool, "rows", pool=i["pool"], nseqs=S, cu=cu, src=table)
+
+
+@pytest.mark.parametrize("lens", [[1, 7, 16, 33], [401]])
+@pytest.mark.parametrize("N", [16, 64, 256])
+def test_scan_huge_rates_and_steps_of_zero(N, lens):
+    """|A| up to the largest fp32 (A log2 e is beyond it) with steps of exactly 0,
+    which change nothing; a NaN in A stays in its column."""
+    S, dim, T = len(lens), 24, sum(lens)
+    i = scan_inputs(T, dim, N, S, 1, BF16, F32, F32, seed=N)
+    i["A"][torch.rand(dim, N, generator=gen(1)) < 0.3] = -3.4e38
+    i["dt"] = i["dt"].abs() * 0.1 * (torch.rand(T, dim, generator=gen(2)) < 0.5)
+    i["dt_bias"] = None
+    got, pool = scan_prompt(i, lens, softplus=False)
+    scan_check(i, got, pool, "prompts", softplus=False, pool=i["pool"], nseqs=S, cu=cu_of(lens), prompt=True)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    rows = [d[k][:S] if k != "A" else d[k] for k in ("x", "dt", "A", "B", "C")]
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_update(pool, *rows, D=d["D"], z=d["z"][:S])
+    i.update({k: i[k][:S] for k in ("x", "dt", "z", "B", "C")})
+    scan_check(i, got, pool, "rows", softplus=False, pool=i["pool"], nseqs=S)
+    d["A"][3, 5] = math.nan
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_update(pool, *rows, D=d["D"], z=d["z"][:S])
+    bad = torch.isnan(pool)
+    assert bool(bad[:, 3, 5].all()) and int(bad.sum()) == S and bool(torch.isnan(got[:, 3]).all())
+    held = i["pool"].to(DEV)
+    got = ssu.scan_fwd_varlen(*rows, cu_of([S]).to(DEV), D=d["D"], z=d["z"][:S], state=held)
+    bad = torch.isnan(held)
+    assert bool(bad[0, 3, 5]) and int(bad.sum()) == 1 and bool(torch.isnan(got[:, 3]).all())
