@@ -371,6 +371,18 @@ __device__ __forceinline__ float peer_float(const float* p, int rank) {
   return v;
 }
 
+// The factor 2^(3 e) that a piece puts on the state that enters it may leave
+// fp32's range though the product does not: a state of 0 stays 0 through a piece
+// that grows, a large one survives a piece that decays below 2^-126.  So it goes
+// on as three factors 2^e, held to [2^-126, 2^127]: they reach from the smallest
+// fp32 to the largest, and each product lies between the state and the result.
+__device__ __forceinline__ float third_of_decay(float e) {
+  float f = ex2(e);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(f) : "f"(0x1p-126f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(f) : "f"(0x1p127f));
+  return f;
+}
+
 // What a CTA's piece does, for the CTAs behind it.
 template <int R, int NPT>
 struct PromptPiece {
@@ -523,13 +535,12 @@ __global__ void __launch_bounds__(kPromptThreads, 4)
           for (int b = 1; b < rank; ++b) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-              const float d = peer_float(&piece.dsum[k][tid], b);
+              const float d = peer_float(&piece.dsum[k][tid], b) * (1.0f / 3.0f);
 #pragma unroll
               for (int j = 0; j < NPT / 2; ++j) {
-                h[k][j].x = fmaf(h[k][j].x, ex2(A2[k][j].x * d),
-                                 peer_float(&piece.h[k * NPT + 2 * j][tid], b));
-                h[k][j].y = fmaf(h[k][j].y, ex2(A2[k][j].y * d),
-                                 peer_float(&piece.h[k * NPT + 2 * j + 1][tid], b));
+                const float fx = third_of_decay(A2[k][j].x * d), fy = third_of_decay(A2[k][j].y * d);
+                h[k][j].x = fmaf(h[k][j].x * fx * fx, fx, peer_float(&piece.h[k * NPT + 2 * j][tid], b));
+                h[k][j].y = fmaf(h[k][j].y * fy * fy, fy, peer_float(&piece.h[k * NPT + 2 * j + 1][tid], b));
               }
             }
           }

@@ -79,3 +79,35 @@ def test_scan_huge_rates_and_steps_of_zero(N, lens):
     got = ssu.scan_fwd_varlen(*rows, cu_of([S]).to(DEV), D=d["D"], z=d["z"][:S], state=held)
     bad = torch.isnan(held)
     assert bool(bad[0, 3, 5]) and int(bad.sum()) == 1 and bool(torch.isnan(got[:, 3]).all())
+
+
+@pytest.mark.parametrize("N", [16, 32, 64, 128, 256])
+def test_scan_split_states_at_the_ends_of_the_range(N):
+    """A long prompt split into pieces whose decay alone leaves fp32's range where the
+    state does not: from 0, from tiny states that grow and from large ones that decay."""
+    T, dim = 1203, 24
+    i = scan_inputs(T, dim, N, 1, 1, BF16, F32, F32, seed=N)
+    i["x"].zero_()
+    i["dt"].zero_()
+    i["dt_bias"] = None
+    for c in range(dim):   # 20 steps of 5: a sum of 100 nats inside one piece for most channels
+        i["dt"][30 + 48 * c:50 + 48 * c, c] = 5.0
+        i["pool"][0, c] *= (0.0, 1e-35, 1e30)[c % 3]
+        i["A"][c] = (1.0, 1.0, -1.0)[c % 3] * (0.9 + 0.1 * torch.rand(N, generator=gen(c)))
+    got, pool = scan_prompt(i, [T], softplus=False)
+    has = scan_check(i, got, pool, "pieces", softplus=False, pool=i["pool"], nseqs=1, cu=cu_of([T]),
+                     prompt=True)
+    assert has.all() and bool((pool[0, 0::3] == 0).all()) and bool((pool[0, 1::3] != 0).all())
+    assert bool(torch.isfinite(pool).all()) and bool((pool[0, 2::3] != 0).all())
+
+
+def test_scan_split_keeps_rows_of_zeros():
+    """Leading rows of zeros under growing factors, then rows that count."""
+    T, dim, N = 1203, 24, 16
+    i = scan_inputs(T, dim, N, 1, 1, BF16, F32, F32, seed=2)
+    i["x"][:-40] = 0.0
+    i["A"], i["dt"], i["dt_bias"] = torch.rand(dim, N, generator=gen(1)), torch.full((T, dim), 2.0), None
+    i["pool"].zero_()
+    got, pool = scan_prompt(i, [T], softplus=False)
+    assert bool(torch.isfinite(pool).all()) and bool((got[:-40] == 0).all())
+    scan_check(i, got, pool, "zeros", softplus=False, pool=i["pool"], nseqs=1, cu=cu_of([T]), prompt=True)
