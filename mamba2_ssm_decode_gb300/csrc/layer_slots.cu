@@ -203,11 +203,15 @@ template <int MOST>
 __global__ void __launch_bounds__(kCopyThreads)
     slots_move_kernel(const __grid_constant__ Pools<MOST> ps, const int* moves, const int* src,
                       const int* dst) {
-  const int64_t chunks = ps.first[ps.n];
-  const int64_t items = *moves * chunks;
+  const int64_t chunks = ps.first[ps.n], half = ps.slots / 2;
+  const int64_t listed = *moves;  // at most half the slots, as the plan leaves them ...
+  const int64_t items = (listed < half ? listed : half) * chunks;
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int64_t m = i / chunks;
-    move_chunk<Fill::kCopy, MOST>(ps, (int)(i - m * chunks), src[m], dst[m]);
+    const unsigned from = src[m], to = dst[m];
+    // ... and ids below `slots`: a workspace that something else wrote moves nothing elsewhere
+    if (from < ps.slots && to < ps.slots)
+      move_chunk<Fill::kCopy, MOST>(ps, (int)(i - m * chunks), from, to);
   }
 }
 

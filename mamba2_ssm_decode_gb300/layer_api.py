@@ -3,7 +3,8 @@ causal convolution, the selective scan with a full A, and the moves of slots.
 
 Argument marshalling only: the checks that tensors describe the layout the ABI
 expects (no hidden copies, no compute) are in csrc/layer_binding.cpp, the calls
-go to the current torch stream of the tensors' device.  ValueError for a
+go to ``stream``, or to the current torch stream of the tensors' device; what a
+caller does not give (``out``, a workspace) is allocated for that stream.  ValueError for a
 rejected argument, NotImplementedError for a capability the library does not
 implement, RuntimeError for a failed launch.
 """
@@ -15,6 +16,7 @@ import os
 import torch
 
 from . import _abi
+from ._alloc import empty, result
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 _ONE_TOKEN, _PACKED, _PROMPT = 0, 1, 2
@@ -70,7 +72,7 @@ def conv_update(conv_state, x, weight, bias=None, activation="silu", state_batch
     "silu" or None.  Slot vectors [batch] int32/int64.  Returns ``out``
     [batch, C] (which may be x itself)."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = result(stream, x.shape, x.dtype, x.device)
     (_module or _binding()).conv(
         _ONE_TOKEN, conv_state, x, weight, bias, _activation(activation), None, None,
         state_batch_indices, dst_state_batch_indices, None, pad_slot_id, out, -1, 1,
@@ -99,7 +101,7 @@ def conv_update_varlen(conv_state, x, weight, bias=None, activation="silu", cu_s
         if cu_seqlens is None:
             nseqs = batch
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = result(stream, x.shape, x.dtype, x.device)
     (_module or _binding()).conv(
         _PACKED, conv_state, x, weight, bias, _activation(activation), cu_seqlens,
         num_accepted_tokens, state_batch_indices, dst_state_batch_indices, None, pad_slot_id, out,
@@ -119,7 +121,7 @@ def conv_fwd_varlen(x, weight, cu_seqlens, bias=None, activation="silu", conv_st
     takes its last W - 1 rows.  Returns ``out`` [rows, C], which must not
     overlap x."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = result(stream, x.shape, x.dtype, x.device)
     (_module or _binding()).conv(
         _PROMPT, conv_state, x, weight, bias, _activation(activation), cu_seqlens, None,
         state_batch_indices, dst_state_batch_indices, has_initial_state, pad_slot_id, out, -1, 1,
@@ -142,7 +144,7 @@ def scan_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     [batch] int32/int64.  Returns ``out`` [batch, dim] (x's dtype, or
     ``out_dtype=torch.float32``)."""
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = result(stream, x.shape, out_dtype or x.dtype, x.device)
     (_module or _binding()).scan(
         _ONE_TOKEN, state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, None, None,
         state_batch_indices, dst_state_batch_indices, None, pad_slot_id, out, -1, 1,
@@ -170,7 +172,7 @@ def scan_update_varlen(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_s
         if cu_seqlens is None:
             nseqs = batch
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = result(stream, x.shape, out_dtype or x.dtype, x.device)
     (_module or _binding()).scan(
         _PACKED, state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens,
         num_accepted_tokens, state_batch_indices, dst_state_batch_indices, None, pad_slot_id, out,
@@ -191,7 +193,7 @@ def scan_fwd_varlen(x, dt, A, B, C, cu_seqlens, out=None, D=None, z=None, dt_bia
     -- ``dst_state_batch_indices`` or the same -- takes its final state.
     Returns ``out`` [rows, dim], which must not overlap an operand."""
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = result(stream, x.shape, out_dtype or x.dtype, x.device)
     (_module or _binding()).scan(
         _PROMPT, state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu_seqlens, None,
         state_batch_indices, dst_state_batch_indices, has_initial_state, pad_slot_id, out, -1, 1,
@@ -238,16 +240,14 @@ def slots_compact(pools, table, pad_slot_id=-1, out=None, num_live=None, workspa
     uint8 tensor of slots_compact_workspace_bytes(...), allocated when needed and
     not given."""
     if out is None:
-        out = torch.empty_like(table)
+        out = result(stream, table.shape, table.dtype, table.device)
     if num_live is None:
-        num_live = torch.empty(1, dtype=torch.int32, device=table.device)
+        num_live = result(stream, 1, torch.int32, table.device)
     if workspace is None:
         n = pools[0].shape[0] if len(pools) and pools[0].dim() else 0
         need = slots_compact_workspace_bytes(n, table.numel(), out is table)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=table.device)
-            if stream is not None:   # not handed out again while that stream uses it
-                workspace.record_stream(stream)
+            workspace = empty(stream, need, torch.uint8, table.device)
     (_module or _binding()).slots_compact(pools, table, out, num_live, workspace, pad_slot_id,
                                           _raw(stream))
     return out, num_live

@@ -14,8 +14,8 @@ import torch
 
 import mamba2_ssm_decode_gb300 as ssu
 
-from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, cu_of, cuda, gen, scan_check,  # noqa: F401
-                             scan_inputs, scan_prompt)
+from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, conv_inputs, cu_of, cuda, gen,  # noqa: F401
+                             same_bits, scan_check, scan_inputs, scan_prompt)
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,98 @@ def test_scan_split_keeps_rows_of_zeros():
     got, pool = scan_prompt(i, [T], softplus=False)
     assert bool(torch.isfinite(pool).all()) and bool((got[:-40] == 0).all())
     scan_check(i, got, pool, "zeros", softplus=False, pool=i["pool"], nseqs=1, cu=cu_of([T]), prompt=True)
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+
+def _stream_calls():
+    """name: (inputs, call(inputs, stream) -> results; the pools are results too)."""
+    T, S, dim, N = 70, 3, 64, 16
+    c, i = conv_inputs(T, dim, 4, 8, seed=1), scan_inputs(T, dim, N, 8, seed=1)
+    d = {**{k: v for k, v in i.items() if k != "pool"}, "state": i["pool"], "conv": c["pool"],
+         "w": c["weight"], "cb": c["bias"], "cu": cu_of([40, 5, 25]),
+         "table": torch.tensor([6, 0, 3], dtype=torch.int32)}
+    scan = lambda d, n: ([d[k][:n] if k != "A" else d[k] for k in ("x", "dt", "A", "B", "C")],  # noqa: E731
+                         dict(D=d["D"], z=d["z"][:n], dt_bias=d["dt_bias"], dt_softplus=True,
+                              state_batch_indices=d["table"]))
+
+    def scan_call(f, n, pool_first, **extra):
+        def call(d, stream):
+            args, kw = scan(d, n)
+            if pool_first:
+                return f(d["state"], *args, **kw, **{k: d[v] for k, v in extra.items()}, stream=stream)
+            return f(*args, d["cu"], state=d["state"], **kw, stream=stream)
+        return call
+
+    pools = lambda d: [d["state"], d["conv"]]  # noqa: E731
+    return d, {
+        "conv_update": lambda d, s: ssu.conv_update(d["conv"], d["x"][:S], d["w"], bias=d["cb"],
+                                                    state_batch_indices=d["table"], stream=s),
+        "conv_update_varlen": lambda d, s: ssu.conv_update_varlen(
+            d["conv"], d["x"], d["w"], bias=d["cb"], cu_seqlens=d["cu"],
+            state_batch_indices=d["table"], stream=s),
+        "conv_fwd_varlen": lambda d, s: ssu.conv_fwd_varlen(
+            d["x"], d["w"], d["cu"], bias=d["cb"], conv_state=d["conv"],
+            state_batch_indices=d["table"], stream=s),
+        "scan_update": scan_call(ssu.scan_update, S, True),
+        "scan_update_varlen": scan_call(ssu.scan_update_varlen, T, True, cu_seqlens="cu"),
+        "scan_fwd_varlen": scan_call(ssu.scan_fwd_varlen, T, False),
+        "slots_copy": lambda d, s: ssu.slots_copy(pools(d), d["table"][:2], d["table"][1:], stream=s),
+        "slots_clear": lambda d, s: ssu.slots_clear(pools(d), d["table"], stream=s),
+        "slots_compact": lambda d, s: ssu.slots_compact(pools(d), d["table"], stream=s),
+        "slots_compact in place": lambda d, s: ssu.slots_compact(pools(d), d["table"], out=d["table"],
+                                                                 stream=s)}
+
+
+@pytest.mark.parametrize("how", ["argument", "current"])
+@pytest.mark.parametrize("name", list(_stream_calls()[1]))
+def test_calls_follow_the_work_of_their_stream(name, how):
+    """The inputs get their values on a side stream, behind work of some 10 ms; nothing
+    between that and the call waits for the GPU.  The call, with `stream=` while another
+    stream is current or with the side stream current, sees those values."""
+    d, calls = _stream_calls()
+    call = calls[name]
+    flat = lambda r: [] if r is None else list(r) if isinstance(r, tuple) else [r]  # noqa: E731
+    late = {k: v.to(DEV) for k, v in d.items()}
+    want_in = {k: v.clone() for k, v in late.items()}
+    want = flat(call(want_in, None)) + [want_in["state"], want_in["conv"]]
+    early = {k: torch.zeros_like(v) for k, v in late.items()}
+    early["table"].fill_(-1)
+    busy = torch.zeros(1 << 28, device=DEV)
+    side = torch.cuda.Stream()
+    call({k: v.clone() for k, v in early.items()}, side)   # everything loaded
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            busy.add_(1.0)
+        for k in early:
+            early[k].copy_(late[k])
+        waiting = torch.cuda.Event()
+        waiting.record()
+        got = call(early, None) if how == "current" else None
+    if how == "argument":
+        got = call(early, side)
+    assert not waiting.query(), "the work in front was over before the call: nothing shown"
+    side.synchronize()
+    got = flat(got) + [early["state"], early["conv"]]
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        same_bits(a, b)
+
+
+def test_results_are_not_memory_in_use_on_the_current_stream():
+    """With `stream=`, a result must not be a block that was just freed on the
+    current stream: work queued there may still be using it."""
+    d, calls = _stream_calls()
+    d = {k: v.to(DEV) for k, v in d.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for name in ("conv_fwd_varlen", "scan_fwd_varlen", "conv_update_varlen", "scan_update_varlen"):
+        freed = [torch.empty_like(d["x"]) for _ in range(8)]
+        places = {t.data_ptr() for t in freed}
+        del freed
+        got = calls[name](d, side)
+        assert got.data_ptr() not in places, name
+    side.synchronize()

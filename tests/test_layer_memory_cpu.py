@@ -1,0 +1,59 @@
+"""Where the layer calls take the memory that their callers do not give, with the
+allocator and the native calls replaced by recorders (no GPU)."""
+from __future__ import annotations
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+from mamba2_ssm_decode_gb300 import layer_api as api
+
+X, I32 = torch.zeros(6, 32), torch.zeros(3, dtype=torch.int32)
+CALLS = {
+    "conv_update": lambda **kw: api.conv_update(None, X, None, **kw),
+    "conv_update_varlen": lambda **kw: api.conv_update_varlen(None, X, None, **kw),
+    "conv_fwd_varlen": lambda **kw: api.conv_fwd_varlen(X, None, I32, **kw),
+    "scan_update": lambda **kw: api.scan_update(None, X, X, None, X, X, **kw),
+    "scan_update_varlen": lambda **kw: api.scan_update_varlen(None, X, X, None, X, X, **kw),
+    "scan_fwd_varlen": lambda **kw: api.scan_fwd_varlen(X, X, None, X, X, I32, **kw),
+    "slots_compact": lambda **kw: api.slots_compact([X], I32, **kw),
+    "slots_compact, in place": lambda **kw: api.slots_compact([X], I32, out=I32, **kw),
+}
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The stream that is current at each allocation of a call."""
+    current, seen, empty = [None], [], torch.empty
+
+    @contextlib.contextmanager
+    def use(stream):
+        before, current[0] = current[0], stream
+        yield
+        current[0] = before
+
+    def recorded(*a, **kw):
+        seen.append(current[0])
+        return empty(*a, **kw)
+
+    nothing = lambda *a: None  # noqa: E731
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: recorded(t.shape, dtype=t.dtype, **kw))
+    monkeypatch.setattr(torch.Tensor, "record_stream", nothing)
+    monkeypatch.setattr(api, "slots_compact_workspace_bytes", lambda *a, **kw: 64)
+    monkeypatch.setattr(api, "_module", types.SimpleNamespace(conv=nothing, scan=nothing,
+                                                              slots_compact=nothing))
+    return seen
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_memory_of_the_call_is_of_its_stream(call, streams):
+    side = types.SimpleNamespace(cuda_stream=1)
+    CALLS[call](stream=side)
+    assert streams and all(s is side for s in streams)
+    del streams[:]
+    CALLS[call]()
+    assert streams and all(s is None for s in streams)
