@@ -14,8 +14,16 @@ def empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def zeros(stream, shape, dtype, device):
+    """... zeroed in that stream's order."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(shape, dtype=dtype, device=device)
+
+
 def result(stream, shape, dtype, device):
-    """... and that the caller's current stream goes on with: it is not handed out
+    """As ``empty``, for what the caller's current stream goes on with: it is not handed out
     again while work queued there by the time it is freed may still read it."""
     t = empty(stream, shape, dtype, device)
     if stream is not None and t.is_cuda:

@@ -1,9 +1,11 @@
 """Python binding of the C ABI (include/ssu.h): argument marshalling only.
 
 Each function takes CUDA torch tensors, checks that they describe the layout
-the ABI expects (no hidden copies, no compute), and calls the library on the
-current torch stream of the tensors' device.  Every step of the operation runs
-in libssu_gb300.so; there is no CPU or torch fallback.
+the ABI expects (no hidden copies, no compute), and calls the library on
+``stream``, or on the current torch stream of the tensors' device; what a caller
+does not give (``out``, scratch, a workspace) is allocated for that stream.
+Every step of the operation runs in libssu_gb300.so; there is no CPU or torch
+fallback.
 
 Exceptions follow the pages' conventions ("mate.mamba"): ValueError for a
 rejected argument, NotImplementedError for a capability the library does not
@@ -16,6 +18,7 @@ import ctypes
 import torch
 
 from . import _abi
+from ._alloc import empty, result, zeros
 
 _FLOAT_DT = {torch.float32: _abi.SSU_F32, torch.bfloat16: _abi.SSU_BF16,
              torch.float16: _abi.SSU_F16}
@@ -186,7 +189,7 @@ def ssu_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=
                         dst_state_batch_indices, out, rand_seed)
     batch = x.shape[0]
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        out = result(stream, x.shape, out_dtype or x.dtype, dev)
     p = _params(state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, pad_slot_id, out,
                 disable_state_update, batch, algorithm, rand_seed, philox_rounds)
     idx_dt = 0
@@ -274,7 +277,7 @@ def ssu_update_varlen(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_so
                              "state_batch_indices, dst_state_batch_indices, "
                              "num_accepted_tokens or cu_seqlens")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        out = result(stream, x.shape, out_dtype or x.dtype, dev)
     p = _params(state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, pad_slot_id, out,
                 disable_state_update, rows, algorithm, rand_seed, philox_rounds)
     meta_dt = 0
@@ -344,7 +347,7 @@ def ssu_replay_update(state, x, dt, A, B, C, x_cache, B_cache, dt_cache, ring_st
         nseqs = rows
         meta = _abi.SSU_I32
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=dev)
+        out = result(stream, x.shape, out_dtype or x.dtype, dev)
     p = _params(state, x, dt, A, B, C, D, z, dt_bias, dt_softplus, pad_slot_id, out, False, rows,
                 "auto", rand_seed, philox_rounds)
     slots, H, P, N = state.shape
@@ -378,7 +381,7 @@ def ssu_replay_update(state, x, dt, A, B, C, x_cache, B_cache, dt_cache, ring_st
         sbi_stride = sbi.stride(0)
         idx = _int_dtype(sbi, "state_batch_indices")
     if update_trackers and scratch is None:
-        scratch = torch.zeros(max(1, nseqs), dtype=torch.int32, device=dev)
+        scratch = zeros(stream, max(1, nseqs), torch.int32, dev)
     rc = _abi.ReplayCache(x_cache.data_ptr(), B_cache.data_ptr(), dt_cache.data_ptr(), R,
                           ring_start.data_ptr(), prev_num_accepted.data_ptr(),
                           min(ring_start.numel(), prev_num_accepted.numel()),
@@ -498,7 +501,7 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
         if not initial_states.is_contiguous():
             raise ValueError("initial_states must be contiguous")
     if out is None:
-        out = torch.empty_like(x)
+        out = result(stream, x.shape, x.dtype, dev)
     if out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError("out must match x's shape and dtype")
     D_per_dim = 0
@@ -521,14 +524,14 @@ def ssd_combined_fwd_varlen(x, dt, A, B, C, chunk_size, cu_seqlens, cu_chunk_seq
             raise ValueError("x, dt, A, B, C and the chunk metadata must be contiguous")
     rows = nchunks if return_intermediate_states else batch
     if states is None:
-        states = torch.empty((rows, H, P, N), dtype=state_dtype, device=dev)
+        states = result(stream, (rows, H, P, N), state_dtype, dev)
     elif (tuple(states.shape) != (rows, H, P, N) or states.dtype != state_dtype
           or not states.is_contiguous()):
         raise ValueError(f"states must be a contiguous {state_dtype} tensor of shape "
                          f"{(rows, H, P, N)}")
     need = ssd_workspace_bytes(nchunks, H, G, P, N, chunk_size)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty(stream, need, torch.uint8, dev)
     p = _abi.SSDParams()
     p.x, p.dt, p.A, p.B, p.C = (x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(),
                                 C.data_ptr())

@@ -4,9 +4,9 @@ causal convolution, the selective scan with a full A, and the moves of slots.
 Argument marshalling only: the checks that tensors describe the layout the ABI
 expects (no hidden copies, no compute) are in csrc/layer_binding.cpp, the calls
 go to ``stream``, or to the current torch stream of the tensors' device; what a
-caller does not give (``out``, a workspace) is allocated for that stream.  ValueError for a
-rejected argument, NotImplementedError for a capability the library does not
-implement, RuntimeError for a failed launch.
+caller does not give (``out``, a workspace) is allocated for that stream.
+ValueError for a rejected argument, NotImplementedError for a capability the
+library does not implement, RuntimeError for a failed launch.
 """
 from __future__ import annotations
 

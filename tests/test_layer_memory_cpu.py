@@ -57,3 +57,39 @@ def test_memory_of_the_call_is_of_its_stream(call, streams):
     del streams[:]
     CALLS[call]()
     assert streams and all(s is None for s in streams)
+
+
+def test_memory_of_the_older_calls_is_of_their_stream(streams, monkeypatch):
+    """The state update, the checkpointing update with its zeroed scratch, and the
+    SSD prefill with its workspace, up to the library's own call."""
+    from mamba2_ssm_decode_gb300 import api as old
+
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: torch.empty(*a, **kw).zero_())
+    monkeypatch.setattr(old, "_require_cuda", lambda *a: torch.device("cpu"))
+    monkeypatch.setattr(old, "ssd_workspace_bytes", lambda *a, **kw: 64)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(old._abi, "lib", Library)
+    monkeypatch.setattr(old, "_stream", lambda dev, stream: None)
+    S, H, P, N, G, R = 2, 2, 64, 64, 1, 4
+    f = lambda *shape: zeros(*shape, dtype=torch.bfloat16)  # noqa: E731
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    state, x, dt, A = zeros(4, H, P, N), f(S, H, P), zeros(S, H), zeros(H)
+    B = f(S, G, N)
+    cu = ints(0, 1, 2)
+    rows = [x, dt, A, B, B]
+    calls = [lambda **kw: old.ssu_update(state, *rows, **kw),
+             lambda **kw: old.ssu_update_varlen(state, *rows, cu_seqlens=cu, **kw),
+             lambda **kw: old.ssu_replay_update(state, *rows, f(4, H, R, P), f(4, G, R, N),
+                                                zeros(4, H, R), ints(0, 0, 0, 0), ints(0, 0, 0, 0), R,
+                                                **kw),
+             lambda **kw: old.ssd_combined_fwd_varlen(*rows, 64, cu, cu, ints(0, 1), ints(0, 1), **kw)]
+    side = types.SimpleNamespace(cuda_stream=1)
+    for call, most in zip(calls, (1, 1, 2, 3)):
+        del streams[:]
+        call(stream=side)
+        assert len(streams) == most and all(s is side for s in streams)
