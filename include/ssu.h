@@ -511,7 +511,7 @@ typedef struct ssu_conv_params {
  * cu_seqlens NULL, dense_steps 1): the rows before a sequence's first come
  * from its read slot, and the slot of step t takes the state after row t.  A
  * pad / out-of-range read slot runs from zero rows and writes no slot.  One
- * launch.  out may be x itself (not an overlapping view of it).
+ * launch.  out may be x itself (an overlapping view of it is refused).
  */
 ssu_status ssu_conv_update(const ssu_conv_params* p, int64_t nseqs, int64_t rows,
                            const void* cu_seqlens, int64_t dense_steps,
@@ -590,7 +590,9 @@ typedef struct ssu_scan_params {
   int64_t pad_slot_id;
 } ssu_scan_params;
 
-/* Decode form; sequences, rows and slots as in ssu_conv_update.  One launch. */
+/* Decode form; sequences, rows and slots as in ssu_conv_update.  One launch.
+ * out may be x, dt or z itself (not an overlapping view of one), and must not
+ * overlap B or C. */
 ssu_status ssu_scan_update(const ssu_scan_params* p, int64_t nseqs, int64_t rows,
                            const void* cu_seqlens, int64_t dense_steps,
                            const void* num_accepted_tokens, ssu_dtype meta_dtype,

@@ -200,12 +200,6 @@ struct Seqs {
   }
 };
 
-void no_overlap(const Tensor& out, std::initializer_list<const Tensor*> operands) {
-  for (const Tensor* t : operands)
-    value_if(t && t->numel() && t->data_ptr() == out.data_ptr(),
-             "out must not overlap an operand of a prompt call");
-}
-
 CUstream_st* stream_of(PyObject* o, int device) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
   return reinterpret_cast<CUstream_st*>((intptr_t)integer(o));
@@ -263,7 +257,6 @@ void conv(PyObject* const* a) {
   p.pad_slot_id = integer(a[11]);
   p.disable_state_update = PyObject_IsTrue(a[15]);
   q.check(rows);
-  if (q.form == Seqs::kPrompt) no_overlap(out, {&x});
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   done(q.call(p, rows, ssu_conv_update, ssu_conv_fwd_varlen, stream_of(a[16], dev)));
 }
@@ -339,7 +332,6 @@ void scan(PyObject* const* a) {
   p.pad_slot_id = integer(a[16]);
   p.disable_state_update = PyObject_IsTrue(a[20]);
   q.check(rows);
-  if (q.form == Seqs::kPrompt) no_overlap(out, {&x, &dt, z, &B, &C});
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   done(q.call(p, rows, ssu_scan_update, ssu_scan_fwd_varlen, stream_of(a[21], dev)));
 }

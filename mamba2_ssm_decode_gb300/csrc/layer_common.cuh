@@ -74,6 +74,28 @@ ssu_status check_prompts(bool pool, int64_t slots, int64_t nseqs, int64_t rows, 
                          ssu_dtype meta_dtype, const void* src, const void* dst,
                          ssu_dtype index_dtype, Seqs* out);
 
+// An operand's memory: in each row `pieces` runs of `bytes` bytes, piece_stride apart.
+struct Rows {
+  const void* p;
+  int64_t stride, bytes;
+  int64_t pieces = 1, piece_stride = 0;
+};
+
+// Whether two operands of `rows` rows share a byte.  Columns of one wider tensor
+// lie between each other's rows and do not.
+bool overlap(const Rows& a, const Rows& b, int64_t rows);
+
+// Rows of `n` elements, and of groups of them.
+inline Rows rows_of(const void* p, int64_t stride, int64_t n, ssu_dtype d) {
+  return Rows{p, stride * size_of(d), n * size_of(d)};
+}
+inline Rows rows_of(const void* p, int64_t stride, int64_t groups, int64_t group_stride, int64_t n,
+                    ssu_dtype d) {
+  const int64_t es = size_of(d);
+  if (groups == 1 || group_stride == n) return Rows{p, stride * es, groups * n * es};
+  return Rows{p, stride * es, n * es, groups, group_stride * es};
+}
+
 // ---------------------------------------------------------------------------
 // device: elements
 // ---------------------------------------------------------------------------

@@ -394,6 +394,18 @@ ssu_status check_conv(const ssu_conv_params* c, int64_t rows, bool pool_needed, 
   return SSU_OK;
 }
 
+// out against x: a row of x is read by the threads of several rows of out in the
+// prompt form; in the decode form out may be x itself, but no other view of it.
+ssu_status check_conv_out(const ssu_conv_params* c, int64_t rows, bool in_place) {
+  const Rows x = rows_of(c->x, c->x_row_stride, c->channels, c->io_dtype);
+  const Rows out = rows_of(c->out, c->out_row_stride, c->channels, c->io_dtype);
+  if (in_place && x.p == out.p && (rows == 1 || x.stride == out.stride)) return SSU_OK;
+  if (overlap(out, x, rows))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not overlap x%s",
+                in_place ? " (it may be the very same rows)" : "");
+  return SSU_OK;
+}
+
 }  // namespace layer
 
 #pragma GCC visibility push(default)
@@ -411,6 +423,7 @@ ssu_status ssu_conv_update(const ssu_conv_params* c, int64_t nseqs, int64_t rows
   if (st == SSU_OK)
     st = check_packed(c->slots, nseqs, rows, cu_seqlens, dense_steps, num_accepted_tokens,
                       meta_dtype, src, dst, index_dtype, &a);
+  if (st == SSU_OK) st = check_conv_out(c, rows, true);
   if (st != SSU_OK) return st;
   if (nseqs == 0 || rows == 0) return ok();
   return launched(launch_conv(c, p, a, (cudaStream_t)stream));
@@ -428,9 +441,8 @@ ssu_status ssu_conv_fwd_varlen(const ssu_conv_params* c, int64_t nseqs, int64_t 
   if (st == SSU_OK)
     st = check_prompts(c->conv_state != nullptr, c->slots, nseqs, rows, cu_seqlens, meta_dtype,
                        state_batch_indices, dst_state_batch_indices, index_dtype, &a);
+  if (st == SSU_OK) st = check_conv_out(c, rows, false);
   if (st != SSU_OK) return st;
-  if (rows > 0 && c->x == c->out)
-    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not be x: rows are read by several blocks");
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
   p.prompt = 1;

@@ -4,6 +4,75 @@
 
 namespace layer {
 
+static int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// A run of a bytes at 0 and runs of b bytes at `at` + k stride, first <= k <= last: do any meet?
+static bool run_meets(int64_t a, int64_t at, int64_t stride, int64_t b, int64_t first, int64_t last) {
+  // at + k stride in (-b, a)
+  if (stride == 0) return at > -b && at < a;
+  if (stride < 0) return run_meets(a, at, -stride, b, -last, -first);
+  int64_t lo = floor_div(-b - at, stride) + 1, hi = floor_div(a - 1 - at, stride);
+  lo = lo > first ? lo : first;
+  hi = hi < last ? hi : last;
+  return lo <= hi;
+}
+
+// One run a row on both sides, b's first at `at` of a's.
+static bool runs_overlap(const Rows& a, const Rows& b, int64_t at, int64_t rows) {
+  const int64_t ea = a.stride * (rows - 1), eb = b.stride * (rows - 1);
+  const int64_t a0 = ea < 0 ? ea : 0, a1 = (ea < 0 ? 0 : ea) + a.bytes;
+  const int64_t b0 = at + (eb < 0 ? eb : 0), b1 = at + (eb < 0 ? 0 : eb) + b.bytes;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.stride == b.stride) return run_meets(a.bytes, at, b.stride, b.bytes, 1 - rows, rows - 1);
+  for (int64_t r = 0; r < rows; ++r)   // interleaved, at other strides
+    if (run_meets(a.bytes, at - r * a.stride, b.stride, b.bytes, 0, rows - 1)) return true;
+  return false;
+}
+
+bool overlap(const Rows& a, const Rows& b, int64_t rows) {
+  if (!a.p || !b.p || rows < 1) return false;
+  const int64_t at = (int64_t)((intptr_t)b.p - (intptr_t)a.p);
+  auto from = [&](const Rows& v) {
+    return (v.stride < 0 ? v.stride * (rows - 1) : 0) +
+           (v.piece_stride < 0 ? v.piece_stride * (v.pieces - 1) : 0);
+  };
+  auto to = [&](const Rows& v) {
+    return (v.stride < 0 ? 0 : v.stride * (rows - 1)) +
+           (v.piece_stride < 0 ? 0 : v.piece_stride * (v.pieces - 1)) + v.bytes;
+  };
+  if (to(a) <= at + from(b) || at + to(b) <= from(a)) return false;
+  for (int64_t i = 0; i < a.pieces; ++i)
+    for (int64_t j = 0; j < b.pieces; ++j)
+      if (runs_overlap(a, b, at + j * b.piece_stride - i * a.piece_stride, rows)) return true;
+  return false;
+}
+
+// out against the operands that other threads read.  In place: out may be x, dt or z itself,
+// whose elements are read by the thread's warp alone, before it writes them.
+static ssu_status check_scan_out(const ssu_scan_params* c, int64_t rows, bool in_place) {
+  const Rows out = rows_of(c->out, c->out_row_stride, c->channels, c->out_dtype);
+  const struct {
+    const char* name;
+    Rows rows;
+    bool elementwise;
+  } in[] = {
+      {"x", rows_of(c->x, c->x_row_stride, c->channels, c->io_dtype), true},
+      {"dt", rows_of(c->dt, c->dt_row_stride, c->channels, c->dt_dtype), true},
+      {"z", rows_of(c->z, c->z_row_stride, c->channels, c->io_dtype), true},
+      {"B", rows_of(c->B, c->B_row_stride, c->ngroups, c->B_group_stride, c->dstate, c->io_dtype), false},
+      {"C", rows_of(c->C, c->C_row_stride, c->ngroups, c->C_group_stride, c->dstate, c->io_dtype), false},
+  };
+  for (const auto& v : in) {
+    const bool same = v.rows.p == out.p && v.rows.bytes == out.bytes &&
+                      (rows == 1 || v.rows.stride == out.stride);
+    if (in_place && v.elementwise && same) continue;
+    if (overlap(out, v.rows, rows))
+      return fail(SSU_ERR_INVALID_ARGUMENT, "out must not overlap %s%s", v.name,
+                  in_place && v.elementwise ? " (it may be the very same rows)" : "");
+  }
+  return SSU_OK;
+}
+
 static ssu_status table_args(const ssu_slot_table* t, const char* name, Table* out) {
   *out = Table{};
   if (!t || !t->indices) return SSU_OK;
@@ -215,6 +284,7 @@ ssu_status ssu_scan_update(const ssu_scan_params* c, int64_t nseqs, int64_t rows
   if (st == SSU_OK)
     st = check_packed(c->slots, nseqs, rows, cu_seqlens, dense_steps, num_accepted_tokens,
                       meta_dtype, src, dst, index_dtype, &a);
+  if (st == SSU_OK) st = check_scan_out(c, rows, true);
   if (st != SSU_OK) return st;
   if (nseqs == 0 || rows == 0) return ok();
   return launched(launch_step(c, p, a, (cudaStream_t)stream));
@@ -232,9 +302,8 @@ ssu_status ssu_scan_fwd_varlen(const ssu_scan_params* c, int64_t nseqs, int64_t 
   if (st == SSU_OK)
     st = check_prompts(c->state != nullptr, c->slots, nseqs, rows, cu_seqlens, meta_dtype,
                        state_batch_indices, dst_state_batch_indices, index_dtype, &a);
+  if (st == SSU_OK) st = check_scan_out(c, rows, false);
   if (st != SSU_OK) return st;
-  if (rows > 0 && (c->out == c->x || c->out == c->dt || c->out == c->z))
-    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not be an operand");
   if (nseqs == 0 || rows == 0) return ok();
   p.has_init = has_initial_state;
   return launched(launch_prompt(c, p, a, (cudaStream_t)stream));

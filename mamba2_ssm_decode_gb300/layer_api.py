@@ -142,7 +142,7 @@ def scan_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     [batch, dim]; dt [batch, dim] in x's dtype or fp32; A [dim, N] fp32; B, C
     [batch, groups, N] or [batch, N]; D, dt_bias [dim] fp32.  Slot vectors
     [batch] int32/int64.  Returns ``out`` [batch, dim] (x's dtype, or
-    ``out_dtype=torch.float32``)."""
+    ``out_dtype=torch.float32``; it may be x, dt or z itself)."""
     if out is None:
         out = result(stream, x.shape, out_dtype or x.dtype, x.device)
     (_module or _binding()).scan(

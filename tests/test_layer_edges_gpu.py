@@ -14,8 +14,8 @@ import torch
 
 import mamba2_ssm_decode_gb300 as ssu
 
-from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, conv_inputs, cu_of, cuda, gen,  # noqa: F401
-                             same_bits, scan_check, scan_inputs, scan_prompt)
+from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, conv_check, conv_inputs,  # noqa: F401
+                             cu_of, cuda, gen, same_bits, scan_check, scan_inputs, scan_prompt)
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +206,72 @@ def test_results_are_not_memory_in_use_on_the_current_stream():
         got = calls[name](d, side)
         assert got.data_ptr() not in places, name
     side.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# memory shared by out and operands
+# ---------------------------------------------------------------------------
+
+def test_out_in_the_columns_beside_its_operands():
+    """x, z, dt, B, C and out as columns of one tensor: no element is shared."""
+    T, dim, N = 70, 64, 16
+    c, i = conv_inputs(T, dim, 4, 2, seed=1), scan_inputs(T, dim, N, 2, seed=1)
+    w, b, pool = cuda(c, "weight", "bias", "pool")
+    wide = torch.empty(T, 2 * dim, dtype=BF16, device=DEV)
+    wide[:, :dim] = c["x"].to(DEV)
+    cu = cu_of([40, 30])
+    got = ssu.conv_fwd_varlen(wide[:, :dim], w, cu.to(DEV), bias=b, conv_state=pool, out=wide[:, dim:])
+    conv_check(c, got, pool, "silu", "columns", pool=c["pool"], nseqs=2, cu=cu, prompt=True)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    names, at = ("x", "z", "dt", "B", "C", "out"), 0
+    wide = torch.empty(T, 4 * dim + 2 * N, dtype=BF16, device=DEV)
+    for k in names:
+        n = N if k in ("B", "C") else dim
+        part = wide[:, at:at + n]
+        if k != "out":
+            part.copy_(d[k].view(T, n))
+        d[k] = part.unsqueeze(1) if k in ("B", "C") else part
+        at += n
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_fwd_varlen(d["x"], d["dt"], d["A"], d["B"], d["C"], cu.to(DEV), D=d["D"], z=d["z"],
+                              dt_bias=d["dt_bias"], dt_softplus=True, state=pool, out=d["out"])
+    scan_check(i, got, pool, "columns", pool=i["pool"], nseqs=2, cu=cu, prompt=True)
+
+
+@pytest.mark.parametrize("name", ["x", "z", "dt"])
+def test_scan_tokens_into_an_operand(name):
+    i = scan_inputs(5, 75, 16, 5, 3, seed=3)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    pool = i["pool"].to(DEV)
+    got = ssu.scan_update(pool, d["x"], d["dt"], d["A"], d["B"], d["C"], D=d["D"], z=d["z"],
+                          dt_bias=d["dt_bias"], dt_softplus=True, out=d[name])
+    assert got is d[name]
+    scan_check(i, got, pool, "in place", pool=i["pool"], nseqs=5)
+
+
+def test_overlapping_views_are_refused():
+    T, dim, N = 6, 32, 16
+    c, i = conv_inputs(T, dim, 4, 6), scan_inputs(T, dim, N, 6)
+    w, pool = cuda(c, "weight", "pool")
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    sp, cu = i["pool"].to(DEV), cu_of([2, 4]).to(DEV)
+    buf = torch.zeros(T + 1, dim, dtype=BF16, device=DEV)
+    shifted = torch.zeros(T, dim + 8, dtype=BF16, device=DEV)
+    for x, out in ((buf[:-1], buf[1:]), (buf[1:], buf[:-1]), (shifted[:, :dim], shifted[:, 8:])):
+        with pytest.raises(ValueError, match="overlap x"):
+            ssu.conv_fwd_varlen(x, w, cu, out=out)
+        with pytest.raises(ValueError, match="overlap x"):
+            ssu.conv_update(pool, x, w, out=out)
+        for k in ("x", "dt", "z"):
+            e = {**d, k: x}
+            with pytest.raises(ValueError, match=f"overlap {k}"):
+                ssu.scan_fwd_varlen(e["x"], e["dt"], e["A"], e["B"], e["C"], cu, z=e["z"], out=out)
+            with pytest.raises(ValueError, match=f"overlap {k}"):
+                ssu.scan_update(sp, e["x"], e["dt"], e["A"], e["B"], e["C"], z=e["z"], out=out)
+    for k in ("B", "C"):
+        both = torch.zeros(T, dim, dtype=BF16, device=DEV)
+        e = {**d, k: both[:, None, 16:]}
+        with pytest.raises(ValueError, match=f"overlap {k}"):
+            ssu.scan_fwd_varlen(e["x"], e["dt"], e["A"], e["B"], e["C"], cu, out=both)
+        with pytest.raises(ValueError, match=f"overlap {k}"):
+            ssu.scan_update(sp, e["x"], e["dt"], e["A"], e["B"], e["C"], out=both)
