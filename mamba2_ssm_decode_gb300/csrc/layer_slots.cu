@@ -331,6 +331,9 @@ static ssu_status compact_as(const ssu_pool* pools, int npools, int64_t slots, c
   if (entries < 0) return fail(SSU_ERR_INVALID_ARGUMENT, "entries must be >= 0");
   if ((entries > 0 && (!table || !table_out)) || !num_live)
     return fail(SSU_ERR_INVALID_ARGUMENT, "table, table_out and num_live must not be NULL");
+  if (table != table_out && overlap(rows_of(table, 0, entries, index_dtype),
+                                    rows_of(table_out, 0, entries, index_dtype), 1))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "table_out must be table or not overlap it");
   const int64_t need = workspace_bytes_of(slots, entries, table == table_out);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(SSU_ERR_INVALID_ARGUMENT,

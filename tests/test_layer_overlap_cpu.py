@@ -82,3 +82,16 @@ def test_many_rows_are_not_looked_at_one_by_one(lib):  # noqa: F811
     assert taken(lib, p, (1 << 31) - 2048, "prompt")
     p = conv(x=FAKE, x_row_stride=256, out=FAKE + 126, out_row_stride=256, conv_state=1 << 50)
     assert not taken(lib, p, (1 << 31) - 2048, "prompt")
+
+
+def test_compaction_tables_that_overlap_in_part(lib):  # noqa: F811
+    one = (_abi.Pool * 1)(_abi.Pool(FAR, 64, 64))
+
+    def refused(table, out, entries, idx):
+        st = lib.ssu_slots_compact(one, 1, 4, table, out, idx, entries, -1, FAR, None, 0, None)
+        return st == INVALID and "not overlap" in lib.ssu_last_error().decode()
+
+    assert refused(FAKE, FAKE + 4, 2, _abi.SSU_I32) and refused(FAKE + 8, FAKE, 2, _abi.SSU_I64)
+    for table, out, n, idx in ((FAKE, FAKE, 2, _abi.SSU_I32), (FAKE + 8, FAKE, 3, _abi.SSU_I64)):
+        want = table != out
+        assert refused(table, out, n, idx) == want
