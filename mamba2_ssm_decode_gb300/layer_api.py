@@ -245,7 +245,8 @@ def slots_compact(pools, table, pad_slot_id=-1, out=None, num_live=None, workspa
         num_live = result(stream, 1, torch.int32, table.device)
     if workspace is None:
         n = pools[0].shape[0] if len(pools) and pools[0].dim() else 0
-        need = slots_compact_workspace_bytes(n, table.numel(), out is table)
+        in_place = out.data_ptr() == table.data_ptr()   # as the library sees it
+        need = slots_compact_workspace_bytes(n, table.numel(), in_place)
         if need > 0:
             workspace = empty(stream, need, torch.uint8, table.device)
     (_module or _binding()).slots_compact(pools, table, out, num_live, workspace, pad_slot_id,

@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import mamba2_ssm_decode_gb300 as ssu
+from oracle import layer
 
 from .test_layer_gpu import (BF16, DEV, F16, F32, OPERANDS, _built, conv_check, conv_inputs,  # noqa: F401
                              cu_of, cuda, gen, same_bits, scan_check, scan_inputs, scan_prompt)
@@ -275,3 +276,16 @@ def test_overlapping_views_are_refused():
             ssu.scan_fwd_varlen(e["x"], e["dt"], e["A"], e["B"], e["C"], cu, out=both)
         with pytest.raises(ValueError, match=f"overlap {k}"):
             ssu.scan_update(sp, e["x"], e["dt"], e["A"], e["B"], e["C"], out=both)
+
+
+@pytest.mark.parametrize("slots", [40, 5000])
+def test_compaction_into_a_view_of_its_table(slots):
+    held = torch.randperm(slots, generator=gen(slots))[:17].int()
+    want, m, moves = layer.compact(held.numpy(), slots)
+    pool = torch.arange(slots, dtype=torch.int32)
+    p, t = pool.to(DEV), held.to(DEV)
+    out, live = ssu.slots_compact([p], t, out=t.view(17))
+    assert t.tolist() == want.tolist() and int(live) == m and out.data_ptr() == t.data_ptr()
+    for a, b in moves.items():
+        pool[b] = a
+    same_bits(p, pool)

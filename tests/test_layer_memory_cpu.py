@@ -93,3 +93,14 @@ def test_memory_of_the_older_calls_is_of_their_stream(streams, monkeypatch):
         del streams[:]
         call(stream=side)
         assert len(streams) == most and all(s is side for s in streams)
+
+
+def test_compaction_into_a_view_of_the_table_is_in_place(monkeypatch):
+    """The workspace is the one that the library asks for, which compares addresses."""
+    asked = []
+    monkeypatch.setattr(api, "slots_compact_workspace_bytes",
+                        lambda slots, n, in_place: asked.append(bool(in_place)) or 0)
+    monkeypatch.setattr(api, "_module", types.SimpleNamespace(slots_compact=lambda *a: None))
+    for out in (I32, I32.view(3), I32[:], torch.zeros_like(I32), None):
+        api.slots_compact([X], I32, out=out)
+    assert asked == [True, True, True, False, False]
