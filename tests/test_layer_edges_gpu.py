@@ -115,6 +115,91 @@ def test_scan_split_keeps_rows_of_zeros():
 
 
 # ---------------------------------------------------------------------------
+# sequences split over the CTAs of a cluster
+# ---------------------------------------------------------------------------
+
+# a mean of 505 rows and few channels select the split for every dstate; the
+# cluster's 16 CTAs then take 16 pieces of some sequences, fewer of others, and
+# one alone takes those of a few tiles
+SPLIT = [900, 1, 0, 333, 1100, 700]
+
+
+@pytest.mark.parametrize("io,dt,state", [(BF16, BF16, F32), (BF16, F32, BF16), (F16, F16, F16),
+                                         (F16, F32, F32), (F32, F32, F32), (F32, F32, BF16)])
+@pytest.mark.parametrize("N,dim,G", [(16, 160, 1), (16, 75, 3), (32, 72, 2), (64, 40, 4),
+                                     (128, 24, 1), (256, 12, 3)])
+def test_split_prompts(io, dt, state, N, dim, G):
+    """Every type, dstate and number of groups; half the sequences are fresh, in slots
+    that hold NaN."""
+    S, T = len(SPLIT), sum(SPLIT)
+    i = scan_inputs(T, dim, N, S + 2, G, io, dt, state, seed=N + dim)
+    slots = torch.randperm(S + 2, generator=gen(1))[:S]
+    init = torch.tensor([s % 2 == 1 for s in range(S)])
+    clean = i["pool"].clone()
+    for s in range(S):
+        if not init[s] and SPLIT[s]:
+            i["pool"][slots[s]] = math.nan
+    got, pool = scan_prompt(i, SPLIT, slots, init)
+    i["pool"] = clean
+    scan_check(i, got, pool, "split", pool=clean, init=init, nseqs=S, cu=cu_of(SPLIT), src=slots,
+               prompt=True)
+
+
+@pytest.mark.parametrize("variant", ["no_pool", "no_z", "no_D", "no_bias", "raw_steps", "dst", "pads",
+                                     "int64", "out_f32", "strided", "odd_strides", "two_d",
+                                     "no_table", "gaps", "big_steps"])
+@pytest.mark.parametrize("dim,N", [(48, 16), (29, 16), (24, 128)])
+def test_split_prompt_variants(variant, dim, N):
+    S, T = len(SPLIT), sum(SPLIT)
+    i = scan_inputs(T, dim, N, S + 2, 1, seed=21)
+    kw, softplus, cu = {}, True, cu_of(SPLIT)
+    slots, init = torch.tensor([5, 0, 3, 1, 6, 2]), torch.tensor([True, False, True, True, False, True])
+    if variant in ("no_z", "no_D", "no_bias"):
+        i[{"no_z": "z", "no_D": "D", "no_bias": "dt_bias"}[variant]] = None
+    if variant == "raw_steps":
+        softplus, i["dt"], i["dt_bias"] = False, i["dt"].abs() * 0.1, i["dt_bias"].abs() * 0.01
+    if variant == "big_steps":
+        i["dt"] = (40.0 * torch.randn(T, dim, generator=gen(2))).to(BF16)
+    if variant == "pads":
+        slots = torch.tensor([5, -1, 3, 99, -1, 2])
+    if variant == "gaps":
+        cu = torch.tensor([3, 880, 880, 900, 1300, 2400, T - 4])
+    if variant in ("strided", "odd_strides"):
+        pad = 16 if variant == "strided" else 5
+        for k in ("x", "z", "dt", "A"):
+            i[k] = torch.cat([i[k], i[k][:, :pad]], 1)[:, :i[k].shape[1]]
+        for k in ("B", "C"):
+            i[k] = torch.cat([i[k], i[k][:, :, :pad]], 2)[:, :, :N]
+    if variant == "two_d":
+        i["B"], i["C"] = i["B"][:, 0], i["C"][:, 0]
+    seqs = dict(nseqs=S, cu=cu, prompt=True)
+    if variant == "no_pool":
+        i["pool"] = None
+    else:
+        seqs.update(pool=i["pool"], init=init)
+        kw["has_initial_state"] = init.to(DEV)
+        idx = torch.int64 if variant == "int64" else torch.int32
+        if variant != "no_table":
+            seqs["src"] = slots
+            kw["state_batch_indices"] = slots.to(idx).to(DEV)
+        if variant == "dst":
+            seqs["dst"] = torch.tensor([6, 4, 2, -1, 0, 7])
+            kw["dst_state_batch_indices"] = seqs["dst"].int().to(DEV)
+    if variant == "out_f32":
+        kw["out_dtype"] = F32
+    else:
+        kw["out"] = torch.full((T, dim), 7.0, dtype=BF16, device=DEV)
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    pool = None if i["pool"] is None else i["pool"].to(DEV)
+    meta = torch.int64 if variant == "int64" else torch.int32
+    got = ssu.scan_fwd_varlen(d["x"], d["dt"], d["A"], d["B"], d["C"], cu.to(meta).to(DEV), D=d["D"],
+                              z=d["z"], dt_bias=d["dt_bias"], dt_softplus=softplus, state=pool, **kw)
+    scan_check(i, got, pool, variant, softplus=softplus, **seqs)
+    if variant == "gaps":   # rows of no sequence
+        assert bool((got[:3] == 7.0).all()) and bool((got[-4:] == 7.0).all())
+
+
+# ---------------------------------------------------------------------------
 # streams
 # ---------------------------------------------------------------------------
 
