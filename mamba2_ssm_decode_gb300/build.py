@@ -69,9 +69,15 @@ def _compile(src, ptxas_info):
     return obj, r.stderr
 
 
-def _compile_binding():
+def _torch():
+    """Where torch is installed, or None.  The library needs none: only the CPython
+    module is built with torch's headers, and is left out without them."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _compile_binding(torch):
     """csrc/layer_binding.cpp to an object file (linked once the library is there)."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     obj = os.path.join(BUILD, "layer_binding.o")
     include = [os.path.join(torch, "include"), os.path.join(cuda, "include"),
@@ -84,8 +90,7 @@ def _compile_binding():
     return obj
 
 
-def _link_binding(obj):
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _link_binding(torch, obj):
     tmp = BINDING + f".{os.getpid()}.tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libssu_gb300.so", "-Wl,-rpath,$ORIGIN",
            f"-L{os.path.join(torch, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
@@ -102,17 +107,18 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     deps = _deps()
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
     todo = [s for s, o in zip(srcs, objs) if force or ptxas_info or _stale(o, [s, *deps])]
+    torch = _torch()
     binding = os.path.join(BUILD, "layer_binding.o")
-    bind = force or _stale(binding, [BINDING_SRC, HEADER, os.path.abspath(__file__)])
+    bind = torch is not None and (
+        force or _stale(binding, [BINDING_SRC, HEADER, os.path.abspath(__file__)]))
+    bound = None
     if todo or bind:
         jobs = len(todo) + bind
         with cf.ThreadPoolExecutor(max_workers=min(jobs, os.cpu_count() or 4)) as ex:
-            bound = ex.submit(_compile_binding) if bind else None
+            bound = ex.submit(_compile_binding, torch) if bind else None
             for obj, log in ex.map(lambda s: _compile(s, ptxas_info), todo):
                 if verbose or ptxas_info:
                     print(f"== {os.path.basename(obj)}\n{log}", file=sys.stderr)
-            if bound:
-                bound.result()
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", *LINK_FLAGS, "-o", tmp, *objs]
@@ -120,8 +126,13 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if torch is None:
+        print("torch is not installed: built the C library alone", file=sys.stderr)
+        return LIB
+    if bound:
+        bound.result()
     if force or bind or not os.path.exists(BINDING):
-        _link_binding(binding)
+        _link_binding(torch, binding)
     return LIB
 
 
