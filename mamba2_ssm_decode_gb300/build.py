@@ -27,6 +27,7 @@ LIB = os.path.join(PKG, "libssu_gb300.so")
 HEADER = os.path.join(ROOT, "include", "ssu.h")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING = os.path.join(PKG, "_layer_binding.so")
+STAMP = os.path.join(BUILD, "layer_binding.torch")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -76,6 +77,12 @@ def _torch():
     return spec.submodule_search_locations[0] if spec else None
 
 
+def _torch_is(torch):
+    """What the module's object file is good for: this torch, at this place."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return f"{torch}\n{f.read()}"
+
+
 def _compile_binding(torch):
     """csrc/layer_binding.cpp to an object file (linked once the library is there)."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -87,7 +94,16 @@ def _compile_binding(torch):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    with open(STAMP, "w") as f:
+        f.write(_torch_is(torch))
     return obj
+
+
+def _binding_stale(torch, obj):
+    if _stale(obj, [BINDING_SRC, HEADER, os.path.abspath(__file__)]) or not os.path.exists(STAMP):
+        return True
+    with open(STAMP) as f:
+        return f.read() != _torch_is(torch)
 
 
 def _link_binding(torch, obj):
@@ -109,8 +125,7 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
     todo = [s for s, o in zip(srcs, objs) if force or ptxas_info or _stale(o, [s, *deps])]
     torch = _torch()
     binding = os.path.join(BUILD, "layer_binding.o")
-    bind = torch is not None and (
-        force or _stale(binding, [BINDING_SRC, HEADER, os.path.abspath(__file__)]))
+    bind = torch is not None and (force or _binding_stale(torch, binding))
     bound = None
     if todo or bind:
         jobs = len(todo) + bind
@@ -131,7 +146,7 @@ def build(force: bool = False, ptxas_info: bool = False, verbose: bool = False) 
         return LIB
     if bound:
         bound.result()
-    if force or bind or not os.path.exists(BINDING):
+    if force or _stale(BINDING, [binding, LIB]):
         _link_binding(torch, binding)
     return LIB
 

@@ -60,3 +60,26 @@ def test_the_library_is_built_where_the_module_fails(tree):
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         b.build()
     assert os.path.exists(b.LIB)
+
+
+@pytest.mark.parametrize("what", ["binding", "lib"])
+def test_a_failed_link_is_made_up_for(tree, what):
+    """After a new object file and a link that failed, an old module does not stay."""
+    b.build()
+    tree.fail, tree.made = {what}, []
+    with pytest.raises(RuntimeError, match="link"):
+        b.build(force=True)
+    tree.fail, tree.made = set(), []
+    b.build()
+    assert "binding" in tree.made
+    tree.made = []
+    b.build()
+    assert tree.made == []
+
+
+def test_another_torch_compiles_the_module_again(tree):
+    b.build()
+    tree.made = []
+    (tree.torch / "version.py").write_text("__version__ = '2'")
+    b.build()
+    assert tree.made == ["layer_binding.o", "binding"]
