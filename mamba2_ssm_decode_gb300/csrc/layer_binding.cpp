@@ -61,6 +61,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{nullptr, ""};
+  return v;
+}
+
 int one_device(std::initializer_list<const Tensor*> ts) {
   int d = -1;
   for (const Tensor* t : ts) {
@@ -255,7 +261,7 @@ void conv(PyObject* const* a) {
   p.out_row_stride = rows2(out, "out", rows, C);
   p.activation = (int)integer(a[5]);
   p.pad_slot_id = integer(a[11]);
-  p.disable_state_update = PyObject_IsTrue(a[15]);
+  p.disable_state_update = truth(a[15]);
   q.check(rows);
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   done(q.call(p, rows, ssu_conv_update, ssu_conv_fwd_varlen, stream_of(a[16], dev)));
@@ -328,9 +334,9 @@ void scan(PyObject* const* a) {
   p.C_group_stride = nd == 3 ? C.stride(1) : N;
   p.A = static_cast<const float*>(A.data_ptr());
   p.A_row_stride = A.stride(0);
-  p.dt_softplus = PyObject_IsTrue(a[10]);
+  p.dt_softplus = truth(a[10]);
   p.pad_slot_id = integer(a[16]);
-  p.disable_state_update = PyObject_IsTrue(a[20]);
+  p.disable_state_update = truth(a[20]);
   q.check(rows);
   const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
   done(q.call(p, rows, ssu_scan_update, ssu_scan_fwd_varlen, stream_of(a[21], dev)));

@@ -374,3 +374,23 @@ def test_compaction_into_a_view_of_its_table(slots):
     for a, b in moves.items():
         pool[b] = a
     same_bits(p, pool)
+
+
+def test_flags_without_a_truth_value():
+    """The caller's own error, and nothing runs."""
+    c, i = conv_inputs(3, 32, 4, 3), scan_inputs(3, 32, 16, 3)
+    x, w, pool = cuda(c, "x", "weight", "pool")
+    d = dict(zip(OPERANDS, cuda(i, *OPERANDS)))
+    args, sp = [d[k] for k in ("x", "dt", "A", "B", "C")], i["pool"].to(DEV)
+
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    for call in (lambda v: ssu.conv_update(pool, x, w, disable_state_update=v),
+                 lambda v: ssu.scan_update(sp, *args, disable_state_update=v),
+                 lambda v: ssu.scan_update(sp, *args, dt_softplus=v)):
+        with pytest.raises(KeyError, match="neither"):
+            call(Neither())
+    same_bits(pool, c["pool"])
+    same_bits(sp, i["pool"])
