@@ -81,9 +81,11 @@ __device__ __forceinline__ void conv_row(IT* out, const float2 (&xs)[W][(V + 1) 
 // of up to ROWS rows (the rows, and the slots that take the state after them)
 // is asked for at once, beside the slot's rows.  ROWS 1: one row a sequence.
 // Bound by the latency of three dependent loads (count, slot, rows) in two or
-// three waves of CTAs: 640 drafted rows x 5376 channels take 14 us for 43 MB.
-// Eight CTAs an SM: 1024 one-row sequences 22.5 us where the 6 that registers
-// would leave take 26.
+// three waves of CTAs: 640 drafted rows x 5376 channels take 14.4 us for 43 MB.
+// Eight CTAs an SM (64 registers, at which the drafted instance spills 28
+// bytes): 1024 one-row sequences 22.5 us where the 6 that registers would leave
+// take 26; with drafted rows the two are alike (256 sequences 12.5 us both, 1024
+// sequences 42.3 and 43.3, on inputs partly in L2).
 constexpr int kStepThreads = 128;
 
 template <class IT, class WT, int W, int V, int ROWS>

@@ -58,8 +58,9 @@ struct ScanArgs {
 // and one wave of CTAs keeps loads in flight throughout.  Bound by HBM: the
 // state is read once a sequence and written once a row.  512 tokens x 5120
 // channels x 16, fp32 state: 56.5 us, 357 MB, 6.3 TB/s; with drafted rows the
-// chain of a row (softplus, shuffles, exponentials) shows: 128 sequences of 1
-// to 4 rows take 50 us for 147 MB.
+// chain of a row (softplus, shuffles, exponentials) shows, and the next
+// sequence's state is asked for only in a sequence's last row: 128 sequences of 1
+// to 4 rows take 46 us for 160 MB.
 // ---------------------------------------------------------------------------
 constexpr int kScanWarps = 4;
 
@@ -67,11 +68,13 @@ template <class ST, int N>
 struct ScanStep {
   using L = ssu::RowLayout<ST, N>;
   // State values per thread: 16 of the short rows, 32 of those whose lanes own
-  // more (64 tokens x 5120 channels x 128, fp32: 74 us with 32, 95 us with 16),
+  // more (64 tokens x 5120 channels x 128, fp32: 72 us with 32, 95 us with 16),
   // and the CTAs an SM that they leave room for (512 tokens x 5120 channels x
   // 16: fp32 state 65 us with four, bf16 47 us; three take 70 and 70, five 67
-  // and 53.  32 tokens x 5120 x 256: 90 us with three, some registers spilled;
-  // two take 109).
+  // and 53).  The long rows have three, some registers spilled: with 16-bit x, B
+  // and C 64 tokens x 5120 x 128 take 72 us where two take 109, 32 tokens x 256 81
+  // us for 107.  fp32 rows pay more for the spills than two CTAs would cost them:
+  // 103 us for 79, and 133 us for 88.
   static constexpr int MOST = L::EPL > 4 ? 32 : 16;
   static constexpr int FIT = MOST / L::EPL > 1 ? MOST / L::EPL : 1;
   static constexpr int U = L::LPR < FIT ? L::LPR : FIT;

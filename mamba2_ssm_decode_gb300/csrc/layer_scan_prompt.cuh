@@ -13,8 +13,8 @@
 // cycles each: 18 to 21), 4 exponentials (16 cycles of the special-function
 // pipe), two shared memory reads of B and C for two channels and two of dt' and
 // dt' x, and a quarter of a staged value.  So neither HBM nor one pipe alone
-// bounds it: at 9001 x 4096 rows x 16 in 16 sequences, 194 us, the fp32 pipe is
-// busy 52 % of the time, the special-function pipe 39 %, shared memory 57 %, the
+// bounds it: at 9001 x 4096 rows x 16 in 16 sequences, 192 us, the fp32 pipe is
+// busy 52 % of the time, the special-function pipe 39 %, shared memory 58 %, the
 // issue slots 66 %; 36 cycles a unit in the full waves, the rest is the tail.
 #pragma once
 
@@ -353,8 +353,8 @@ __device__ __forceinline__ void scan_rows(const ScanArgs& p,
 //     h_leave = exp(A sum dt') h_enter + h_from_zero;
 // the first meanwhile finishes its piece from the true state.  Then each CTA
 // folds the pieces in front of its own, read from its neighbours' shared
-// memory, and runs its piece for the outputs.  The exponentials are paid twice
-// over (K - 1) / K of the rows.
+// memory, and runs its piece for the outputs.  All pieces but the first and the
+// last pay for their exponentials twice: 1.7 passes over the rows with 7 pieces.
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
 }
@@ -622,9 +622,15 @@ cudaError_t launch_scan_prompt(const ScanArgs& p, const Seqs& a,
 }
 
 // Two channels a thread share what is read of B and C.  Four columns of each
-// leave 126 registers and 16 warps an SM; eight (one wave of 512 CTAs for 1024)
+// leave 125 registers and 16 warps an SM; eight (one wave of 512 CTAs for 1024)
 // take 207 us where four take 202, four channels of four 225.  The long rows
 // have eight: half the lanes to a channel, half the sums to reduce.
+//
+// Four CTAs an SM serve every type and dstate.  Three, with 168 registers, take as
+// long within 2 % for 16-bit rows of dstate 32 to 256, more for an odd number of
+// channels (336 us for 296) and for the split of 6001 x 1024 x 128 in fp32 (892 us
+// for 732), less for other fp32 rows (9001 x 4096 x 16 196 us for 226, 2001 x 4096
+// x 128 488 for 512, where four spill 1.5 KB, 1001 x 4096 x 256 720 for 765).
 template <class IT, class DT>
 cudaError_t launch_scan_prompt_n(int N, const ScanArgs& p, const Seqs& a,
                                  cudaStream_t stream) {
