@@ -303,7 +303,8 @@ __device__ __forceinline__ float softplus_sum(float a, float b) {
 }
 
 // ... of V sums at once.  What a sum lost is below 2^-21 of the result unless v
-// is below -16 (or not finite): then all are done with it.
+// is below -16 (or not finite): only then is it put back, for each sum by itself,
+// so that no channel's bits depend on its neighbours'.
 template <int V>
 __device__ __forceinline__ void softplus_sums(float* a, const float* b) {
   float v[V];
@@ -318,7 +319,11 @@ __device__ __forceinline__ void softplus_sums(float* a, const float* b) {
     for (int i = 0; i < V; ++i) a[i] = softplus_from(v[i], 0.0f);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = softplus_sum(a[i], b[i]);
+    for (int i = 0; i < V; ++i) {
+      const float part = v[i] - a[i];
+      const float lost = (a[i] - (v[i] - part)) + (b[i] - part);
+      a[i] = softplus_from(v[i], v[i] > -16.0f || v[i] == -INFINITY ? 0.0f : lost);
+    }
   }
 }
 

@@ -114,6 +114,57 @@ def test_scan_split_keeps_rows_of_zeros():
     scan_check(i, got, pool, "zeros", softplus=False, pool=i["pool"], nseqs=1, cu=cu_of([T]), prompt=True)
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("name", ["x", "dt", "z", "B", "C"])
+@pytest.mark.parametrize("lens,at", [([9, 21, 5], 17), ([700, 401, 333], 950), ([700, 401, 333], 1100)])
+def test_scan_bad_values_stay_where_they_belong(lens, at, name, bad):
+    """A NaN or an infinity in one row, whole sequences and split ones, the last row of
+    one among them: earlier rows, other channels (groups for B and C) and other
+    sequences keep their bits."""
+    dim, N, G, S = 48, 16, 2, len(lens)
+    i = scan_inputs(sum(lens), dim, N, S, G, BF16, F32, F32, seed=4)
+    clean, held = scan_prompt(i, lens)
+    i[name] = i[name].clone()
+    c = 7
+    if name in ("B", "C"):
+        i[name][at, 1, 3] = bad
+        touched = torch.arange(dim) >= dim // 2
+    else:
+        i[name][at, c] = bad
+        touched = torch.arange(dim) == c
+    got, pool = scan_prompt(i, lens)
+    q = next(s for s in range(S) if sum(lens[:s + 1]) > at)
+    end = sum(lens[:q + 1]) if name in ("x", "dt", "B") else at + 1   # z and C: that row alone
+    hit = torch.zeros(got.shape, dtype=torch.bool)
+    hit[at:end, touched] = True
+    same_bits(got.cpu()[~hit], clean.cpu()[~hit])
+    assert not torch.equal(got.cpu()[hit], clean.cpu()[hit])
+    hit = torch.zeros(pool.shape, dtype=torch.bool)
+    if name in ("x", "dt", "B"):
+        hit[q, touched] = True
+        assert not torch.equal(pool.cpu()[hit], held.cpu()[hit])
+    same_bits(pool.cpu()[~hit], held.cpu()[~hit])
+
+
+@pytest.mark.parametrize("C", [64, 37])
+def test_conv_bad_values_stay_where_they_belong(C):
+    """NaN in one element: its channel's next W rows of the same sequence, no others."""
+    lens, at, W = [40, 90, 5], 127, 4
+    i = conv_inputs(sum(lens), C, W, 3, seed=4)
+    cu = cu_of(lens).to(DEV)
+    x, w, b, held = cuda(i, "x", "weight", "bias", "pool")
+    clean = ssu.conv_fwd_varlen(x, w, cu, bias=b, conv_state=held)
+    x[at, 5] = math.nan
+    pool = i["pool"].to(DEV)
+    got = ssu.conv_fwd_varlen(x, w, cu, bias=b, conv_state=pool)
+    bad = torch.isnan(got)
+    assert bad.nonzero().tolist() == [[r, 5] for r in range(at, 130)]
+    same_bits(got[~bad], clean[~bad])
+    bad = torch.isnan(pool)
+    assert bad.nonzero().tolist() == [[1, 0, 5]]
+    same_bits(pool[~bad], held[~bad])
+
+
 # ---------------------------------------------------------------------------
 # sequences split over the CTAs of a cluster
 # ---------------------------------------------------------------------------
