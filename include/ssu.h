@@ -662,6 +662,187 @@ ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, c
                              int64_t workspace_bytes, struct CUstream_st* stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrent layer whose state
+ * is the decayed sum of outer products of values and keys.  For value head h,
+ * group g = h / (nheads / ngroups) and row r of a sequence:
+ *   S[h][p][n] <- exp(ld) S[h][p][n] + v[r][h][p] k[r][g][n]
+ *   out[r][h][p] = scale sum_n S[h][p][n] q[r][g][n]
+ * in fp32; a state is rounded (to nearest even) only where it is stored.
+ *
+ * state      [slots, nheads, dv, dk], contiguous, 16-byte aligned, F32 / BF16 /
+ *            F16 (the layout of ssu_params' state with headdim dv, dstate dk);
+ *            dk 16, 32, 64, 128 or 256, dv up to 256, up to 4096 heads.
+ * io_dtype   F32, BF16 or F16: q, k, v and out.
+ * q, k       [rows, ngroups, dk], element (r, g, n) at r * row_stride +
+ *            g * group_stride + n (strides in elements).
+ * v, out     [rows, nheads, dv], likewise; out must not overlap an operand.
+ * log_decay  ld, fp32, element (r, h) at r * log_decay_row_stride +
+ *            h * log_decay_head_stride (a row stride of 0: one value per head),
+ *            or NULL: no decay.  -infinity forgets what came before.
+ * disable_state_update  1: no slot is written (decode form).
+ */
+typedef struct ssu_linattn_params {
+  void* state;
+  ssu_dtype state_dtype;
+  int64_t slots, nheads, ngroups, dv, dk;
+  ssu_dtype io_dtype;
+  const void* q;
+  int64_t q_row_stride, q_group_stride;
+  const void* k;
+  int64_t k_row_stride, k_group_stride;
+  const void* v;
+  int64_t v_row_stride, v_head_stride;
+  void* out;
+  int64_t out_row_stride, out_head_stride;
+  const float* log_decay;
+  int64_t log_decay_row_stride, log_decay_head_stride;
+  float scale;
+  int disable_state_update;
+  int64_t pad_slot_id;
+} ssu_linattn_params;
+
+/* Decode form; sequences, rows and slots as in ssu_conv_update.  One launch. */
+ssu_status ssu_linattn_update(const ssu_linattn_params* p, int64_t nseqs, int64_t rows,
+                              const void* cu_seqlens, int64_t dense_steps,
+                              const void* num_accepted_tokens, ssu_dtype meta_dtype,
+                              const ssu_slot_table* src, const ssu_slot_table* dst,
+                              ssu_dtype index_dtype, struct CUstream_st* stream);
+
+/* Bytes of workspace ssu_linattn_fwd_varlen needs for these sizes (0: none; -1
+ * for a negative size). */
+int64_t ssu_linattn_workspace_bytes(int64_t rows, int64_t nseqs, int64_t nheads, int64_t dv,
+                                    int64_t dk, ssu_dtype io_dtype);
+
+/*
+ * Prompt form; arguments and rules as in ssu_conv_fwd_varlen (state may be
+ * NULL).  workspace: device memory of ssu_linattn_workspace_bytes(...) bytes,
+ * 16-byte aligned; nothing in it need be kept between calls, and calls that
+ * share it must not overlap.
+ */
+ssu_status ssu_linattn_fwd_varlen(const ssu_linattn_params* p, int64_t nseqs, int64_t rows,
+                                  const void* cu_seqlens, ssu_dtype meta_dtype,
+                                  const void* state_batch_indices,
+                                  const void* dst_state_batch_indices, ssu_dtype index_dtype,
+                                  const uint8_t* has_initial_state, void* workspace,
+                                  int64_t workspace_bytes, struct CUstream_st* stream);
+
+/*
+ * Verification of drafted tokens: what the next call's num_accepted_tokens and
+ * input tokens are.  A sequence with n drafts has n + 1 rows of target_probs:
+ * row j holds the target's probabilities at draft j's place, row n those after
+ * the last draft.  With p = target_probs[row j][draft j] and q =
+ * draft_probs[s][j][draft j] (1 where draft_probs is NULL: certain drafts),
+ * drafts are taken in order while uniform[s][j] q < p, decided exactly.  The
+ * next token comes from what is left of the deciding row -- max(p - q, 0) where
+ * a draft was turned down (without draft_probs: p but for the draft), p after
+ * the last -- by the inverse of its cumulative sum at uniform[s][drafts]: each
+ * token weighs round(r 2^44), r clamped to [0, 1] (NaN weighs nothing), W is
+ * the weights' sum, and the token is the first whose running sum exceeds
+ * floor(u W).  Where nothing is left (W = 0) the row's p itself takes its place;
+ * where that weighs nothing either, the token is -1.
+ *
+ * target_probs  [rows, vocab], probs_dtype (F32 / BF16 / F16), unit stride along
+ *               the vocabulary; vocab up to 2^19.
+ * draft_probs   [nseqs, drafts, vocab], likewise, or NULL.
+ * draft_tokens  [nseqs, drafts], token_dtype (I32 / I64); a draft outside the
+ *               vocabulary is turned down.
+ * uniform       [nseqs, drafts + 1], fp32 in [0, 1): for each draft, and, last,
+ *               for the token that is drawn.
+ * cu_seqlens    [nseqs + 1] row starts (meta_dtype), clamped to [0, rows]; a
+ *               sequence of n + 1 rows has n drafts (at most `drafts`), one of
+ *               none has nothing.  NULL: drafts + 1 rows each.
+ * greedy        [nseqs] bytes, or NULL (all 0): 1 takes drafts while they are
+ *               their row's largest value (the lowest token of equal ones), and
+ *               then that token; any scores will do as target_probs.
+ * out           [nseqs, drafts + 1], token_dtype: the drafts taken, the next
+ *               token, then -1.
+ * num_accepted  [nseqs], count_dtype (I32 / I64): tokens in out, drafts taken
+ *               plus one (0 for a sequence without rows): the
+ *               num_accepted_tokens of the next packed call.
+ * Up to 65535 sequences and 4096 drafts each.  One launch.
+ */
+typedef struct ssu_drafts_params {
+  const void* target_probs;
+  ssu_dtype probs_dtype;
+  int64_t rows, vocab, target_row_stride;
+  const void* draft_probs;
+  int64_t draft_seq_stride, draft_step_stride;
+  const void* draft_tokens;
+  ssu_dtype token_dtype;
+  int64_t draft_tokens_seq_stride;
+  int64_t nseqs, drafts;
+  const float* uniform;
+  int64_t uniform_seq_stride;
+  const void* cu_seqlens;
+  ssu_dtype meta_dtype;
+  const uint8_t* greedy;
+  void* out;
+  int64_t out_seq_stride;
+  void* num_accepted;
+  ssu_dtype count_dtype;
+} ssu_drafts_params;
+
+ssu_status ssu_drafts_verify(const ssu_drafts_params* p, struct CUstream_st* stream);
+
+/*
+ * The maps of a packed batch of prompts, from the lengths of its sequences
+ * (all index_dtype, I32 / I64, contiguous; no two outputs may overlap).
+ *   lens          [nseqs] tokens of each sequence in this call (0 is fine, below
+ *                 zero counts as 0).  Together they should be at most `rows`;
+ *                 what is beyond is cut off.
+ *   context_lens  [nseqs] tokens of each sequence before this call, or NULL (0).
+ *   cu_seqlens    [nseqs + 1] row starts.
+ *   Chunks as ssd_combined_fwd_varlen takes them: a sequence's end at multiples
+ *   of chunk_size of its own positions (so that a continued one's first chunk
+ *   closes the one it was left in), and a sequence without tokens has one empty
+ *   chunk, which carries its state through.
+ *   cu_chunk_seqlens [max_chunks + 1], seq_idx [max_chunks]; chunks from
+ *                 num_chunks [1] on are empty ones of the last sequence.
+ *   last_chunk_indices [nseqs]
+ *   has_initial_state  [nseqs] bytes: context_lens > 0.
+ *   row_seq, row_pos   [rows] or NULL: a row's sequence and position (context
+ *                 included); -1 behind the last sequence.
+ * max_chunks must be at least rows / chunk_size + nseqs (2 nseqs with
+ * context_lens), which no lengths exceed.  At most SSU_PROMPT_MAPS_MAX_SEQS
+ * sequences, chunk_size at most 2^20.  One launch.
+ */
+#define SSU_PROMPT_MAPS_MAX_SEQS 16384
+
+typedef struct ssu_prompt_maps_params {
+  const void* lens;
+  const void* context_lens;
+  ssu_dtype index_dtype;
+  int64_t nseqs, rows, chunk_size, max_chunks;
+  void* cu_seqlens;
+  void* cu_chunk_seqlens;
+  void* seq_idx;
+  void* last_chunk_indices;
+  uint8_t* has_initial_state;
+  void* num_chunks;
+  void* row_seq;
+  void* row_pos;
+} ssu_prompt_maps_params;
+
+ssu_status ssu_prompt_maps(const ssu_prompt_maps_params* p, struct CUstream_st* stream);
+
+/*
+ * Fill a slot table [nseqs, steps] (index_dtype, contiguous): row s is to hold
+ * counts[s] slots (cut to [0, steps]).  Its valid entries among the first
+ * counts[s] stay; the others take the lowest slots that no such entry of the
+ * table holds (nor pad_slot_id), in ascending order along the table; entries
+ * from counts[s] on become pad_slot_id, and the slots they held are free.
+ *   table_out    the new table; may be `table`.
+ *   fresh        [nseqs, steps]: the slots newly given, pad_slot_id elsewhere
+ *                (what ssu_slots_clear takes).
+ *   num_missing  entries that got none because no slot was left (pad_slot_id).
+ * Up to 2^20 slots and 2^24 entries.  One launch.
+ */
+ssu_status ssu_slots_assign(const void* table, const void* counts, ssu_dtype index_dtype,
+                            int64_t nseqs, int64_t steps, int64_t slots, int64_t pad_slot_id,
+                            void* table_out, void* fresh, int32_t* num_missing,
+                            struct CUstream_st* stream);
+
+/*
  * Bits of the device-side error word (values, not bit positions).
  */
 #define SSU_DEVICE_ERR_COPY_TIMEOUT 1u    /* a state tile copy never landed */

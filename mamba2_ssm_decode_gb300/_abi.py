@@ -124,7 +124,51 @@ class Pool(ctypes.Structure):
     _fields_ = [("data", _c_p), ("slot_bytes", _c_i64), ("slot_stride_bytes", _c_i64)]
 
 
+class LinattnParams(ctypes.Structure):
+    """struct ssu_linattn_params."""
+
+    _fields_ = [
+        ("state", _c_p), ("state_dtype", _c_int),
+        ("slots", _c_i64), ("nheads", _c_i64), ("ngroups", _c_i64), ("dv", _c_i64), ("dk", _c_i64),
+        ("io_dtype", _c_int),
+        ("q", _c_p), ("q_row_stride", _c_i64), ("q_group_stride", _c_i64),
+        ("k", _c_p), ("k_row_stride", _c_i64), ("k_group_stride", _c_i64),
+        ("v", _c_p), ("v_row_stride", _c_i64), ("v_head_stride", _c_i64),
+        ("out", _c_p), ("out_row_stride", _c_i64), ("out_head_stride", _c_i64),
+        ("log_decay", _c_p), ("log_decay_row_stride", _c_i64), ("log_decay_head_stride", _c_i64),
+        ("scale", ctypes.c_float), ("disable_state_update", _c_int), ("pad_slot_id", _c_i64),
+    ]
+
+
+class DraftsParams(ctypes.Structure):
+    """struct ssu_drafts_params."""
+
+    _fields_ = [
+        ("target_probs", _c_p), ("probs_dtype", _c_int),
+        ("rows", _c_i64), ("vocab", _c_i64), ("target_row_stride", _c_i64),
+        ("draft_probs", _c_p), ("draft_seq_stride", _c_i64), ("draft_step_stride", _c_i64),
+        ("draft_tokens", _c_p), ("token_dtype", _c_int), ("draft_tokens_seq_stride", _c_i64),
+        ("nseqs", _c_i64), ("drafts", _c_i64),
+        ("uniform", _c_p), ("uniform_seq_stride", _c_i64),
+        ("cu_seqlens", _c_p), ("meta_dtype", _c_int), ("greedy", _c_p),
+        ("out", _c_p), ("out_seq_stride", _c_i64), ("num_accepted", _c_p), ("count_dtype", _c_int),
+    ]
+
+
+class PromptMapsParams(ctypes.Structure):
+    """struct ssu_prompt_maps_params."""
+
+    _fields_ = [
+        ("lens", _c_p), ("context_lens", _c_p), ("index_dtype", _c_int),
+        ("nseqs", _c_i64), ("rows", _c_i64), ("chunk_size", _c_i64), ("max_chunks", _c_i64),
+        ("cu_seqlens", _c_p), ("cu_chunk_seqlens", _c_p), ("seq_idx", _c_p),
+        ("last_chunk_indices", _c_p), ("has_initial_state", _c_p), ("num_chunks", _c_p),
+        ("row_seq", _c_p), ("row_pos", _c_p),
+    ]
+
+
 SLOTS_MAX_POOLS = 256   # SSU_SLOTS_MAX_POOLS
+PROMPT_MAPS_MAX_SEQS = 16384   # SSU_PROMPT_MAPS_MAX_SEQS
 
 
 _lock = threading.Lock()
@@ -167,6 +211,16 @@ def lib() -> ctypes.CDLL:
                            ("ssu_scan_update", decode), ("ssu_scan_fwd_varlen", prompt)):
             f = getattr(L, name)
             f.restype, f.argtypes = _c_int, args
+        L.ssu_linattn_update.restype, L.ssu_linattn_update.argtypes = _c_int, decode
+        L.ssu_linattn_fwd_varlen.restype = _c_int
+        L.ssu_linattn_fwd_varlen.argtypes = prompt[:-1] + [_c_p, _c_i64, _c_p]
+        L.ssu_linattn_workspace_bytes.restype = _c_i64
+        L.ssu_linattn_workspace_bytes.argtypes = [_c_i64] * 5 + [_c_int]
+        L.ssu_drafts_verify.restype, L.ssu_drafts_verify.argtypes = _c_int, [_c_p, _c_p]
+        L.ssu_prompt_maps.restype, L.ssu_prompt_maps.argtypes = _c_int, [_c_p, _c_p]
+        L.ssu_slots_assign.restype = _c_int
+        L.ssu_slots_assign.argtypes = [_c_p, _c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_i64,
+                                       _c_p, _c_p, _c_p, _c_p]
         L.ssu_slots_copy.restype = _c_int
         L.ssu_slots_copy.argtypes = [_c_p, _c_int, _c_i64, _c_p, _c_p, _c_int,
                                      _c_i64, _c_i64, _c_p]

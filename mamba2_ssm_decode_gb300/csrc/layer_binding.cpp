@@ -342,6 +342,205 @@ void scan(PyObject* const* a) {
   done(q.call(p, rows, ssu_scan_update, ssu_scan_fwd_varlen, stream_of(a[21], dev)));
 }
 
+// Row and inner strides of a [rows, n, dim] operand with unit dim stride.
+void rows3(const Tensor& t, const char* name, int64_t rows, int64_t n, int64_t dim, int64_t* rs,
+           int64_t* is) {
+  value_if(t.dim() != 3 || t.size(0) != rows || t.size(1) != n || t.size(2) != dim, name,
+           " must be [", rows, ", ", n, ", ", dim, "], got ", t.sizes());
+  value_if(dim > 1 && t.stride(2) != 1, name, " must be contiguous along its last dimension, got ",
+           t.strides());
+  *rs = t.stride(0);
+  *is = t.stride(1);
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
+  return v;
+}
+
+// linattn(form, state, q, k, v, log_decay, scale, cu, na, src, dst, init, pad, out, nseqs, steps,
+//         disable, workspace, stream)
+void linattn(PyObject* const* a) {
+  const Tensor* state = tensor(a[1], "state");
+  const Tensor &q = needed(a[2], "q"), &k = needed(a[3], "k"), &v = needed(a[4], "v");
+  const Tensor &out = needed(a[13], "out"), *ld = tensor(a[5], "log_decay");
+  const Tensor* ws = tensor(a[17], "workspace");
+  Seqs s(a[0], a + 7, a[14], a[15]);
+  const int dev = one_device({&q, state, &k, &v, ld, s.cu, s.na, s.src, s.dst, s.init, &out, ws});
+  value_if(q.dim() != 3 || v.dim() != 3, "q and k must be [rows, groups, dk], v [rows, heads, dv]; "
+           "got q=", q.sizes(), ", v=", v.sizes());
+  const int64_t rows = v.size(0), H = v.size(1), dv = v.size(2), G = q.size(1), dk = q.size(2);
+  const auto io = v.scalar_type();
+  ssu_linattn_params p{};
+  p.io_dtype = float_of(v, "v");
+  value_if(q.scalar_type() != io || k.scalar_type() != io || out.scalar_type() != io,
+           "q, k and out must share the v dtype (", io, ")");
+  rows3(q, "q", rows, G, dk, &p.q_row_stride, &p.q_group_stride);
+  rows3(k, "k", rows, G, dk, &p.k_row_stride, &p.k_group_stride);
+  rows3(v, "v", rows, H, dv, &p.v_row_stride, &p.v_head_stride);
+  rows3(out, "out", rows, H, dv, &p.out_row_stride, &p.out_head_stride);
+  if (ld) {
+    unsupported_if(ld->scalar_type() != at::kFloat, "log_decay must be fp32, got ",
+                   ld->scalar_type());
+    const bool each = ld->dim() == 2;
+    value_if((!each && ld->dim() != 1) || ld->size(each) != H || (each && ld->size(0) != rows),
+             "log_decay must be [", H, "] or [", rows, ", ", H, "], got ", ld->sizes());
+    p.log_decay = static_cast<const float*>(ld->data_ptr());
+    p.log_decay_row_stride = each ? ld->stride(0) : 0;
+    p.log_decay_head_stride = ld->stride(each);
+  }
+  if (state) {
+    value_if(state->dim() != 4 || state->size(1) != H || state->size(2) != dv ||
+                 state->size(3) != dk,
+             "state must be [slots, ", H, ", ", dv, ", ", dk, "], got ", state->sizes());
+    value_if(!state->is_contiguous(), "state must be contiguous");
+    p.state = state->data_ptr();
+    p.state_dtype = float_of(*state, "state");
+    p.slots = state->size(0);
+  }
+  p.nheads = H;
+  p.ngroups = G;
+  p.dv = dv;
+  p.dk = dk;
+  p.q = q.data_ptr();
+  p.k = k.data_ptr();
+  p.v = v.data_ptr();
+  p.out = out.data_ptr();
+  p.scale = (float)number(a[6]);
+  p.pad_slot_id = integer(a[12]);
+  p.disable_state_update = truth(a[16]);
+  value_if(ws && !ws->is_contiguous(), "workspace must be contiguous");
+  s.check(rows);
+  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  CUstream_st* stream = stream_of(a[18], dev);
+  auto prompt = [&](const ssu_linattn_params* c, int64_t nseqs, int64_t n, const void* cu,
+                    ssu_dtype meta, const void* src, const void* dst, ssu_dtype index,
+                    const uint8_t* init, CUstream_st* on) {
+    return ssu_linattn_fwd_varlen(c, nseqs, n, cu, meta, src, dst, index, init,
+                                  ws ? ws->data_ptr() : nullptr, ws ? (int64_t)ws->nbytes() : 0, on);
+  };
+  done(s.call(p, rows, ssu_linattn_update, prompt, stream));
+}
+
+// Sequence stride of a [n, m] operand with unit stride along m.
+int64_t rows_of(const Tensor& t, const char* name, int64_t n, int64_t m) {
+  value_if(t.dim() != 2 || t.size(0) != n || t.size(1) != m, name, " must be [", n, ", ", m,
+           "], got ", t.sizes());
+  value_if(m > 1 && t.stride(1) != 1, name, " must be contiguous along its last dimension, got ",
+           t.strides());
+  return t.stride(0);
+}
+
+const uint8_t* flags(const Tensor* t, const char* name, int64_t n) {
+  if (!t) return nullptr;
+  value_if(t->scalar_type() != at::kBool && t->scalar_type() != at::kByte, name,
+           " must be bool or uint8, got ", t->scalar_type());
+  return static_cast<const uint8_t*>(vector(t, name, n));
+}
+
+// drafts_verify(target_probs, draft_tokens, uniform, draft_probs, cu_seqlens, greedy, out,
+//               num_accepted, stream)
+void drafts_verify(PyObject* const* a) {
+  const Tensor &p = needed(a[0], "target_probs"), &d = needed(a[1], "draft_tokens");
+  const Tensor &u = needed(a[2], "uniform"), &out = needed(a[6], "out");
+  const Tensor *q = tensor(a[3], "draft_probs"), *cu = tensor(a[4], "cu_seqlens");
+  const Tensor *greedy = tensor(a[5], "greedy"), &n = needed(a[7], "num_accepted");
+  const int dev = one_device({&p, &d, &u, q, cu, greedy, &out, &n});
+  value_if(p.dim() != 2, "target_probs must be [rows, vocab], got ", p.sizes());
+  value_if(d.dim() != 2, "draft_tokens must be [sequences, drafts], got ", d.sizes());
+  const int64_t S = d.size(0), K = d.size(1), V = p.size(1);
+  ssu_drafts_params c{};
+  c.target_probs = p.data_ptr();
+  c.probs_dtype = float_of(p, "target_probs");
+  c.rows = p.size(0);
+  c.vocab = V;
+  c.target_row_stride = rows_of(p, "target_probs", c.rows, V);
+  if (q) {
+    value_if(q->scalar_type() != p.scalar_type(), "draft_probs must share the target_probs dtype");
+    rows3(*q, "draft_probs", S, K, V, &c.draft_seq_stride, &c.draft_step_stride);
+    // no drafts: nothing to read, whatever the pointer
+    c.draft_probs = K > 0 ? q->data_ptr() : nullptr;
+  }
+  c.draft_tokens = d.data_ptr();
+  c.token_dtype = index_of(d, "draft_tokens");
+  c.draft_tokens_seq_stride = rows_of(d, "draft_tokens", S, K);
+  c.nseqs = S;
+  c.drafts = K;
+  unsupported_if(u.scalar_type() != at::kFloat, "uniform must be fp32, got ", u.scalar_type());
+  c.uniform = static_cast<const float*>(u.data_ptr());
+  c.uniform_seq_stride = rows_of(u, "uniform", S, K + 1);
+  if (cu) {
+    c.cu_seqlens = vector(cu, "cu_seqlens", S + 1);
+    c.meta_dtype = index_of(*cu, "cu_seqlens");
+  }
+  c.greedy = flags(greedy, "greedy", S);
+  value_if(out.scalar_type() != d.scalar_type(), "out must have draft_tokens' dtype (",
+           d.scalar_type(), "), got ", out.scalar_type());
+  c.out = out.data_ptr();
+  c.out_seq_stride = rows_of(out, "out", S, K + 1);
+  c.num_accepted = const_cast<void*>(vector(&n, "num_accepted", S));
+  c.count_dtype = index_of(n, "num_accepted");
+  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  done(ssu_drafts_verify(&c, stream_of(a[8], dev)));
+}
+
+// prompt_maps(lens, context_lens, chunk_size, rows, max_chunks, cu_seqlens, cu_chunk_seqlens,
+//             seq_idx, last_chunk_indices, has_initial_state, num_chunks, row_seq, row_pos, stream)
+void prompt_maps(PyObject* const* a) {
+  const Tensor &lens = needed(a[0], "lens"), *context = tensor(a[1], "context_lens");
+  const Tensor &cu = needed(a[5], "cu_seqlens"), &chunks = needed(a[6], "cu_chunk_seqlens");
+  const Tensor &seq = needed(a[7], "seq_idx"), &last = needed(a[8], "last_chunk_indices");
+  const Tensor &init = needed(a[9], "has_initial_state"), &num = needed(a[10], "num_chunks");
+  const Tensor &row_seq = needed(a[11], "row_seq"), &row_pos = needed(a[12], "row_pos");
+  const int dev = one_device({&lens, context, &cu, &chunks, &seq, &last, &init, &num, &row_seq,
+                              &row_pos});
+  ssu_prompt_maps_params c{};
+  c.index_dtype = index_of(lens, "lens");
+  c.nseqs = lens.numel();
+  c.lens = vector(&lens, "lens", c.nseqs);
+  c.chunk_size = integer(a[2]);
+  c.rows = integer(a[3]);
+  c.max_chunks = integer(a[4]);
+  auto map = [&](const Tensor& t, const char* name, int64_t n) {
+    value_if(t.scalar_type() != lens.scalar_type(), name, " must have lens' dtype (",
+             lens.scalar_type(), "), got ", t.scalar_type());
+    return const_cast<void*>(vector(&t, name, n));
+  };
+  if (context) c.context_lens = map(*context, "context_lens", c.nseqs);
+  c.cu_seqlens = map(cu, "cu_seqlens", c.nseqs + 1);
+  c.cu_chunk_seqlens = map(chunks, "cu_chunk_seqlens", c.max_chunks + 1);
+  c.seq_idx = map(seq, "seq_idx", c.max_chunks);
+  c.last_chunk_indices = map(last, "last_chunk_indices", c.nseqs);
+  c.has_initial_state = const_cast<uint8_t*>(flags(&init, "has_initial_state", c.nseqs));
+  c.num_chunks = map(num, "num_chunks", 1);
+  c.row_seq = map(row_seq, "row_seq", c.rows);
+  c.row_pos = map(row_pos, "row_pos", c.rows);
+  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  done(ssu_prompt_maps(&c, stream_of(a[13], dev)));
+}
+
+// slots_assign(table, counts, slots, pad, out, fresh, num_missing, stream)
+void slots_assign(PyObject* const* a) {
+  const Tensor &t = needed(a[0], "table"), &counts = needed(a[1], "counts");
+  const Tensor &out = needed(a[4], "out"), &fresh = needed(a[5], "fresh");
+  const Tensor& missing = needed(a[6], "num_missing");
+  const int dev = one_device({&t, &counts, &out, &fresh, &missing});
+  const ssu_dtype d = index_of(t, "table");
+  value_if(t.dim() != 2 || !t.is_contiguous(), "table must be [sequences, steps] and contiguous, "
+           "got ", t.sizes());
+  for (const Tensor* o : {&out, &fresh})
+    value_if(o->sizes() != t.sizes() || o->scalar_type() != t.scalar_type() || !o->is_contiguous(),
+             "out and fresh must match table's shape and dtype");
+  value_if(counts.scalar_type() != t.scalar_type(), "counts must have table's dtype");
+  value_if(missing.scalar_type() != at::kInt || missing.numel() != 1,
+           "num_missing must be one int32");
+  const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+  done(ssu_slots_assign(t.data_ptr(), vector(&counts, "counts", t.size(0)), d, t.size(0), t.size(1),
+                        integer(a[2]), integer(a[3]), out.data_ptr(), fresh.data_ptr(),
+                        static_cast<int32_t*>(missing.data_ptr()), stream_of(a[7], dev)));
+}
+
 // Pools [slots, ...] that share the slot ids, and the device that they and `others` are on.
 struct Pools {
   std::vector<ssu_pool> pool;
@@ -456,6 +655,10 @@ PyMethodDef methods[] = {method<conv, 17>("conv"),
                          method<slots_copy, 5>("slots_copy"),
                          method<slots_clear, 4>("slots_clear"),
                          method<slots_compact, 7>("slots_compact"),
+                         method<linattn, 19>("linattn"),
+                         method<drafts_verify, 9>("drafts_verify"),
+                         method<prompt_maps, 14>("prompt_maps"),
+                         method<slots_assign, 8>("slots_assign"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods,
