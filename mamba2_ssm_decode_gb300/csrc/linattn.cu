@@ -64,10 +64,11 @@ static ssu_status check(const ssu_linattn_params* c, int64_t rows, bool pool_nee
   p->ld_rs = c->log_decay_row_stride;
   p->ld_hs = c->log_decay_head_stride;
   p->scale = c->scale;
-  auto on16 = [&](const void* ptr, int64_t rs, int64_t gs) {
-    return aligned(ptr, 16) && rs * es % 16 == 0 && (p->G == 1 || gs * es % 16 == 0);
+  auto on16 = [&](const void* ptr, int64_t rs, int64_t n, int64_t is) {
+    return aligned(ptr, 16) && rs * es % 16 == 0 && (n == 1 || is * es % 16 == 0);
   };
-  p->qk_vec = on16(c->q, p->q_rs, p->q_gs) && on16(c->k, p->k_rs, p->k_gs);
+  p->qk_vec = on16(c->q, p->q_rs, p->G, p->q_gs) && on16(c->k, p->k_rs, p->G, p->k_gs);
+  p->v_vec = on16(c->v, p->v_rs, p->H, p->v_hs);
   p->disable = c->disable_state_update != 0;
   p->pad = c->pad_slot_id;
   return SSU_OK;
@@ -136,7 +137,10 @@ ssu_status ssu_linattn_update(const ssu_linattn_params* c, int64_t nseqs, int64_
 int64_t ssu_linattn_workspace_bytes(int64_t rows, int64_t nseqs, int64_t nheads, int64_t dv,
                                     int64_t dk, ssu_dtype io_dtype) {
   if (rows < 0 || nseqs < 0 || nheads < 0 || dv < 0 || dk < 0) return -1;
-  return 0;
+  if (rows == 0 || nseqs == 0 ||
+      !linattn::takes_prompt(rows, nseqs, nheads, dv, dk, io_dtype))
+    return 0;
+  return linattn::prompt_workspace(rows, nseqs, nheads, dv, dk);
 }
 
 ssu_status ssu_linattn_fwd_varlen(const ssu_linattn_params* c, int64_t nseqs, int64_t rows,
@@ -157,6 +161,15 @@ ssu_status ssu_linattn_fwd_varlen(const ssu_linattn_params* c, int64_t nseqs, in
   if (nseqs == 0 || rows == 0) return ok();
   p.prompt = 1;
   p.has_init = has_initial_state;
+  // rows that do not start on 16-byte boundaries cannot be copied in whole vectors
+  if (takes_prompt(rows, nseqs, c->nheads, c->dv, c->dk, c->io_dtype) && p.qk_vec && p.v_vec) {
+    const int64_t need = prompt_workspace(rows, nseqs, c->nheads, c->dv, c->dk);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+      return fail(SSU_ERR_INVALID_ARGUMENT,
+                  "ssu_linattn_fwd_varlen needs a 16-byte aligned workspace of %lld bytes, got %lld",
+                  (long long)need, (long long)workspace_bytes);
+    return launched(launch_prompt(p, a, c->io_dtype, workspace, (cudaStream_t)stream));
+  }
   return launched(launch_walk(c, p, a, (cudaStream_t)stream));
 }
 

@@ -29,6 +29,7 @@ struct Args {
   int64_t ld_rs, ld_hs;  // ld_rs 0: one value per head
   float scale;
   int qk_vec;  // every vector of q and k starts on a 16-byte boundary
+  int v_vec;   // so does every one of v
   int disable;
   int64_t pad;
   // prompt form: the state is written once, after the last row
@@ -40,5 +41,13 @@ struct Args {
 cudaError_t launch_walk_f32(const Args& p, const Seqs& a, cudaStream_t stream);
 cudaError_t launch_walk_bf16(const Args& p, const Seqs& a, cudaStream_t stream);
 cudaError_t launch_walk_f16(const Args& p, const Seqs& a, cudaStream_t stream);
+
+// Prompts on the tensor cores (linattn_prompt.cuh): whether they take such a call,
+// and the bytes of workspace it needs.
+bool takes_prompt(int64_t rows, int64_t nseqs, int64_t heads, int64_t dv, int64_t dk,
+                  ssu_dtype io);
+int64_t prompt_workspace(int64_t rows, int64_t nseqs, int64_t heads, int64_t dv, int64_t dk);
+cudaError_t launch_prompt(const Args& p, const Seqs& a, ssu_dtype io, void* workspace,
+                          cudaStream_t stream);
 
 }  // namespace linattn
