@@ -69,6 +69,7 @@ static ssu_status check(const ssu_linattn_params* c, int64_t rows, bool pool_nee
   };
   p->qk_vec = on16(c->q, p->q_rs, p->G, p->q_gs) && on16(c->k, p->k_rs, p->G, p->k_gs);
   p->v_vec = on16(c->v, p->v_rs, p->H, p->v_hs);
+  p->o_vec = on16(c->out, p->o_rs, p->H, p->o_hs);
   p->disable = c->disable_state_update != 0;
   p->pad = c->pad_slot_id;
   return SSU_OK;
@@ -161,8 +162,12 @@ ssu_status ssu_linattn_fwd_varlen(const ssu_linattn_params* c, int64_t nseqs, in
   if (nseqs == 0 || rows == 0) return ok();
   p.prompt = 1;
   p.has_init = has_initial_state;
-  // rows that do not start on 16-byte boundaries cannot be copied in whole vectors
-  if (takes_prompt(rows, nseqs, c->nheads, c->dv, c->dk, c->io_dtype) && p.qk_vec && p.v_vec) {
+  // tensor maps have rows on 16-byte boundaries, at positive strides below 2^40 bytes
+  auto mapped = [](int64_t n, int64_t stride) { return n == 1 || (stride > 0 && stride < 1LL << 39); };
+  const bool maps = p.qk_vec && p.v_vec && mapped(rows, p.q_rs) && mapped(p.G, p.q_gs) &&
+                    mapped(rows, p.k_rs) && mapped(p.G, p.k_gs) && mapped(rows, p.v_rs) &&
+                    mapped(p.H, p.v_hs);
+  if (maps && takes_prompt(rows, nseqs, c->nheads, c->dv, c->dk, c->io_dtype)) {
     const int64_t need = prompt_workspace(rows, nseqs, c->nheads, c->dv, c->dk);
     if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
       return fail(SSU_ERR_INVALID_ARGUMENT,

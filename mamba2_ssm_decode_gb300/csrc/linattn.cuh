@@ -30,6 +30,7 @@ struct Args {
   float scale;
   int qk_vec;  // every vector of q and k starts on a 16-byte boundary
   int v_vec;   // so does every one of v
+  int o_vec;   // ... and of out
   int disable;
   int64_t pad;
   // prompt form: the state is written once, after the last row

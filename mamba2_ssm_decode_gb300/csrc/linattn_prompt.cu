@@ -57,6 +57,39 @@ int64_t prompt_workspace(int64_t rows, int64_t nseqs, int64_t heads, int64_t dv,
   return Layout(rows, nseqs, heads, dv, dk).bytes;
 }
 
+using Encode = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder, which is not linked against; looked up once.
+static Encode encoder() {
+  static const Encode f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return f;
+}
+
+// [rows][n][dim] 16-bit elements, strides in elements, as boxes of 64 rows x 1 x 64.
+static bool map_of(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int64_t n, int64_t dim,
+                   int64_t row_stride, int64_t stride) {
+  const Encode f = encoder();
+  if (!f) return false;
+  // a stride that is never taken may be anything the call allows
+  if (n == 1) stride = dim;
+  if (rows == 1) row_stride = n * stride;
+  const cuuint64_t size[3] = {(cuuint64_t)dim, (cuuint64_t)n, (cuuint64_t)rows};
+  const cuuint64_t bytes[2] = {(cuuint64_t)stride * 2, (cuuint64_t)row_stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)kC}, step[3] = {1, 1, 1};
+  return f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+           const_cast<void*>(p), size, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_prompt(const Args& p, const Seqs& a, ssu_dtype io, void* workspace,
                           cudaStream_t stream) {
   const Layout l(a.rows, a.n, p.H, p.dv, p.dk);
@@ -73,6 +106,10 @@ cudaError_t launch_prompt(const Args& p, const Seqs& a, ssu_dtype io, void* work
   g.entries = (int)l.entries;
   g.err = ssu::device_error_word();
   if (!g.err) return cudaErrorInvalidValue;
+  if (!map_of(&g.q, io == SSU_BF16, p.q, a.rows, p.G, p.dk, p.q_rs, p.q_gs) ||
+      !map_of(&g.k, io == SSU_BF16, p.k, a.rows, p.G, p.dk, p.k_rs, p.k_gs) ||
+      !map_of(&g.v, io == SSU_BF16, p.v, a.rows, p.H, p.dv, p.v_rs, p.v_hs))
+    return cudaErrorInvalidValue;
   linattn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(g);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -21,16 +21,19 @@
 // output's own rounding), w V as three of bf16 where the state is kept in 32 bits
 // (2^-26; two leave 2^-17, which shows in it), else two.
 //
-// One CTA of 20 warps works on a chunk of one head at a time, chunks of a
-// sequence in order: 4 warps turn scores into P, 4 write outputs, 8 update S and
-// weigh V (each owns 32 lanes of tensor memory, so the tiles' rows), one issues
-// the products, three load Q, K, V and sum the decays, three chunks ahead.
+// One CTA of 24 warps works on a chunk of one head at a time, chunks of a
+// sequence in order: 4 warps turn scores into P, 4 write outputs, 8 update S (each
+// owns 32 lanes of tensor memory, so the tiles' rows), 4 weigh V, half a chunk
+// ahead of its product, one issues the products, one has Q, K and V copied (TMA,
+// three chunks ahead, 128-byte swizzle) and sums the decays.
 // Items -- a sequence's, or a piece's, chunks of one head -- are handed out by a
 // counter, longest first.  A sequence of more chunks than every SM's fair share
 // is cut into pieces: a first launch computes what each piece adds to the state
 // (the fourth product alone) and its decay, and a piece's item then starts by
 // adding up the pieces before it.
 #pragma once
+
+#include <cuda.h>
 
 #include "linattn.cuh"
 #include "ssd_tc.cuh"
@@ -44,8 +47,6 @@ using ssu::mbar_test;
 using ssu::smem_addr;
 
 constexpr int kC = 64;             // tokens of a chunk
-constexpr int kCol = kC * 16 + 16;  // bytes between the 16-byte columns of a tile: 16 of padding
-                                    // put the pieces of a row on banks of their own
 constexpr int kStages = 3;
 constexpr unsigned kErrMma = SSU_DEVICE_ERR_MMA_TIMEOUT;
 
@@ -63,6 +64,7 @@ struct Header {
 };
 
 struct PromptArgs {
+  CUtensorMap q, k, v;  // [rows][groups or heads][dk or dv], boxes of 64 rows x 1 x 64
   Args p;
   Seqs a;
   Header* head;
@@ -160,27 +162,51 @@ struct Chunk {
 
 struct Tables {        // of a chunk, in units of log2
   float a[kC];         // a_t
+  float x[kC];         // e^(r - a_s), r the a of the last token of s's 16
   float ea[kC];        // scale e^(a_t)
   float w[kC];         // e^(a_C - a_s); 0 behind the last row
+  float r[kC / 16];    // the four r
   float keep, add;     // e^(a_C) = keep + add, keep 0 or 1
   float decay;         // e^(a_C)
+  int mild;            // e^(a_t - r) and e^(r - a_s) stay within 2^60 inside the 16 of an r
 };
+
+// A tile: 64 rows (tokens) of 128 bytes, one after the other, the 16-byte pieces
+// of row s at (piece ^ s % 8): the 128-byte swizzle, whose atoms are 8 rows.  Wider
+// rows are several tiles.
+constexpr int kTile = kC * 128;
+__device__ __forceinline__ int tile_at(int s, int piece) {
+  return (piece >> 3) * kTile + s * 128 + ((piece ^ s) & 7) * 16;
+}
+// Descriptors of operands in tiles.  Rows are the operand's M (or N): 32 bytes
+// further per 16 of K.  Rows are its K: 16 of them are 2048 bytes, and 64 of M (N)
+// a tile.
+__device__ __forceinline__ uint64_t rows_mn(uint32_t addr) {
+  return tc::sdesc(addr, 16, 1024) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t rows_k(uint32_t addr) {
+  return tc::sdesc(addr, kTile, 1024) | (2ull << 61);
+}
 
 template <int DV, int DK>
 struct Sizes {
-  static constexpr int kQ = DK / 8 * kCol, kV = DV / 8 * kCol, kP = kC / 8 * kCol;
+  static constexpr int kQ = DK / 64 * kTile, kV = DV / 64 * kTile, kP = kTile;
   static constexpr int kStage = 2 * kQ + kV;
   static constexpr int kCols = 512;  // of tensor memory
   // columns: D, o1, o2, scores (two), S (high parts, remainders)
   static constexpr int kD = 0, kO1 = 128, kO2 = 192, kSc = 256, kS = 384;
+  // outputs are turned in the place of Q, where they fit: Q is done with by then
+  static constexpr int kOut = DV > DK ? kV : 0;
 };
 
 template <int DV, int DK, int PARTS>
 struct PromptSmem {
   using Z = Sizes<DV, DK>;
-  unsigned char stage[kStages][Z::kStage];
+  unsigned char stage[kStages][Z::kStage];  // Q, K, V
   unsigned char wv[PARTS][Z::kV];
   unsigned char p[2][Z::kP];
+  unsigned char out[Z::kOut ? Z::kOut : 16];
+  unsigned char turn[8][DV / 4 * 48];  // rows of S on their way from and to global memory
   Tables tab[kStages];
   Chunk chunk[kStages];
   float row_max[2][128];    // fp16: the largest value of half a row of S
@@ -188,15 +214,13 @@ struct PromptSmem {
   int bad[2][128];          // the first token of the chunk whose v is not finite
   int any_bad[2];
   uint64_t full[kStages], empty[kStages], sc_full[2];
-  uint64_t p_ready, p_free, o_full, o_free, s_ready, v_ready, d_full;
-  uint64_t loaders, state_warps, out_warps, fin;  // warps of a role meet; the last product
+  uint64_t p_ready, p_free, o_full, o_free, s_ready, d_full, wv_ready[2], wv_free[2];
+  uint64_t state_warps, out_warps, fin;  // warps of a role meet; the last product
   uint32_t tmem;
   int abort;
-  int item;
 };
 
-constexpr int kPromptThreads = 640;
-constexpr int kLoaders = 96;
+constexpr int kPromptThreads = 768;
 
 __device__ __forceinline__ void st_tmem8(uint32_t addr, const uint32_t (&r)[8]) {
   asm volatile(
@@ -208,14 +232,82 @@ __device__ __forceinline__ void wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// As tc::mma, with A in tensor memory.
+// The products, issued by a whole warp of which one lane is elected (the same one
+// every time): control flow stays uniform, and with it the descriptors in uniform
+// registers.  From a branch that one lane takes, each took 100 to 160 cycles.
+// D (tensor memory) = A B^T, or += where `accumulate` is not 0.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// ... with A in tensor memory.
 __device__ __forceinline__ void mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One arrival on `bar` once every product before has completed.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A box of 64 rows x 64 elements from (row, group, column).
+__device__ __forceinline__ void load_box(uint32_t to, const CUtensorMap* map, uint32_t bar, int col,
+                                         int group, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5}], [%2];" ::"r"(to),
+      "l"(map), "r"(bar), "r"(col), "r"(group), "r"(row)
+      : "memory");
+}
+
+// 16 lanes x 32 (or 16) columns as 8 x 8 fragments: v[4 f + i] is row lane / 4 + (i
+// < 2 ? 0 : 8), column 8 f + 2 (lane % 4) + i % 2.
+__device__ __forceinline__ void ld_frag4(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void ld_frag2(uint32_t addr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four 8 x 8 matrices of fragments to shared memory; lane l gives the address of row
+// l % 8 of matrix l / 8.  TRANS: rows in memory are the fragments' columns.
+template <bool TRANS>
+__device__ __forceinline__ void st_frags(uint32_t addr, const uint32_t (&w)[4]) {
+  if constexpr (TRANS)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+  else
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
 }
 
 // Waits for a phase; gives up after two seconds, or when another thread did.
@@ -273,14 +365,34 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// The part of (a, b) that 16 bits hold, and what they leave of it.
+// The 16-bit part of two fp32 numbers, which leaves the rest of them.
 template <class IT>
-__device__ __forceinline__ uint32_t part(float& a, float& b) {
-  const uint32_t w = pack2<IT>(a, b);
-  const float2 f = unpack2<IT>(w);
-  a -= f.x;
-  b -= f.y;
+__device__ __forceinline__ uint32_t part(float2& v) {
+  const uint32_t w = pack2<IT>(v.x, v.y);
+  v = __ffma2_rn(unpack2<IT>(w), make_float2(-1.0f, -1.0f), v);
   return w;
+}
+// ... cut off, not rounded: three such parts of 8 bits are all of an fp32 number.
+__device__ __forceinline__ uint32_t part_cut(float2& v) {
+  const uint32_t x = __float_as_uint(v.x), y = __float_as_uint(v.y);
+  const float2 f = make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u));
+  v = __ffma2_rn(f, make_float2(-1.0f, -1.0f), v);
+  return __byte_perm(x, y, 0x7632);
+}
+
+// Stays 0 while the two values of every word are finite.
+template <class IT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w, uint32_t acc) {
+  if constexpr (std::is_same<IT, __nv_bfloat16>::value) {
+    const __nv_bfloat162 r =
+        __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w), __nv_bfloat162{},
+                *reinterpret_cast<const __nv_bfloat162*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&w), __half2{},
+                              *reinterpret_cast<const __half2*>(&acc));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 }
 
 template <int N>
@@ -292,23 +404,22 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Sixteen values of this thread's row of a state in global memory, columns
-// [c, c + 16): loaded (or stored) by the warp in whole rows, 16 bytes a lane, and
-// turned through `buf`, ROWS rows of 80 bytes.  `rows`: rows the warp has (32 or 16;
-// row = lane).  ST is the state's type.
+// Eight values of this thread's row of a state in global memory, columns [c, c +
+// 8): loaded (or stored) by the warp in whole rows, 16 bytes a lane, and turned
+// through `buf`, ROWS rows of 48 bytes.  Row = lane % ROWS.  ST is the state's type.
 template <class ST, int DK, int ROWS>
-__device__ __forceinline__ void load_rows16(const ST* tile, int c, unsigned char* buf, float* v) {
-  constexpr int PER = 16 * (int)sizeof(ST) / 16;  // lanes of a row
+__device__ __forceinline__ void load_rows8(const ST* tile, int c, unsigned char* buf, float* v) {
+  constexpr int PER = 8 * (int)sizeof(ST) / 16;  // lanes of a row
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < ROWS * PER / 32; ++i) {
+  for (int i = 0; i < (ROWS * PER + 31) / 32; ++i) {
     const int row = (i * 32 + lane) / PER, piece = lane % PER;
-    const uint4 w =
-        *reinterpret_cast<const uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST)));
-    *reinterpret_cast<uint4*>(buf + row * 80 + piece * 16) = w;
+    if (row < ROWS)
+      *reinterpret_cast<uint4*>(buf + row * 48 + piece * 16) =
+          *reinterpret_cast<const uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST)));
   }
   __syncwarp();
-  const unsigned char* mine = buf + (lane % ROWS) * 80;
+  const unsigned char* mine = buf + (lane % ROWS) * 48;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const uint4 w = *reinterpret_cast<const uint4*>(mine + i * 16);
@@ -318,8 +429,8 @@ __device__ __forceinline__ void load_rows16(const ST* tile, int c, unsigned char
       if constexpr (sizeof(ST) == 4) v[i * 4 + k] = __uint_as_float(u[k]);
       else {
         const float2 f = unpack2<ST>(u[k]);
-        v[i * 8 + 2 * k] = f.x;
-        v[i * 8 + 2 * k + 1] = f.y;
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
       }
     }
   }
@@ -327,28 +438,29 @@ __device__ __forceinline__ void load_rows16(const ST* tile, int c, unsigned char
 }
 
 template <class ST, int DK, int ROWS>
-__device__ __forceinline__ void store_rows16(ST* tile, int c, unsigned char* buf, const float* v) {
-  constexpr int PER = 16 * (int)sizeof(ST) / 16;
+__device__ __forceinline__ void store_rows8(ST* tile, int c, unsigned char* buf, const float* v) {
+  constexpr int PER = 8 * (int)sizeof(ST) / 16;
   const int lane = threadIdx.x & 31;
   if (lane < ROWS) {
-    unsigned char* mine = buf + lane * 80;
+    unsigned char* mine = buf + lane * 48;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       uint32_t u[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if constexpr (sizeof(ST) == 4) u[k] = __float_as_uint(v[i * 4 + k]);
-        else u[k] = pack2<ST>(v[i * 8 + 2 * k], v[i * 8 + 2 * k + 1]);
+        else u[k] = pack2<ST>(v[2 * k], v[2 * k + 1]);
       }
       *reinterpret_cast<uint4*>(mine + i * 16) = make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < ROWS * PER / 32; ++i) {
+  for (int i = 0; i < (ROWS * PER + 31) / 32; ++i) {
     const int row = (i * 32 + lane) / PER, piece = lane % PER;
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + row * 80 + piece * 16);
-    *reinterpret_cast<uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST))) = w;
+    if (row < ROWS)
+      *reinterpret_cast<uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST))) =
+          *reinterpret_cast<const uint4*>(buf + row * 48 + piece * 16);
   }
   __syncwarp();
 }
@@ -363,15 +475,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   constexpr int LIST = FULL ? 1 : 0;
   constexpr int ROWS = DV / 4;  // lanes of each 32 that hold a row where dv is one side (M = DV)
   constexpr int HALF = DK / 2;  // columns of S a thread owns
-  extern __shared__ __align__(128) unsigned char smem_raw[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const Args& p = g.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.full[i], kLoaders);
-      mbar_init(&sm.empty[i], FULL ? 5 : 1);  // the products' end; the output warps' look at a_t
+      mbar_init(&sm.full[i], 2);              // the copies' bytes; the tables
+      mbar_init(&sm.empty[i], FULL ? 13 : 9);  // the products' end; S's warps; the output warps
     }
     mbar_init(&sm.sc_full[0], 1);
     mbar_init(&sm.sc_full[1], 1);
@@ -380,9 +492,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, 4);
     mbar_init(&sm.s_ready, 8);
-    mbar_init(&sm.v_ready, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.wv_ready[i], 4);
+      mbar_init(&sm.wv_free[i], 1);
+    }
     mbar_init(&sm.d_full, 1);
-    mbar_init(&sm.loaders, kLoaders / 32);
     mbar_init(&sm.state_warps, 8);
     mbar_init(&sm.out_warps, 4);
     mbar_init(&sm.fin, 1);
@@ -391,119 +505,118 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     sm.any_bad[0] = sm.any_bad[1] = 0;
   }
   if (tid < 128) sm.bad[0][tid] = sm.bad[1][tid] = kC;
-  if (warp == 16) tc::alloc(smem_addr(&sm.tmem), Z::kCols);
+  // P above its diagonal stays zero throughout
+  for (int i = tid; i < 2 * Z::kP / 16; i += kPromptThreads)
+    reinterpret_cast<uint4*>(sm.p[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc::fence_proxy_async();
+  if (warp == 20) tc::alloc(smem_addr(&sm.tmem), Z::kCols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem;
   const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes
 
-  if (wg == 4) {
-    regs_dec<80>();
-    if (warp == 16) {
+  if (wg == 5) {
+    regs_dec<64>();
+    if (warp == 20) {
       // ---- the products --------------------------------------------------
-      if (lane == 0) {
+      {
         constexpr uint32_t kIdSc = tc::idesc_f16(kBF16, 64, 64, false, false);
-        constexpr uint32_t kIdO1 = tc::idesc_f16(kBF16, DV, 64, true, false);
         constexpr uint32_t kIdO2 = tc::idesc_f16(kBF16, DV, 64, false, false);
         constexpr uint32_t kIdD = tc::idesc_f16(kBF16, DV, DK, true, true);
         const uint32_t sp = smem_addr(sm.p[0]), swv = smem_addr(sm.wv[0]);
+        auto at_k = [](int kk) { return (uint32_t)(kk / 4 * kTile + kk % 4 * 32); };
         auto scores = [&](int n) {
           const uint32_t q = smem_addr(sm.stage[n % kStages]), k = q + Z::kQ;
           tc::fence_after_sync();
-          tc::fence_proxy_async();
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
-            tc::mma(tmem + Z::kSc + (n & 1) * 64, tc::sdesc(q + kk * 2 * kCol, kCol, 128),
-                    tc::sdesc(k + kk * 2 * kCol, kCol, 128), kIdSc, kk != 0);
-          tc::commit(smem_addr(&sm.sc_full[n & 1]));
+            mma(tmem + Z::kSc + (n & 1) * 64, rows_mn(q + at_k(kk)), rows_mn(k + at_k(kk)), kIdSc,
+                    kk != 0);
+          commit(smem_addr(&sm.sc_full[n & 1]));
         };
         bool ahead = false;  // the scores of chunk n are under way
         for (int n = 0;; ++n) {
           const int st = n % kStages;
-          if (!wait(sm, g.err, &sm.full[st], (n / kStages) & 1)) break;
+          if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1)) break;
           if (sm.chunk[st].stop) break;
           const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
           if constexpr (FULL) {
             if (!ahead) scores(n);
             const int nx = (n + 1) % kStages;
-            ahead = mbar_test(&sm.full[nx], ((n + 1) / kStages) & 1) && !sm.chunk[nx].stop;
+            ahead = __all_sync(0xffffffffu, mbar_test(&sm.full[nx], ((n + 1) / kStages) & 1)) &&
+                    !sm.chunk[nx].stop;
             if (ahead) scores(n + 1);
-            if (!wait(sm, g.err, &sm.p_ready, n & 1)) break;
           }
-          if (!wait(sm, g.err, &sm.v_ready, n & 1)) break;
+          // S is given, and with it D of the chunk before is read
+          if (!warp_wait(sm, g.err, &sm.s_ready, n & 1)) break;
           if constexpr (FULL) {
-            if (n > 0 && !wait(sm, g.err, &sm.o_free, (n - 1) & 1)) break;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int kk = 0; kk < kC / 16; ++kk)
-                tc::mma(tmem + Z::kO1, tc::sdesc(v + kk * 256, 128, kCol),
-                        tc::sdesc(sp + part * Z::kP + kk * 2 * kCol, kCol, 128), kIdO1,
-                        (part | kk) != 0);
-            tc::commit(smem_addr(&sm.p_free));
-            if (!wait(sm, g.err, &sm.s_ready, n & 1)) break;
+            if (n > 0 && !warp_wait(sm, g.err, &sm.o_free, (n - 1) & 1)) break;
             tc::fence_after_sync();
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
               for (int kk = 0; kk < DK / 16; ++kk)
-                mma_ta(tmem + Z::kO2, tmem + Z::kS + part * HALF + kk * 8,
-                       tc::sdesc(q + kk * 2 * kCol, kCol, 128), kIdO2, (part | kk) != 0);
-            tc::commit(smem_addr(&sm.o_full));
+                mma_ta(tmem + Z::kO2, tmem + Z::kS + part * HALF + kk * 8, rows_mn(q + at_k(kk)),
+                       kIdO2, (part | kk) != 0);
           }
-          tc::fence_after_sync();
+          bool dead = false;
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part)
+          for (int hh = 0; hh < 2; ++hh) {  // half of the tokens
+            dead = dead || !warp_wait(sm, g.err, &sm.wv_ready[hh], n & 1);
+            tc::fence_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < kC / 16; ++kk)
-              tc::mma(tmem + Z::kD, tc::sdesc(swv + part * Z::kV + kk * 256, 128, kCol),
-                      tc::sdesc(k + kk * 256, 128, kCol), kIdD, (part | kk) != 0);
-          tc::commit(smem_addr(&sm.d_full));
-          tc::commit(smem_addr(&sm.empty[st]));
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+              for (int kk = 2 * hh; kk < 2 * hh + 2; ++kk)
+                mma(tmem + Z::kD, rows_k(swv + part * Z::kV + kk * 2048), rows_k(k + kk * 2048), kIdD,
+                    (part | kk) != 0);
+            commit(smem_addr(&sm.wv_free[hh]));
+          }
+          if (dead) break;
+          commit(smem_addr(&sm.d_full));
+          if constexpr (FULL) {
+            if (!warp_wait(sm, g.err, &sm.p_ready, n & 1)) break;
+            tc::fence_after_sync();
+            // tokens before s take nothing from it: the first 16 kk columns are done
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < kC / 16; ++kk)
+                mma(tmem + Z::kO1 + 16 * kk, rows_k(v + kk * 2048),
+                        rows_mn(sp + part * Z::kP + kk * 2048 + kk * 32),
+                        tc::idesc_f16(kBF16, DV, kC - 16 * kk, true, false), (part | kk) != 0);
+            commit(smem_addr(&sm.p_free));
+            commit(smem_addr(&sm.o_full));
+          }
+          commit(smem_addr(&sm.empty[st]));
         }
         // nothing is in flight any more when the tensor memory is given back
-        tc::commit(smem_addr(&sm.fin));
+        commit(smem_addr(&sm.fin));
         const uint64_t t0 = ssu::global_ns();
         while (!mbar_test(&sm.fin, 0) && ssu::global_ns() - t0 < ssu::kWaitLimitNs) {
         }
       }
       __syncwarp();
-    } else {
-      // ---- loads, three warps --------------------------------------------
-      const int lt = tid - 17 * 32;  // 0 .. 95
+    } else if (warp == 21) {
+      // ---- copies and tables -----------------------------------------------
       const int items = g.head->count[LIST] * p.H;
       int n = 0;
       bool live = true;
-      uint32_t met = 0;
-      auto landed = [&](int m) {  // this thread's copies of chunk m are in shared memory
-        tc::fence_proxy_async();
-        mbar_arrive(&sm.full[m % kStages]);
-      };
       int next = 0;
-      if (lt == 0) next = atomicAdd(&g.head->next[LIST], 1);
+      if (lane == 0) next = atomicAdd(&g.head->next[LIST], 1);
       while (live) {
-        if (lt == 0) {
-          sm.item = next;
-          next = atomicAdd(&g.head->next[LIST], 1);  // on its way during this item
-        }
-        if (!meet(sm, g.err, &sm.loaders, met)) live = false;
-        const int item = sm.item;
-        if (!meet(sm, g.err, &sm.loaders, met)) live = false;
-        if (!live || item >= items) break;
+        const int item = __shfl_sync(0xffffffffu, next, 0);
+        if (item >= items) break;
+        if (lane == 0) next = atomicAdd(&g.head->next[LIST], 1);  // on its way during this item
         const Piece piece = g.pieces[LIST][item / p.H];
         const int h = item % p.H, grp = h / p.hr;
-        const IT* qg = static_cast<const IT*>(p.q) + (int64_t)piece.r0 * p.q_rs + grp * p.q_gs;
-        const IT* kg = static_cast<const IT*>(p.k) + (int64_t)piece.r0 * p.k_rs + grp * p.k_gs;
-        const IT* vg = static_cast<const IT*>(p.v) + (int64_t)piece.r0 * p.v_rs + h * p.v_hs;
         const int chunks = (piece.len + kC - 1) / kC;
         auto decay_at = [&](int t) {
           return p.ld && t < piece.len ? p.ld[(int64_t)(piece.r0 + t) * p.ld_rs + h * p.ld_hs]
                                        : 0.0f;
         };
-        float l0 = 0.0f, l1 = 0.0f;
-        if (warp == 17) l0 = decay_at(2 * lane), l1 = decay_at(2 * lane + 1);
+        float l0 = decay_at(2 * lane), l1 = decay_at(2 * lane + 1);
         for (int c = 0; c < chunks; ++c, ++n) {
           const int st = n % kStages;
           if (n >= kStages && !warp_wait(sm, g.err, &sm.empty[st], (n / kStages - 1) & 1)) {
@@ -511,109 +624,129 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             break;
           }
           const int t0 = c * kC, rows = min(kC, piece.len - t0);
-          const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
-          auto tile = [&](uint32_t to, const IT* from, int64_t rs, int pieces) {
-            for (int i = lt; i < kC * pieces; i += kLoaders) {
-              const int row = i / pieces, col = i % pieces;
-              tc::cp16(to + col * kCol + row * 16, from + (t0 + (row < rows ? row : 0)) * rs + col * 8,
-                       row < rows ? 16u : 0u);
-            }
-          };
-          if constexpr (FULL) tile(q, qg, p.q_rs, DK / 8);
-          tile(k, kg, p.k_rs, DK / 8);
-          tile(v, vg, p.v_rs, DV / 8);
-          tc::cp_commit();
-          if (warp == 17) {
-            // a_t in 64 bits: differences of large sums keep their digits.  A log decay below
-            // -160 (in units of log2) is a decay of zero in fp32 and is held there.
-            auto held = [](float l) {
-              l *= kLog2e;
-              asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-160.0f));
-              return (double)l;
-            };
-            const double d0 = held(l0), d1 = held(l1);
-            double inc = d0 + d1;
+          if (lane == 0) {
+            const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
+            const uint32_t bar = smem_addr(&sm.full[st]);
+            ssu::mbar_arrive_expect_tx(&sm.full[st], FULL ? Z::kStage : Z::kStage - Z::kQ);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const double u = __shfl_up_sync(0xffffffffu, inc, o);
-              if (lane >= o) inc += u;
+            for (int i = 0; i < DK / 64; ++i) {
+              if (FULL) load_box(q + i * kTile, &g.q, bar, 64 * i, grp, piece.r0 + t0);
+              load_box(k + i * kTile, &g.k, bar, 64 * i, grp, piece.r0 + t0);
             }
-            const double end = __shfl_sync(0xffffffffu, inc, 31);
-            const double a1 = inc, a0 = inc - d1;
-            Tables& tab = sm.tab[st];
-            const int t = 2 * lane;
-            tab.a[t] = (float)a0;
-            tab.a[t + 1] = (float)a1;
-            tab.ea[t] = p.scale * exp2f((float)a0);
-            tab.ea[t + 1] = p.scale * exp2f((float)a1);
-            tab.w[t] = t < rows ? exp2f((float)(end - a0)) : 0.0f;
-            tab.w[t + 1] = t + 1 < rows ? exp2f((float)(end - a1)) : 0.0f;
-            if (lane == 0) {
-              // near 1 the decay is 1 + add: rounded by itself it would be off by the same
-              // 2^-25 chunk after chunk
-              const float e = exp2f((float)end);
-              tab.decay = e;
-              tab.keep = e > 0.5f ? 1.0f : 0.0f;
-              tab.add = e > 0.5f ? expm1f((float)(end * 0.69314718055994531)) : e;
-            }
-            l0 = decay_at(t0 + kC + 2 * lane);
-            l1 = decay_at(t0 + kC + 2 * lane + 1);
-          }
-          if (lt == 0)
+#pragma unroll
+            for (int i = 0; i < DV / 64; ++i)
+              load_box(v + i * kTile, &g.v, bar, 64 * i, h, piece.r0 + t0);
             sm.chunk[st] = Chunk{h, piece.r0 + t0, rows, c == 0, c == chunks - 1, 0, piece};
-          if (n > 0) {
-            tc::cp_wait<1>();
-            landed(n - 1);
           }
+          // a_t in 64 bits: differences of large sums keep their digits.  A log decay below
+          // -160 (in units of log2) is a decay of zero in fp32 and is held there.
+          auto held = [](float l) {
+            l *= kLog2e;
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-160.0f));
+            return (double)l;
+          };
+          const double d0 = held(l0), d1 = held(l1);
+          l0 = decay_at(t0 + kC + 2 * lane);
+          l1 = decay_at(t0 + kC + 2 * lane + 1);
+          double inc = d0 + d1;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const double u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+          }
+          const double end = __shfl_sync(0xffffffffu, inc, 31);
+          const double ref = __shfl_sync(0xffffffffu, inc, lane | 7);
+          const double a1 = inc, a0 = inc - d1;
+          Tables& tab = sm.tab[st];
+          const int t = 2 * lane;
+          const float x0 = (float)(ref - a0), x1 = (float)(ref - a1);
+          *reinterpret_cast<float2*>(tab.a + t) = make_float2((float)a0, (float)a1);
+          *reinterpret_cast<float2*>(tab.x + t) = make_float2(exp2f(x0), exp2f(x1));
+          *reinterpret_cast<float2*>(tab.ea + t) =
+              make_float2(p.scale * exp2f((float)a0), p.scale * exp2f((float)a1));
+          *reinterpret_cast<float2*>(tab.w + t) =
+              make_float2(t < rows ? exp2f((float)(end - a0)) : 0.0f,
+                          t + 1 < rows ? exp2f((float)(end - a1)) : 0.0f);
+          const bool mild =
+              __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f);
+          if ((lane & 7) == 7) tab.r[lane / 8] = (float)a1;
+          if (lane == 0) {
+            // near 1 the decay is 1 + add: rounded by itself it would be off by the same
+            // 2^-25 chunk after chunk
+            const float e = exp2f((float)end);
+            tab.decay = e;
+            tab.keep = e > 0.5f ? 1.0f : 0.0f;
+            tab.add = e > 0.5f ? expm1f((float)(end * 0.69314718055994531)) : e;
+            tab.mild = mild;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[st]);
         }
       }
-      tc::cp_wait<0>();
-      if (live) {
-        if (n > 0) landed(n - 1);
+      if (live && lane == 0) {
         const int st = n % kStages;
-        if (n < kStages || warp_wait(sm, g.err, &sm.empty[st], (n / kStages - 1) & 1)) {
-          if (lt == 0) sm.chunk[st].stop = 1;
-          landed(n);
+        if (n < kStages || wait(sm, g.err, &sm.empty[st], (n / kStages - 1) & 1)) {
+          sm.chunk[st].stop = 1;
+          mbar_arrive(&sm.full[st]);
+          mbar_arrive(&sm.full[st]);
         }
       }
+      __syncwarp();
     }
   } else if (wg == 0) {
-    regs_dec<80>();
+    regs_dec<64>();
     if constexpr (FULL) {
-      // ---- P --------------------------------------------------------------
-      const int t = 16 * warp + (lane & 15);
+      // ---- P: rows 16 warp + r and r + 8, r = lane / 4; columns 2 (lane % 4) and the next of
+      // each eight -------------------------------------------------------------
+      const int r = lane >> 2, cc = 2 * (lane & 3);
+      const int t0 = 16 * warp + r, t1 = t0 + 8;
+      // where this lane's row of the four matrices of 16 x 16 values goes
+      const int mrow = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), mpiece = lane >> 4;
       for (int n = 0;; ++n) {
         const int st = n % kStages;
         if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
+        const Tables& tab = sm.tab[st];
+        const float a0 = tab.a[t0], a1 = tab.a[t1];
+        const bool mild = tab.mild;
         if (!warp_wait(sm, g.err, &sm.sc_full[n & 1], (n >> 1) & 1)) break;
         if (n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
-        __syncwarp();
         tc::fence_after_sync();
-        const Tables& tab = sm.tab[st];
-        const float at = tab.a[t];
-#pragma unroll
-        for (int c = 0; c < kC; c += 16) {
-          float s[16];
-          tc::ld16(tmem + quad + Z::kSc + (n & 1) * 64 + c, s);
+#pragma unroll 1
+        for (int b = 0; b <= warp; ++b) {  // 16 columns
+          float s[8];
+          ld_frag2(tmem + quad + Z::kSc + (n & 1) * 64 + 16 * b, s);
+          const float u0 = p.scale * ex2(a0 - tab.r[b]), u1 = p.scale * ex2(a1 - tab.r[b]);
           tc::wait_ld();
-          uint32_t hi[8], lo[8];
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x = c + i <= t ? s[i] * (p.scale * ex2(at - tab.a[c + i])) : 0.0f;
-            float y = c + i + 1 <= t ? s[i + 1] * (p.scale * ex2(at - tab.a[c + i + 1])) : 0.0f;
-            hi[i / 2] = part<IT>(x, y);
-            lo[i / 2] = pack2<IT>(x, y);
-          }
-          if (lane < 16) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              unsigned char* to = sm.p[0] + (c / 8 + j) * kCol + t * 16;
-              *reinterpret_cast<uint4*>(to) =
-                  make_uint4(hi[4 * j], hi[4 * j + 1], hi[4 * j + 2], hi[4 * j + 3]);
-              *reinterpret_cast<uint4*>(to + Z::kP) =
-                  make_uint4(lo[4 * j], lo[4 * j + 1], lo[4 * j + 2], lo[4 * j + 3]);
+          for (int f = 0; f < 2; ++f) {  // 8 columns
+            const int c = 16 * b + 8 * f + cc;
+            float2 e0, e1;
+            if (mild) {
+              const float2 x = *reinterpret_cast<const float2*>(tab.x + c);
+              e0 = __fmul2_rn(x, make_float2(u0, u0));
+              e1 = __fmul2_rn(x, make_float2(u1, u1));
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(tab.a + c);
+              e0 = make_float2(p.scale * ex2(a0 - x.x), p.scale * ex2(a0 - x.y));
+              e1 = make_float2(p.scale * ex2(a1 - x.x), p.scale * ex2(a1 - x.y));
             }
+            float2 y0 = __fmul2_rn(make_float2(s[4 * f], s[4 * f + 1]), e0);
+            float2 y1 = __fmul2_rn(make_float2(s[4 * f + 2], s[4 * f + 3]), e1);
+            if (b == warp) {
+              if (c > t0) y0.x = 0.0f;
+              if (c + 1 > t0) y0.y = 0.0f;
+              if (c > t1) y1.x = 0.0f;
+              if (c + 1 > t1) y1.y = 0.0f;
+            }
+            hi[2 * f] = part<IT>(y0);
+            lo[2 * f] = pack2<IT>(y0.x, y0.y);
+            hi[2 * f + 1] = part<IT>(y1);
+            lo[2 * f + 1] = pack2<IT>(y1.x, y1.y);
           }
+          const uint32_t to = smem_addr(sm.p[0]) + tile_at(mrow, 2 * b + mpiece);
+          st_frags<false>(to, hi);
+          st_frags<false>(to + Z::kP, lo);
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
@@ -622,59 +755,171 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     }
   } else if (wg == 1) {
-    regs_dec<80>();
+    regs_dec<64>();
     if constexpr (FULL) {
-      // ---- outputs -----------------------------------------------------------
-      const int pv = ROWS * (warp & 3) + lane % ROWS;
+      // ---- outputs: o^T's rows are channels; turned in shared memory -----------
+      const int w = warp & 3, r = lane >> 2, cc = 2 * (lane & 3);
+      constexpr int SEG = ROWS / 8;  // 16-byte pieces of a token's row that a warp writes
+      const bool vec = p.o_vec;
       uint32_t met = 0;
-      bool any_dead = false;
-      for (int n = 0; !any_dead; ++n) {
+      bool dead = false;
+      for (int n = 0; !dead; ++n) {
         const int st = n % kStages;
         if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
         const int rows = sm.chunk[st].rows;
         IT* out = static_cast<IT*>(p.out) + (int64_t)sm.chunk[st].r0 * p.o_rs +
-                  sm.chunk[st].h * p.o_hs + pv;
+                  sm.chunk[st].h * p.o_hs;
+        unsigned char* turn = Z::kOut ? sm.out : sm.stage[st];
+        const Tables& tab = sm.tab[st];
         if (!warp_wait(sm, g.err, &sm.o_full, n & 1)) break;
-        __syncwarp();
         tc::fence_after_sync();
-        const float back = kBF16 ? 1.0f : sm.row_scale[n & 1][pv];
         const int any = sm.any_bad[n & 1];
-        const int bad = any ? sm.bad[n & 1][pv] : kC;
-#pragma unroll
-        for (int c = 0; c < kC; c += 16) {
+#pragma unroll 1
+        for (int i = 0; i < ROWS / 16 * 2; ++i) {  // 16 channels, 32 tokens
+          const int lh = i >> 1, c0 = (i & 1) * 32, ch = ROWS * w + 16 * lh;
+          float back0 = 1.0f, back1 = 1.0f;
+          if constexpr (!kBF16) {
+            back0 = sm.row_scale[n & 1][ch + r];
+            back1 = sm.row_scale[n & 1][ch + r + 8];
+          }
           float o1[16], o2[16];
-          tc::ld16(tmem + quad + Z::kO1 + c, o1);
-          tc::ld16(tmem + quad + Z::kO2 + c, o2);
+          ld_frag4(tmem + quad + ((uint32_t)(16 * lh) << 16) + Z::kO1 + c0, o1);
+          ld_frag4(tmem + quad + ((uint32_t)(16 * lh) << 16) + Z::kO2 + c0, o2);
           tc::wait_ld();
-          if (c == kC - 16) {  // all of it read
-            if (any) {
-              if (!meet(sm, g.err, &sm.out_warps, met)) any_dead = true;
-              if (lane < ROWS) sm.bad[n & 1][pv] = kC;
-              if (tid == 128) sm.any_bad[n & 1] = 0;
-            }
-            tc::fence_before_sync();
+          uint32_t y[8];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int c = c0 + 8 * f + cc;
+            const float2 e = *reinterpret_cast<const float2*>(tab.ea + c);
+            const float2 b0 = kBF16 ? e : make_float2(e.x * back0, e.y * back0);
+            const float2 b1 = kBF16 ? e : make_float2(e.x * back1, e.y * back1);
+            float2 v0 = __ffma2_rn(make_float2(o2[4 * f], o2[4 * f + 1]), b0,
+                                   make_float2(o1[4 * f], o1[4 * f + 1]));
+            float2 v1 = __ffma2_rn(make_float2(o2[4 * f + 2], o2[4 * f + 3]), b1,
+                                   make_float2(o1[4 * f + 2], o1[4 * f + 3]));
+            y[2 * f] = pack2<IT>(v0.x, v0.y);
+            y[2 * f + 1] = pack2<IT>(v1.x, v1.y);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y = fmaf(o2[i] * back, sm.tab[st].ea[c + i], o1[i]);
-            if (c + i >= bad) y = NAN;
-            if (lane < ROWS && c + i < rows) out[(c + i) * p.o_rs] = from_f<IT>(y);
+          for (int k = 0; k < 2; ++k) {  // 16 tokens x 16 channels
+            const int t = c0 + 16 * k + (lane >> 4) * 8 + (lane & 7);
+            const uint32_t four[4] = {y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+            st_frags<true>(smem_addr(turn) + tile_at(t, ch / 8 + ((lane >> 3) & 1)), four);
           }
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.o_free);
-          mbar_arrive(&sm.empty[st]);
+        if (any) {
+          __syncwarp();
+          if (lane < ROWS) {
+            const int ch = ROWS * w + lane;
+#pragma unroll 1
+            for (int t = sm.bad[n & 1][ch]; t < kC; ++t)
+              reinterpret_cast<IT*>(turn + tile_at(t, ch / 8))[ch % 8] = from_f<IT>(NAN);
+            sm.bad[n & 1][ch] = kC;
+          }
+          if (!meet(sm, g.err, &sm.out_warps, met)) dead = true;  // all have looked at any_bad
+          if (w == 0 && lane == 0) sm.any_bad[n & 1] = 0;
         }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_free);
+        // the warp's channels of every token: 16 bytes a lane
+#pragma unroll 4
+        for (int i = 0; i < kC * SEG / 32; ++i) {
+          const int t = (i * 32 + lane) / SEG, piece = w * SEG + lane % SEG;
+          const uint4 y = *reinterpret_cast<const uint4*>(turn + tile_at(t, piece));
+          if (t >= rows) continue;
+          IT* to = out + t * p.o_rs + piece * 8;
+          if (vec) {
+            *reinterpret_cast<uint4*>(to) = y;
+          } else {
+            const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(u[e >> 1] >> (e & 1 ? 16 : 0));
+          }
+        }
+        tc::fence_proxy_async();  // the stage is filled by copies again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[st]);
       }
     }
+  } else if (wg == 4) {
+    regs_dec<64>();
+    // ---- w V ---------------------------------------------------------------
+    const int w4 = warp & 3;  // pieces w4, w4 + 4, ... of a token's row
+    for (int n = 0;; ++n) {
+      const int st = n % kStages;
+      if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
+      const int rows = sm.chunk[st].rows;
+      unsigned char* k = sm.stage[st] + Z::kQ;
+      unsigned char* v = k + Z::kQ;
+      bool dead = false;
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {
+        const int s = 32 * hh + lane;  // the token whose pieces this thread takes
+        const float w = sm.tab[st].w[s];
+        if (n > 0 && !warp_wait(sm, g.err, &sm.wv_free[hh], (n - 1) & 1)) dead = true;
+        if (rows < kC && s >= rows) {
+          // another sequence's rows: zeros, which leave D alone whatever they held
+#pragma unroll 1
+          for (int i = w4; i < DK / 8; i += 4)
+            *reinterpret_cast<uint4*>(k + tile_at(s, i)) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int i = w4; i < DV / 8; i += 4)
+            *reinterpret_cast<uint4*>(v + tile_at(s, i)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint32_t odd = 0;
+#pragma unroll 2
+        for (int i = 0; i < DV / 32; ++i) {
+          const int at = tile_at(s, 4 * i + w4);
+          const uint4 raw = *reinterpret_cast<const uint4*>(v + at);
+          const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+          uint32_t o[PARTS][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            odd = not_finite<IT>(u[e], odd);
+            float2 x = __fmul2_rn(unpack2<IT>(u[e]), make_float2(w, w));
+            if constexpr (PARTS == 3) {
+              o[0][e] = part_cut(x);
+              o[1][e] = part_cut(x);
+              o[2][e] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+            } else {
+              o[0][e] = part<IT>(x);
+              o[1][e] = pack2<IT>(x.x, x.y);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            *reinterpret_cast<uint4*>(sm.wv[q] + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+        }
+        if (odd) {
+          // A value that is not finite must not reach the tokens before its own, as 0 x
+          // infinity would in P V: it is taken out of V, and the outputs of its channel are
+          // NaN from its token on, as the state is.
+#pragma unroll 1
+          for (int c = 0; c < DV / 4; ++c) {
+            const int piece = 4 * (c / 8) + w4;
+            uint16_t* x = reinterpret_cast<uint16_t*>(v + tile_at(s, piece)) + c % 8;
+            const uint32_t e = kBF16 ? 0x7f80u : 0x7c00u;
+            if ((*x & e) == e) {
+              *x = 0;
+              atomicMin(&sm.bad[n & 1][piece * 8 + c % 8], s);
+              sm.any_bad[n & 1] = 1;
+            }
+          }
+        }
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.wv_ready[hh]);
+      }
+      if (dead) break;
+    }
   } else {
-    regs_inc<120>();
-    // ---- S and w V -------------------------------------------------------
+    regs_inc<112>();
+    // ---- S ---------------------------------------------------------------
     const int half = wg - 2, st_tid = tid - 256;  // 0 .. 255
     const int row = ROWS * (warp & 3) + lane % ROWS;
-    unsigned char* buf = sm.wv[0] + (warp - 8) * ROWS * 80;  // this warp's, while w V is not in use
-    static_assert(8 * ROWS * 80 <= PARTS * Z::kV, "the buffers fit w V's place");
+    unsigned char* buf = sm.turn[warp - 8];
     float S[HALF];
     float total = 1.0f;
     uint32_t met = 0;
@@ -682,7 +927,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     auto state_warps_meet = [&] {
       if (!meet(sm, g.err, &sm.state_warps, met)) dead = true;
     };
-    // S as the next chunk's operand
+    // S as a chunk's operand: columns [c, c + 16), divided by a power of two
+    auto operand = [&](int c, float by) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 v = make_float2(S[c + 2 * i], S[c + 2 * i + 1]);
+        if (!kBF16) v = __fmul2_rn(v, make_float2(by, by));
+        hi[i] = part<IT>(v);
+        lo[i] = pack2<IT>(v.x, v.y);
+      }
+      const uint32_t at = tmem + quad + Z::kS + (half * HALF + c) / 2;
+      st_tmem8(at, hi);
+      st_tmem8(at + HALF, lo);
+    };
+    auto given = [&] {
+      wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.s_ready);
+    };
     auto give = [&](int n) {
       float by = 1.0f;
       if constexpr (!kBF16) {
@@ -701,22 +965,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         state_warps_meet();  // row_max is written again in the next chunk
       }
 #pragma unroll
-      for (int c = 0; c < HALF; c += 16) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x = S[c + 2 * i] * by, y = S[c + 2 * i + 1] * by;
-          hi[i] = part<IT>(x, y);
-          lo[i] = pack2<IT>(x, y);
-        }
-        const uint32_t at = tmem + quad + Z::kS + (half * HALF + c) / 2;
-        st_tmem8(at, hi);
-        st_tmem8(at + HALF, lo);
-      }
-      wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_ready);
+      for (int c = 0; c < HALF; c += 16) operand(c, by);
+      given();
     };
     auto rows_of_state = [&](auto* pool, int64_t slot, int h) {
       return pool + ((slot * p.H + h) * DV + ROWS * (warp & 3)) * DK + half * HALF;
@@ -729,12 +979,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int st = n % kStages;
       if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
       const Tables& tab = sm.tab[st];
-      // what is looked at after w V is given over, when the stage may be filled again
-      const float keep = tab.keep, add = tab.add;
-      const bool last = sm.chunk[st].last;
-      const Piece pc = sm.chunk[st].piece;
-      const int h = sm.chunk[st].h;
-      if (sm.chunk[st].first) {
+      const float keep = tab.keep, add = tab.add, decay = tab.decay;
+      const bool first = sm.chunk[st].first, last = sm.chunk[st].last;
+      Piece pc{};
+      int h = 0;
+      if (first || last) {
+        pc = sm.chunk[st].piece;
+        h = sm.chunk[st].h;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);  // all that this warp looks at
+      if (first) {
 #pragma unroll
         for (int i = 0; i < HALF; ++i) S[i] = 0.0f;
         total = 1.0f;
@@ -758,15 +1013,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int64_t slot = from.id(pc.seq, g.a.idx64);
           if (from.found && slot_ok(slot, p.pad, p.slots) && (!p.has_init || p.has_init[pc.seq])) {
 #pragma unroll
-            for (int c = 0; c < HALF; c += 16) {
+            for (int c = 0; c < HALF; c += 8) {
               if (p.state_dtype == SSU_F32)
-                load_rows16<float, DK, ROWS>(rows_of_state(static_cast<const float*>(p.state), slot, h),
+                load_rows8<float, DK, ROWS>(rows_of_state(static_cast<const float*>(p.state), slot, h),
                                              c, buf, S + c);
               else if (p.state_dtype == SSU_BF16)
-                load_rows16<__nv_bfloat16, DK, ROWS>(
+                load_rows8<__nv_bfloat16, DK, ROWS>(
                     rows_of_state(static_cast<const __nv_bfloat16*>(p.state), slot, h), c, buf, S + c);
               else
-                load_rows16<__half, DK, ROWS>(
+                load_rows8<__half, DK, ROWS>(
                     rows_of_state(static_cast<const __half*>(p.state), slot, h), c, buf, S + c);
             }
           }
@@ -777,55 +1032,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               to[i * ROWS] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
           }
         }
-        state_warps_meet();  // the buffers are w V's again
         if (FULL) give(n);
+        else given();
       }
-      total *= tab.decay;
-      // w V
-      const unsigned char* v = sm.stage[st] + 2 * Z::kQ;
-#pragma unroll 1
-      for (int i = st_tid; i < kC * (DV / 8); i += 256) {
-        const int s = i % kC, at = i / kC * kCol + s * 16;
-        const uint4 raw = *reinterpret_cast<const uint4*>(v + at);
-        uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-        const float w = tab.w[s];
-        uint32_t o[PARTS][4];
-        bool odd = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t e = kBF16 ? 0x7f807f80u : 0x7c007c00u;
-          const uint32_t x = u[k] & e;
-          odd |= (x & 0xffffu) == (e & 0xffffu) || (x >> 16) == (e >> 16);
-          const float2 f = unpack2<IT>(u[k]);
-          float a = f.x * w, b = f.y * w;
-#pragma unroll
-          for (int r = 0; r < PARTS - 1; ++r) o[r][k] = part<IT>(a, b);
-          o[PARTS - 1][k] = pack2<IT>(a, b);
-        }
-#pragma unroll
-        for (int r = 0; r < PARTS; ++r)
-          *reinterpret_cast<uint4*>(sm.wv[r] + at) = make_uint4(o[r][0], o[r][1], o[r][2], o[r][3]);
-        if (odd) {
-          // A value that is not finite must not reach the tokens before its own, as 0 x
-          // infinity would in P V: it is taken out of V, and the outputs of its channel are
-          // NaN from its token on, as the state is.
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t e = kBF16 ? 0x7f80u : 0x7c00u;
-            uint16_t* x = reinterpret_cast<uint16_t*>(const_cast<unsigned char*>(v + at)) + k;
-            if ((*x & e) == e) {
-              *x = 0;
-              atomicMin(&sm.bad[n & 1][i / kC * 8 + k], s);
-              sm.any_bad[n & 1] = 1;
-            }
-          }
-        }
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_ready);
+      total *= decay;
       if (!warp_wait(sm, g.err, &sm.d_full, n & 1)) break;
-      __syncwarp();
       tc::fence_after_sync();
 #pragma unroll
       for (int c = 0; c < HALF; c += 16) {
@@ -833,11 +1044,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc::ld16(tmem + quad + Z::kD + half * HALF + c, d);
         tc::wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[c + i] = fmaf(S[c + i], add, fmaf(keep, S[c + i], d[i]));
+        for (int i = 0; i < 16; i += 2) {
+          const float2 x = make_float2(S[c + i], S[c + i + 1]);
+          const float2 y =
+              __ffma2_rn(x, make_float2(add, add),
+                         __ffma2_rn(x, make_float2(keep, keep), make_float2(d[i], d[i + 1])));
+          S[c + i] = y.x;
+          S[c + i + 1] = y.y;
+        }
+        if (FULL && kBF16 && !last) operand(c, 1.0f);  // of the next chunk
       }
       tc::fence_before_sync();
       if (!last) {
-        if (FULL) give(n + 1);
+        if (FULL && !kBF16) give(n + 1);
+        else given();
         continue;
       }
       if constexpr (!FULL) {
@@ -854,25 +1074,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (from.found && slot_ok(from.id(pc.seq, g.a.idx64), p.pad, p.slots) &&
             write_slot(g.a, pc.seq, 0, p.pad, p.slots, &to)) {
 #pragma unroll
-          for (int c = 0; c < HALF; c += 16) {
+          for (int c = 0; c < HALF; c += 8) {
             if (p.state_dtype == SSU_F32)
-              store_rows16<float, DK, ROWS>(rows_of_state(static_cast<float*>(p.state), to, h), c,
+              store_rows8<float, DK, ROWS>(rows_of_state(static_cast<float*>(p.state), to, h), c,
                                             buf, S + c);
             else if (p.state_dtype == SSU_BF16)
-              store_rows16<__nv_bfloat16, DK, ROWS>(
+              store_rows8<__nv_bfloat16, DK, ROWS>(
                   rows_of_state(static_cast<__nv_bfloat16*>(p.state), to, h), c, buf, S + c);
             else
-              store_rows16<__half, DK, ROWS>(rows_of_state(static_cast<__half*>(p.state), to, h), c,
+              store_rows8<__half, DK, ROWS>(rows_of_state(static_cast<__half*>(p.state), to, h), c,
                                              buf, S + c);
           }
         }
-        state_warps_meet();
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 16) tc::dealloc(tmem, Z::kCols);
+  if (warp == 20) tc::dealloc(tmem, Z::kCols);
 }
 
 }  // namespace linattn

@@ -18,7 +18,7 @@ cudaError_t launch_chunks(const PromptArgs& g, int ctas, cudaStream_t stream) {
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
-  if (fa.numRegs != 96) return cudaErrorInvalidConfiguration;
+  if (fa.numRegs != 80) return cudaErrorInvalidConfiguration;
   kernel<<<(unsigned)ctas, kPromptThreads, ask, stream>>>(g);
   return cudaGetLastError();
 }
