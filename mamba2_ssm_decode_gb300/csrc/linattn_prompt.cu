@@ -24,7 +24,7 @@ struct Layout {
     const int64_t chunks = (rows + kC - 1) / kC;
     // every SM's share of the chunks; sequences beyond it are cut into pieces of a third of it
     const int64_t share = (chunks * heads + sms - 1) / sms;
-    cut = (int)(share / 3 > 4 ? share / 3 : 4);
+    cut = (int)((share + 2) / 3 > 4 ? (share + 2) / 3 : 4);
     fair = (int)(share > cut ? share : cut);
     // a cut sequence has more than 64 `fair` rows, c > fair chunks and at most c / cut + 1
     // pieces; all of them together have at most rows / 64 + 1 chunks each

@@ -24,7 +24,7 @@
 // One CTA of 24 warps works on a chunk of one head at a time, chunks of a
 // sequence in order: 4 warps turn scores into P, 4 write outputs, 8 update S (each
 // owns 32 lanes of tensor memory, so the tiles' rows), 4 weigh V, half a chunk
-// ahead of its product, one issues the products, one has Q, K and V copied (TMA,
+// ahead of its product, three issue the products, one has Q, K and V copied (TMA,
 // three chunks ahead, 128-byte swizzle) and sums the decays.
 // Items -- a sequence's, or a piece's, chunks of one head -- are handed out by a
 // counter, longest first.  A sequence of more chunks than every SM's fair share
@@ -211,10 +211,10 @@ struct PromptSmem {
   Chunk chunk[kStages];
   float row_max[2][128];    // fp16: the largest value of half a row of S
   float row_scale[2][128];  // fp16: what a row of S was divided by
-  int bad[2][128];          // the first token of the chunk whose v is not finite
-  int any_bad[2];
-  uint64_t full[kStages], empty[kStages], sc_full[2];
-  uint64_t p_ready, p_free, o_full, o_free, s_ready, d_full, wv_ready[2], wv_free[2];
+  int bad[kStages][128];    // the first token of the chunk whose v is not finite
+  int any_bad[kStages];
+  uint64_t full[kStages], empty[kStages], v_ready[kStages], sc_full[2], sc_free[2];
+  uint64_t p_ready, p_free, o_full, o_free, s_ready, s_free, d_full, d_free, wv_ready[2], wv_free[2];
   uint64_t state_warps, out_warps, fin;  // warps of a role meet; the last product
   uint32_t tmem;
   int abort;
@@ -233,8 +233,10 @@ __device__ __forceinline__ void wait_st() {
 }
 
 // The products, issued by a whole warp of which one lane is elected (the same one
-// every time): control flow stays uniform, and with it the descriptors in uniform
-// registers.  From a branch that one lane takes, each took 100 to 160 cycles.
+// every time).  What a product is given lies in uniform registers, which takes
+// control flow that the compiler knows to be uniform and unrolled loops: then a
+// product of 128 x 128 x 16 takes 65 cycles, 68 among 20 busy warps; from a loop
+// that is not unrolled 65 and 440.
 // D (tensor memory) = A B^T, or += where `accumulate` is not 0.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                     uint32_t accumulate) {
@@ -310,14 +312,15 @@ __device__ __forceinline__ void st_frags(uint32_t addr, const uint32_t (&w)[4]) 
                  : "memory");
 }
 
-// Waits for a phase; gives up after two seconds, or when another thread did.
+// Waits for a phase; gives up after about two seconds, or when another thread did.
+// Few instructions, because it stands in two dozen places: a test may sleep for a
+// microsecond, and 2^21 of them are the limit.
 template <class SM>
 __device__ __forceinline__ bool wait(SM& sm, unsigned* err, uint64_t* bar, uint32_t parity) {
-  if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = ssu::global_ns();
-  while (!ssu::mbar_test_sleep(bar, parity, 20000u)) {
+#pragma unroll 1
+  for (int tries = 0; !ssu::mbar_test_sleep(bar, parity, 1000u); ++tries) {
     if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-    if (ssu::global_ns() - t0 > ssu::kWaitLimitNs) {
+    if (tries >> 21) {
       *reinterpret_cast<volatile int*>(&sm.abort) = 1;
       atomicOr(err, kErrMma);
       return false;
@@ -478,20 +481,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const Args& p = g.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wg = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), wg = warp >> 2;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 2);              // the copies' bytes; the tables
-      mbar_init(&sm.empty[i], FULL ? 13 : 9);  // the products' end; S's warps; the output warps
+      mbar_init(&sm.empty[i], FULL ? 15 : 9);  // the products' end; S's warps; the output warps
+      mbar_init(&sm.v_ready[i], 4);
     }
-    mbar_init(&sm.sc_full[0], 1);
-    mbar_init(&sm.sc_full[1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.sc_full[i], 1);
+      mbar_init(&sm.sc_free[i], 4);
+    }
     mbar_init(&sm.p_ready, 4);
     mbar_init(&sm.p_free, 1);
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_free, 4);
     mbar_init(&sm.s_ready, 8);
+    mbar_init(&sm.s_free, 1);
+    mbar_init(&sm.d_free, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.wv_ready[i], 4);
       mbar_init(&sm.wv_free[i], 1);
@@ -499,12 +508,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(&sm.d_full, 1);
     mbar_init(&sm.state_warps, 8);
     mbar_init(&sm.out_warps, 4);
-    mbar_init(&sm.fin, 1);
+    mbar_init(&sm.fin, FULL ? 3 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sm.abort = 0;
-    sm.any_bad[0] = sm.any_bad[1] = 0;
+    for (int i = 0; i < kStages; ++i) sm.any_bad[i] = 0;
   }
-  if (tid < 128) sm.bad[0][tid] = sm.bad[1][tid] = kC;
+  if (tid < 128)
+    for (int i = 0; i < kStages; ++i) sm.bad[i][tid] = kC;
   // P above its diagonal stays zero throughout
   for (int i = tid; i < 2 * Z::kP / 16; i += kPromptThreads)
     reinterpret_cast<uint4*>(sm.p[0])[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -518,79 +528,70 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   if (wg == 5) {
     regs_dec<64>();
-    if (warp == 20) {
-      // ---- the products --------------------------------------------------
-      {
-        constexpr uint32_t kIdSc = tc::idesc_f16(kBF16, 64, 64, false, false);
-        constexpr uint32_t kIdO2 = tc::idesc_f16(kBF16, DV, 64, false, false);
-        constexpr uint32_t kIdD = tc::idesc_f16(kBF16, DV, DK, true, true);
-        const uint32_t sp = smem_addr(sm.p[0]), swv = smem_addr(sm.wv[0]);
-        auto at_k = [](int kk) { return (uint32_t)(kk / 4 * kTile + kk % 4 * 32); };
-        auto scores = [&](int n) {
-          const uint32_t q = smem_addr(sm.stage[n % kStages]), k = q + Z::kQ;
+    // ---- the products: scores, D and the outputs' two from a warp each, so that none
+    // waits for what only another one needs
+    if (warp == 20 || warp == 22 || warp == 23) {
+      constexpr uint32_t kIdSc = tc::idesc_f16(kBF16, 64, 64, false, false);
+      constexpr uint32_t kIdO2 = tc::idesc_f16(kBF16, DV, 64, false, false);
+      constexpr uint32_t kIdD = tc::idesc_f16(kBF16, DV, DK, true, true);
+      const uint32_t sp = smem_addr(sm.p[0]), swv = smem_addr(sm.wv[0]);
+      auto at_k = [](int kk) { return (uint32_t)(kk / 4 * kTile + kk % 4 * 32); };
+      for (int n = 0; FULL || warp == 22; ++n) {
+        const int st = n % kStages;
+        if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1)) break;
+        if (__any_sync(0xffffffffu, sm.chunk[st].stop)) break;
+        const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
+        if (warp == 20) {
+          if (n > 1 && !warp_wait(sm, g.err, &sm.sc_free[n & 1], ((n >> 1) - 1) & 1)) break;
           tc::fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
             mma(tmem + Z::kSc + (n & 1) * 64, rows_mn(q + at_k(kk)), rows_mn(k + at_k(kk)), kIdSc,
-                    kk != 0);
+                kk);
           commit(smem_addr(&sm.sc_full[n & 1]));
-        };
-        bool ahead = false;  // the scores of chunk n are under way
-        for (int n = 0;; ++n) {
-          const int st = n % kStages;
-          if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1)) break;
-          if (sm.chunk[st].stop) break;
-          const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
-          if constexpr (FULL) {
-            if (!ahead) scores(n);
-            const int nx = (n + 1) % kStages;
-            ahead = __all_sync(0xffffffffu, mbar_test(&sm.full[nx], ((n + 1) / kStages) & 1)) &&
-                    !sm.chunk[nx].stop;
-            if (ahead) scores(n + 1);
-          }
-          // S is given, and with it D of the chunk before is read
-          if (!warp_wait(sm, g.err, &sm.s_ready, n & 1)) break;
-          if constexpr (FULL) {
-            if (n > 0 && !warp_wait(sm, g.err, &sm.o_free, (n - 1) & 1)) break;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int kk = 0; kk < DK / 16; ++kk)
-                mma_ta(tmem + Z::kO2, tmem + Z::kS + part * HALF + kk * 8, rows_mn(q + at_k(kk)),
-                       kIdO2, (part | kk) != 0);
-          }
-          bool dead = false;
+        } else if (warp == 22) {
+          // D, ahead of S: all that it waits for is the reading of the D before
+          bool dead = n > 0 && !warp_wait(sm, g.err, &sm.d_free, (n - 1) & 1);
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {  // half of the tokens
             dead = dead || !warp_wait(sm, g.err, &sm.wv_ready[hh], n & 1);
             tc::fence_after_sync();
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-              for (int kk = 2 * hh; kk < 2 * hh + 2; ++kk)
-                mma(tmem + Z::kD, rows_k(swv + part * Z::kV + kk * 2048), rows_k(k + kk * 2048), kIdD,
-                    (part | kk) != 0);
+            for (int i = 0; i < 2 * PARTS; ++i) {
+              const int part = i >> 1, kk = 2 * hh + (i & 1);
+              mma(tmem + Z::kD, rows_k(swv + part * Z::kV + kk * 2048), rows_k(k + kk * 2048), kIdD,
+                  part | kk);
+            }
             commit(smem_addr(&sm.wv_free[hh]));
           }
           if (dead) break;
           commit(smem_addr(&sm.d_full));
-          if constexpr (FULL) {
-            if (!warp_wait(sm, g.err, &sm.p_ready, n & 1)) break;
-            tc::fence_after_sync();
-            // tokens before s take nothing from it: the first 16 kk columns are done
+        } else {
+          if (!warp_wait(sm, g.err, &sm.s_ready, n & 1)) break;
+          if (n > 0 && !warp_wait(sm, g.err, &sm.o_free, (n - 1) & 1)) break;
+          tc::fence_after_sync();
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+          for (int i = 0; i < DK / 8; ++i)  // the high parts, then the remainders
+            mma_ta(tmem + Z::kO2, tmem + Z::kS + i * 8, rows_mn(q + at_k(i % (DK / 16))), kIdO2, i);
+          commit(smem_addr(&sm.s_free));
+          // values that are not finite are out of V by then
+          if (!warp_wait(sm, g.err, &sm.v_ready[st], (n / kStages) & 1)) break;
+          if (!warp_wait(sm, g.err, &sm.p_ready, n & 1)) break;
+          tc::fence_after_sync();
+          // tokens before s take nothing from it: the first 16 kk columns are done
 #pragma unroll
-              for (int kk = 0; kk < kC / 16; ++kk)
-                mma(tmem + Z::kO1 + 16 * kk, rows_k(v + kk * 2048),
-                        rows_mn(sp + part * Z::kP + kk * 2048 + kk * 32),
-                        tc::idesc_f16(kBF16, DV, kC - 16 * kk, true, false), (part | kk) != 0);
-            commit(smem_addr(&sm.p_free));
-            commit(smem_addr(&sm.o_full));
+          for (int i = 0; i < kC / 8; ++i) {
+            const int part = i >> 2, kk = i & 3;
+            mma(tmem + Z::kO1 + 16 * kk, rows_k(v + kk * 2048),
+                rows_mn(sp + part * Z::kP + kk * 2048 + kk * 32),
+                tc::idesc_f16(kBF16, DV, kC - 16 * kk, true, false), i);
           }
-          commit(smem_addr(&sm.empty[st]));
+          commit(smem_addr(&sm.p_free));
+          commit(smem_addr(&sm.o_full));
         }
+        commit(smem_addr(&sm.empty[st]));
+      }
+      if (FULL || warp == 22) {
         // nothing is in flight any more when the tensor memory is given back
         commit(smem_addr(&sm.fin));
         const uint64_t t0 = ssu::global_ns();
@@ -619,11 +620,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         float l0 = decay_at(2 * lane), l1 = decay_at(2 * lane + 1);
         for (int c = 0; c < chunks; ++c, ++n) {
           const int st = n % kStages;
+          const int t0 = c * kC, rows = min(kC, piece.len - t0);
+          // A log decay below -160 (in units of log2) is a decay of zero in fp32 and is held
+          // there.
+          auto held = [](float l) {
+            l *= kLog2e;
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-160.0f));
+            return l;
+          };
+          const float d0 = held(l0), d1 = held(l1);
+          l0 = decay_at(t0 + kC + 2 * lane);
+          l1 = decay_at(t0 + kC + 2 * lane + 1);
+          // a_t in 64 bits, so that differences of large sums keep their digits: in units of
+          // 2^-44 (sums of doubles took this warp twice the time of a chunk's products), or
+          // as doubles where the batch has something that these do not hold
+          float a0, a1, x0, x1, w0, w1, end;  // a_t; r - a_t; a_C - a_t; a_C
+          auto sums = [&](auto e0, auto e1, float unit) {
+            auto inc = e0 + e1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const auto u = __shfl_up_sync(0xffffffffu, inc, o);
+              if (lane >= o) inc += u;
+            }
+            const auto all = __shfl_sync(0xffffffffu, inc, 31);
+            const auto ref = __shfl_sync(0xffffffffu, inc, lane | 7);
+            const auto before = inc - e1;
+            a0 = (float)before * unit;
+            a1 = (float)inc * unit;
+            x0 = (float)(ref - before) * unit;
+            x1 = (float)(ref - inc) * unit;
+            w0 = (float)(all - before) * unit;
+            w1 = (float)(all - inc) * unit;
+            end = (float)all * unit;
+          };
+          if (__all_sync(0xffffffffu, d0 <= 4096.0f && d1 <= 4096.0f))
+            sums(__float2ll_rn(d0 * 0x1p44f), __float2ll_rn(d1 * 0x1p44f), 0x1p-44f);
+          else
+            sums((double)d0, (double)d1, 1.0f);
+          // all of it before the stage is free
+          const int t = 2 * lane;
+          const float2 x = make_float2(ex2(x0), ex2(x1));
+          const float2 ea = make_float2(p.scale * ex2(a0), p.scale * ex2(a1));
+          const float2 w = make_float2(t < rows ? ex2(w0) : 0.0f, t + 1 < rows ? ex2(w1) : 0.0f);
+          const bool mild =
+              __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f);
+          // near 1 the decay is 1 + add: rounded by itself it would be off by the same
+          // 2^-25 chunk after chunk
+          const float e = ex2(end);
+          const float keep = e > 0.5f ? 1.0f : 0.0f;
+          const float add = e > 0.5f ? expm1f(end * 0.693147181f) : e;
           if (n >= kStages && !warp_wait(sm, g.err, &sm.empty[st], (n / kStages - 1) & 1)) {
             live = false;
             break;
           }
-          const int t0 = c * kC, rows = min(kC, piece.len - t0);
           if (lane == 0) {
             const uint32_t q = smem_addr(sm.stage[st]), k = q + Z::kQ, v = k + Z::kQ;
             const uint32_t bar = smem_addr(&sm.full[st]);
@@ -638,45 +687,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               load_box(v + i * kTile, &g.v, bar, 64 * i, h, piece.r0 + t0);
             sm.chunk[st] = Chunk{h, piece.r0 + t0, rows, c == 0, c == chunks - 1, 0, piece};
           }
-          // a_t in 64 bits: differences of large sums keep their digits.  A log decay below
-          // -160 (in units of log2) is a decay of zero in fp32 and is held there.
-          auto held = [](float l) {
-            l *= kLog2e;
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-160.0f));
-            return (double)l;
-          };
-          const double d0 = held(l0), d1 = held(l1);
-          l0 = decay_at(t0 + kC + 2 * lane);
-          l1 = decay_at(t0 + kC + 2 * lane + 1);
-          double inc = d0 + d1;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-          }
-          const double end = __shfl_sync(0xffffffffu, inc, 31);
-          const double ref = __shfl_sync(0xffffffffu, inc, lane | 7);
-          const double a1 = inc, a0 = inc - d1;
           Tables& tab = sm.tab[st];
-          const int t = 2 * lane;
-          const float x0 = (float)(ref - a0), x1 = (float)(ref - a1);
-          *reinterpret_cast<float2*>(tab.a + t) = make_float2((float)a0, (float)a1);
-          *reinterpret_cast<float2*>(tab.x + t) = make_float2(exp2f(x0), exp2f(x1));
-          *reinterpret_cast<float2*>(tab.ea + t) =
-              make_float2(p.scale * exp2f((float)a0), p.scale * exp2f((float)a1));
-          *reinterpret_cast<float2*>(tab.w + t) =
-              make_float2(t < rows ? exp2f((float)(end - a0)) : 0.0f,
-                          t + 1 < rows ? exp2f((float)(end - a1)) : 0.0f);
-          const bool mild =
-              __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f);
-          if ((lane & 7) == 7) tab.r[lane / 8] = (float)a1;
+          *reinterpret_cast<float2*>(tab.a + t) = make_float2(a0, a1);
+          *reinterpret_cast<float2*>(tab.x + t) = x;
+          *reinterpret_cast<float2*>(tab.ea + t) = ea;
+          *reinterpret_cast<float2*>(tab.w + t) = w;
+          if ((lane & 7) == 7) tab.r[lane / 8] = a1;
           if (lane == 0) {
-            // near 1 the decay is 1 + add: rounded by itself it would be off by the same
-            // 2^-25 chunk after chunk
-            const float e = exp2f((float)end);
             tab.decay = e;
-            tab.keep = e > 0.5f ? 1.0f : 0.0f;
-            tab.add = e > 0.5f ? expm1f((float)(end * 0.69314718055994531)) : e;
+            tab.keep = keep;
+            tab.add = add;
             tab.mild = mild;
           }
           __syncwarp();
@@ -751,7 +771,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc::fence_proxy_async();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready);
+        if (lane == 0) {
+          mbar_arrive(&sm.sc_free[n & 1]);
+          mbar_arrive(&sm.p_ready);
+        }
       }
     }
   } else if (wg == 1) {
@@ -773,7 +796,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const Tables& tab = sm.tab[st];
         if (!warp_wait(sm, g.err, &sm.o_full, n & 1)) break;
         tc::fence_after_sync();
-        const int any = sm.any_bad[n & 1];
+        const int any = sm.any_bad[st];
 #pragma unroll 1
         for (int i = 0; i < ROWS / 16 * 2; ++i) {  // 16 channels, 32 tokens
           const int lh = i >> 1, c0 = (i & 1) * 32, ch = ROWS * w + 16 * lh;
@@ -812,12 +835,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (lane < ROWS) {
             const int ch = ROWS * w + lane;
 #pragma unroll 1
-            for (int t = sm.bad[n & 1][ch]; t < kC; ++t)
+            for (int t = sm.bad[st][ch]; t < kC; ++t)
               reinterpret_cast<IT*>(turn + tile_at(t, ch / 8))[ch % 8] = from_f<IT>(NAN);
-            sm.bad[n & 1][ch] = kC;
+            sm.bad[st][ch] = kC;
           }
           if (!meet(sm, g.err, &sm.out_warps, met)) dead = true;  // all have looked at any_bad
-          if (w == 0 && lane == 0) sm.any_bad[n & 1] = 0;
+          if (w == 0 && lane == 0) sm.any_bad[st] = 0;
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -903,8 +926,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const uint32_t e = kBF16 ? 0x7f80u : 0x7c00u;
             if ((*x & e) == e) {
               *x = 0;
-              atomicMin(&sm.bad[n & 1][piece * 8 + c % 8], s);
-              sm.any_bad[n & 1] = 1;
+              atomicMin(&sm.bad[st][piece * 8 + c % 8], s);
+              sm.any_bad[st] = 1;
             }
           }
         }
@@ -912,6 +935,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.wv_ready[hh]);
       }
+      if (lane == 0) mbar_arrive(&sm.v_ready[st]);
       if (dead) break;
     }
   } else {
@@ -1032,8 +1056,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               to[i * ROWS] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
           }
         }
-        if (FULL) give(n);
-        else given();
+      }
+      if constexpr (FULL) {
+        // o2 of the chunk before has read its S
+        if (n > 0 && !warp_wait(sm, g.err, &sm.s_free, (n - 1) & 1)) break;
+        tc::fence_after_sync();
+        give(n);
       }
       total *= decay;
       if (!warp_wait(sm, g.err, &sm.d_full, n & 1)) break;
@@ -1052,14 +1080,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           S[c + i] = y.x;
           S[c + i + 1] = y.y;
         }
-        if (FULL && kBF16 && !last) operand(c, 1.0f);  // of the next chunk
       }
       tc::fence_before_sync();
-      if (!last) {
-        if (FULL && !kBF16) give(n + 1);
-        else given();
-        continue;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.d_free);
+      if (!last) continue;
       if constexpr (!FULL) {
         if (lane < ROWS) {
           float4* to = entry(pc.base + pc.j + 1, h);
