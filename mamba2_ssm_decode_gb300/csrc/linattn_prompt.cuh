@@ -19,7 +19,9 @@
 // that add up to them: P and S as a high part and a remainder (to 2^-17 of each
 // with bf16, 2^-22 with fp16, where one part alone would be as far off as the
 // output's own rounding), w V as three of bf16 where the state is kept in 32 bits
-// (2^-26; two leave 2^-17, which shows in it), else two.
+// (2^-26; two leave 2^-17, which shows in it), else two.  fp16 has no room for what
+// is large or small: there the rows of P and S and all of a chunk's w V are brought
+// to the middle of its range by powers of two, which are taken out of the products.
 //
 // One CTA of 24 warps works on a chunk of one head at a time, chunks of a
 // sequence in order: 4 warps turn scores into P, 4 write outputs, 8 update S (each
@@ -209,13 +211,18 @@ struct PromptSmem {
   unsigned char turn[8][DV / 4 * 48];  // rows of S on their way from and to global memory
   Tables tab[kStages];
   Chunk chunk[kStages];
-  float row_max[2][128];    // fp16: the largest value of half a row of S
-  float row_scale[2][128];  // fp16: what a row of S was divided by
+  // fp16 (two parts) alone
+  static constexpr int kScaled = PARTS == 2 ? 128 : 1;
+  float row_max[2][kScaled];    // the largest value of half a row of S
+  float row_scale[2][kScaled];  // what a row of S was divided by
+  float p_scale[2][kScaled];    // ... a token's row of P
+  float v_scale[kStages];       // ... w V
+  uint32_t v_max[4];
   int bad[kStages][128];    // the first token of the chunk whose v is not finite
   int any_bad[kStages];
   uint64_t full[kStages], empty[kStages], v_ready[kStages], sc_full[2], sc_free[2];
   uint64_t p_ready, p_free, o_full, o_free, s_ready, s_free, d_full, d_free, wv_ready[2], wv_free[2];
-  uint64_t state_warps, out_warps, fin;  // warps of a role meet; the last product
+  uint64_t state_warps, out_warps, v_warps, fin;  // warps of a role meet; the last product
   uint32_t tmem;
   int abort;
 };
@@ -383,6 +390,16 @@ __device__ __forceinline__ uint32_t part_cut(float2& v) {
   return __byte_perm(x, y, 0x7632);
 }
 
+// The power of two that brings m to [2^to, 2^(to + 1)), and its reciprocal; 1 where m
+// is 0 or not finite.  Held so that both are fp32 numbers.
+__device__ __forceinline__ float toward(float m, int to, float* back) {
+  const int field = (int)(__float_as_uint(m) >> 23) & 255;
+  int e = field - 127 - to;
+  e = field == 255 || !(m > 0.0f) ? 0 : e < -100 ? -100 : e > 110 ? 110 : e;
+  *back = __uint_as_float((uint32_t)(127 + e) << 23);
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
 // Stays 0 while the two values of every word are finite.
 template <class IT>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w, uint32_t acc) {
@@ -508,6 +525,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     mbar_init(&sm.d_full, 1);
     mbar_init(&sm.state_warps, 8);
     mbar_init(&sm.out_warps, 4);
+    mbar_init(&sm.v_warps, 4);
     mbar_init(&sm.fin, FULL ? 3 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sm.abort = 0;
@@ -731,13 +749,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!warp_wait(sm, g.err, &sm.sc_full[n & 1], (n >> 1) & 1)) break;
         if (n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
         tc::fence_after_sync();
-#pragma unroll 1
-        for (int b = 0; b <= warp; ++b) {  // 16 columns
+        // 16 columns: scale e^(a_t - a_s) q_t . k_s, 0 above the diagonal
+        auto weighed = [&](int b, float2 (&y)[4]) {
           float s[8];
           ld_frag2(tmem + quad + Z::kSc + (n & 1) * 64 + 16 * b, s);
           const float u0 = p.scale * ex2(a0 - tab.r[b]), u1 = p.scale * ex2(a1 - tab.r[b]);
           tc::wait_ld();
-          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {  // 8 columns
             const int c = 16 * b + 8 * f + cc;
@@ -751,22 +768,69 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               e0 = make_float2(p.scale * ex2(a0 - x.x), p.scale * ex2(a0 - x.y));
               e1 = make_float2(p.scale * ex2(a1 - x.x), p.scale * ex2(a1 - x.y));
             }
-            float2 y0 = __fmul2_rn(make_float2(s[4 * f], s[4 * f + 1]), e0);
-            float2 y1 = __fmul2_rn(make_float2(s[4 * f + 2], s[4 * f + 3]), e1);
+            float2 &y0 = y[2 * f], &y1 = y[2 * f + 1];
+            y0 = __fmul2_rn(make_float2(s[4 * f], s[4 * f + 1]), e0);
+            y1 = __fmul2_rn(make_float2(s[4 * f + 2], s[4 * f + 3]), e1);
             if (b == warp) {
               if (c > t0) y0.x = 0.0f;
               if (c + 1 > t0) y0.y = 0.0f;
               if (c > t1) y1.x = 0.0f;
               if (c + 1 > t1) y1.y = 0.0f;
             }
-            hi[2 * f] = part<IT>(y0);
-            lo[2 * f] = pack2<IT>(y0.x, y0.y);
-            hi[2 * f + 1] = part<IT>(y1);
-            lo[2 * f + 1] = pack2<IT>(y1.x, y1.y);
+          }
+        };
+        auto leave = [&](int b, float2 (&y)[4]) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = part<IT>(y[i]);
+            lo[i] = pack2<IT>(y[i].x, y[i].y);
           }
           const uint32_t to = smem_addr(sm.p[0]) + tile_at(mrow, 2 * b + mpiece);
           st_frags<false>(to, hi);
           st_frags<false>(to + Z::kP, lo);
+        };
+        if constexpr (kBF16) {
+#pragma unroll 1
+          for (int b = 0; b <= warp; ++b) {
+            float2 y[4];
+            weighed(b, y);
+            leave(b, y);
+          }
+        } else {
+          float2 y[4][4];
+          float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (b > warp) continue;
+            weighed(b, y[b]);
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              m0 = fmaxf(m0, fmaxf(fabsf(y[b][2 * f].x), fabsf(y[b][2 * f].y)));
+              m1 = fmaxf(m1, fmaxf(fabsf(y[b][2 * f + 1].x), fabsf(y[b][2 * f + 1].y)));
+            }
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          float back0, back1;
+          const float by0 = toward(m0, 10, &back0), by1 = toward(m1, 10, &back1);
+          if ((lane & 3) == 0) {
+            sm.p_scale[n & 1][t0] = back0;
+            sm.p_scale[n & 1][t1] = back1;
+          }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            if (b > warp) continue;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              y[b][2 * f] = __fmul2_rn(y[b][2 * f], make_float2(by0, by0));
+              y[b][2 * f + 1] = __fmul2_rn(y[b][2 * f + 1], make_float2(by1, by1));
+            }
+            leave(b, y[b]);
+          }
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
@@ -816,10 +880,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const float2 e = *reinterpret_cast<const float2*>(tab.ea + c);
             const float2 b0 = kBF16 ? e : make_float2(e.x * back0, e.y * back0);
             const float2 b1 = kBF16 ? e : make_float2(e.x * back1, e.y * back1);
-            float2 v0 = __ffma2_rn(make_float2(o2[4 * f], o2[4 * f + 1]), b0,
-                                   make_float2(o1[4 * f], o1[4 * f + 1]));
-            float2 v1 = __ffma2_rn(make_float2(o2[4 * f + 2], o2[4 * f + 3]), b1,
-                                   make_float2(o1[4 * f + 2], o1[4 * f + 3]));
+            float2 v0 = make_float2(o1[4 * f], o1[4 * f + 1]);
+            float2 v1 = make_float2(o1[4 * f + 2], o1[4 * f + 3]);
+            if constexpr (!kBF16) {
+              const float2 back = *reinterpret_cast<const float2*>(&sm.p_scale[n & 1][c]);
+              v0 = __fmul2_rn(v0, back);
+              v1 = __fmul2_rn(v1, back);
+            }
+            v0 = __ffma2_rn(make_float2(o2[4 * f], o2[4 * f + 1]), b0, v0);
+            v1 = __ffma2_rn(make_float2(o2[4 * f + 2], o2[4 * f + 3]), b1, v1);
             y[2 * f] = pack2<IT>(v0.x, v0.y);
             y[2 * f + 1] = pack2<IT>(v1.x, v1.y);
           }
@@ -870,6 +939,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     regs_dec<64>();
     // ---- w V ---------------------------------------------------------------
     const int w4 = warp & 3;  // pieces w4, w4 + 4, ... of a token's row
+    uint32_t met = 0;
     for (int n = 0;; ++n) {
       const int st = n % kStages;
       if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
@@ -877,10 +947,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       unsigned char* k = sm.stage[st] + Z::kQ;
       unsigned char* v = k + Z::kQ;
       bool dead = false;
+      float by = 1.0f;
+      if constexpr (!kBF16) {
+        // the largest |w v| of the chunk comes to 2^14
+        float m = 0.0f;
+#pragma unroll 1
+        for (int s = lane; s < min(rows, kC); s += 32) {
+          __half2 top{};
+#pragma unroll 2
+          for (int i = w4; i < DV / 8; i += 4) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(v + tile_at(s, i));
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&u[e])));
+          }
+          m = fmaxf(m, sm.tab[st].w[s] * fmaxf(__low2float(top), __high2float(top)));
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (n > 0 && !warp_wait(sm, g.err, &sm.wv_free[0], (n - 1) & 1)) dead = true;
+        if (lane == 0) sm.v_max[w4] = most;
+        if (!meet(sm, g.err, &sm.v_warps, met)) dead = true;
+        m = __uint_as_float(max(max(sm.v_max[0], sm.v_max[1]), max(sm.v_max[2], sm.v_max[3])));
+        float back;
+        by = toward(m, 14, &back);
+        if (w4 == 0 && lane == 0) sm.v_scale[st] = back;
+        if (!meet(sm, g.err, &sm.v_warps, met)) dead = true;  // v_max is written again
+      }
 #pragma unroll 1
       for (int hh = 0; hh < 2; ++hh) {
         const int s = 32 * hh + lane;  // the token whose pieces this thread takes
-        const float w = sm.tab[st].w[s];
+        const float w = sm.tab[st].w[s] * by;
         if (n > 0 && !warp_wait(sm, g.err, &sm.wv_free[hh], (n - 1) & 1)) dead = true;
         if (rows < kC && s >= rows) {
           // another sequence's rows: zeros, which leave D alone whatever they held
@@ -981,11 +1078,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (lane < ROWS) sm.row_max[half][row] = m;
         state_warps_meet();
         m = fmaxf(sm.row_max[0][row], sm.row_max[1][row]);
-        int e = (int)((__float_as_uint(m) >> 23) & 255) - 127 - 10;
-        e = m > 0.0f ? (e < -100 ? -100 : e > 110 ? 110 : e) : 0;
-        by = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (half == 0 && lane < ROWS)
-          sm.row_scale[n & 1][row] = __uint_as_float((uint32_t)(127 + e) << 23);
+        float back;
+        by = toward(m, 10, &back);
+        if (half == 0 && lane < ROWS) sm.row_scale[n & 1][row] = back;
         state_warps_meet();  // row_max is written again in the next chunk
       }
 #pragma unroll
@@ -1066,6 +1161,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       total *= decay;
       if (!warp_wait(sm, g.err, &sm.d_full, n & 1)) break;
       tc::fence_after_sync();
+      float back = 1.0f;
+      if constexpr (!kBF16) back = sm.v_scale[st];
 #pragma unroll
       for (int c = 0; c < HALF; c += 16) {
         float d[16];
@@ -1074,9 +1171,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           const float2 x = make_float2(S[c + i], S[c + i + 1]);
-          const float2 y =
-              __ffma2_rn(x, make_float2(add, add),
-                         __ffma2_rn(x, make_float2(keep, keep), make_float2(d[i], d[i + 1])));
+          float2 y = make_float2(d[i], d[i + 1]);
+          if constexpr (kBF16)
+            y = __ffma2_rn(x, make_float2(keep, keep), y);
+          else  // keep is 0 or 1: rounded once, too
+            y = __ffma2_rn(y, make_float2(back, back), __fmul2_rn(x, make_float2(keep, keep)));
+          y = __ffma2_rn(x, make_float2(add, add), y);
           S[c + i] = y.x;
           S[c + i + 1] = y.y;
         }

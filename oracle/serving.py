@@ -65,9 +65,9 @@ def linattn(q, k, v, log_decay=None, scale=1.0, pool=None, init=None, write=True
 
 
 def _best(row):
-    """The largest value's lowest place; NaN is never the largest (-1: nothing else)."""
-    row = np.where(np.isnan(row), -np.inf, row)
-    return int(row.argmax()) if (row > -np.inf).any() or len(row) else -1
+    """The largest value's lowest place; NaN is never it (-1: there is nothing else)."""
+    numbers = np.flatnonzero(~np.isnan(row))
+    return int(numbers[row[numbers].argmax()]) if len(numbers) else -1
 
 
 def verify(p, drafts, u, q=None, cu=None, greedy=None):
@@ -94,7 +94,7 @@ def verify(p, drafts, u, q=None, cu=None, greedy=None):
             inside = 0 <= d < V
             if greedy is not None and bool(greedy[s]):
                 best = _best(row)
-                if j < n and best == d:
+                if j < n and best == d and inside:
                     taken.append(d)
                 else:
                     token = best
