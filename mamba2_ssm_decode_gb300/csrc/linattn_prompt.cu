@@ -16,8 +16,8 @@ cudaError_t launch_chunks_f16(const PromptArgs& g, int ctas, cudaStream_t stream
 // How a call is cut, and where its workspace holds what.
 struct Layout {
   int fair, cut;
-  int64_t entries, pieces;  // most states, most pieces
-  int64_t piece_at[2], decay_at, state_at, bytes;
+  int64_t entries, pieces, split;  // most states, pieces, sequences in pieces
+  int64_t piece_at[2], cut_at, decay_at, state_at, bytes;
 
   Layout(int64_t rows, int64_t nseqs, int64_t heads, int64_t dv, int64_t dk) {
     const int64_t sms = ssu::sm_count();
@@ -25,11 +25,13 @@ struct Layout {
     // every SM's share of the chunks; sequences beyond it are cut into pieces of a third of it
     const int64_t share = (chunks * heads + sms - 1) / sms;
     cut = (int)((share + 2) / 3 > 4 ? (share + 2) / 3 : 4);
-    fair = (int)(share > cut ? share : cut);
+    // ... where that saves more than the two launches it takes, some four chunks' time
+    const int64_t worth = 2 * (int64_t)cut + 4;
+    fair = (int)(share > worth ? share : worth);
     // a cut sequence has more than 64 `fair` rows, c > fair chunks and at most c / cut + 1
     // pieces; all of them together have at most rows / 64 + 1 chunks each
     const int64_t most = rows / ((int64_t)kC * fair);
-    const int64_t split = nseqs < most ? nseqs : most;
+    split = nseqs < most ? nseqs : most;
     entries = split ? (rows / kC + split) / cut + split : 0;
     pieces = nseqs + entries;
     auto round = [](int64_t n) { return (n + 255) / 256 * 256; };
@@ -38,6 +40,8 @@ struct Layout {
       piece_at[i] = at;
       at += round((i ? pieces : entries) * (int64_t)sizeof(Piece));
     }
+    cut_at = at;
+    at += round(split * (int64_t)sizeof(CutSeq));
     decay_at = at;
     at += round(entries * heads * 4);
     state_at = at;
@@ -99,11 +103,13 @@ cudaError_t launch_prompt(const Args& p, const Seqs& a, ssu_dtype io, void* work
   g.a = a;
   g.head = reinterpret_cast<Header*>(ws);
   for (int i = 0; i < 2; ++i) g.pieces[i] = reinterpret_cast<Piece*>(ws + l.piece_at[i]);
+  g.cuts = reinterpret_cast<CutSeq*>(ws + l.cut_at);
   g.decay = reinterpret_cast<float*>(ws + l.decay_at);
   g.state = reinterpret_cast<float*>(ws + l.state_at);
   g.fair = l.fair;
   g.cut = l.cut;
   g.entries = (int)l.entries;
+  g.splits = (int)l.split;
   g.err = ssu::device_error_word();
   if (!g.err) return cudaErrorInvalidValue;
   if (!map_of(&g.q, io == SSU_BF16, p.q, a.rows, p.G, p.dk, p.q_rs, p.q_gs) ||
@@ -121,6 +127,11 @@ cudaError_t launch_prompt(const Args& p, const Seqs& a, ssu_dtype io, void* work
   const bool bf16 = io == SSU_BF16;
   if (l.entries > 0) {
     e = (bf16 ? launch_pieces_bf16 : launch_pieces_f16)(g, ctas(l.entries), stream);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)p.H * p.dv * p.dk / 4;
+    e = launch_after(linattn_join_kernel,
+                     dim3((unsigned)((items + kJoinThreads - 1) / kJoinThreads), (unsigned)l.split),
+                     kJoinThreads, 0, stream, g);
     if (e != cudaSuccess) return e;
   }
   return (bf16 ? launch_chunks_bf16 : launch_chunks_f16)(g, ctas(l.pieces), stream);

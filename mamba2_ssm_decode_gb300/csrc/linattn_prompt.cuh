@@ -31,8 +31,9 @@
 // Items -- a sequence's, or a piece's, chunks of one head -- are handed out by a
 // counter, longest first.  A sequence of more chunks than every SM's fair share
 // is cut into pieces: a first launch computes what each piece adds to the state
-// (the fourth product alone) and its decay, and a piece's item then starts by
-// adding up the pieces before it.
+// (the fourth product alone) and its decay, a second one adds them up to the state
+// that enters each piece.  Every launch but the first is set up while the one before
+// runs (programmatic dependent launch).
 #pragma once
 
 #include <cuda.h>
@@ -61,8 +62,14 @@ struct Piece {
 
 // What the plan leaves in the workspace.
 struct Header {
-  int next[2];   // items handed out: of the first launch, of the second
+  int next[2];   // items handed out: of the pieces' launch, of the last
   int count[2];  // pieces of each
+  int cuts;      // sequences in pieces
+};
+
+// A sequence in pieces: its entries in the workspace's states.
+struct CutSeq {
+  int base, of;
 };
 
 struct PromptArgs {
@@ -71,10 +78,11 @@ struct PromptArgs {
   Seqs a;
   Header* head;
   Piece* pieces[2];
+  CutSeq* cuts;
   float* decay;  // [entries][H]: what a piece decays the state by
   float* state;  // [entries][H][dv * dk], in the threads' order
   int fair, cut;  // chunks: more than `fair` of them are cut into pieces of about `cut`
-  int entries;
+  int entries, splits;  // room: states, sequences in pieces
   unsigned* err;
 };
 
@@ -85,7 +93,10 @@ constexpr int kPlanThreads = 1024, kBuckets = 64;
 
 struct Cut {
   int r0, len, chunks, pieces, each;  // each: chunks of a piece (the last may have fewer)
+  Cut() = default;
   __device__ __forceinline__ Cut(const PromptArgs& g, int s, bool split) {
+    r0 = len = chunks = pieces = each = 0;
+    if (s >= g.a.n) return;
     r0 = clamped(load_int(g.a.cu, s, g.a.meta64), g.a.rows);
     const int end = clamped(load_int(g.a.cu, s + 1, g.a.meta64), g.a.rows);
     len = end > r0 ? end - r0 : 0;
@@ -103,51 +114,144 @@ struct Cut {
   }
 };
 
+// What follows may be set up by now; it waits for this launch's end all the same.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// The launch before has ended, and its results can be read.
+__device__ __forceinline__ void launch_before_ended() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A launch that may be set up while the one before it on the stream still runs.
+template <class... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// f(piece, base, j) for every piece of sequences s .. s + 31 (a lane's own is c): a
+// whole sequence by its lane, one in pieces by all lanes.  base: of its entries.
+template <class F>
+__device__ __forceinline__ void each_piece(const Cut& c, int base, F f) {
+  const int lane = threadIdx.x & 31;
+  if (c.pieces == 1) f(c, base, lane, 0);
+  for (unsigned m = __ballot_sync(0xffffffffu, c.pieces > 1); m; m &= m - 1) {
+    const int from = __ffs(m) - 1;
+    Cut d;
+    d.r0 = __shfl_sync(0xffffffffu, c.r0, from);
+    d.len = __shfl_sync(0xffffffffu, c.len, from);
+    d.chunks = __shfl_sync(0xffffffffu, c.chunks, from);
+    d.pieces = __shfl_sync(0xffffffffu, c.pieces, from);
+    d.each = __shfl_sync(0xffffffffu, c.each, from);
+    const int b = __shfl_sync(0xffffffffu, base, from);
+    for (int j = lane; j < d.pieces; j += 32) f(d, b, from, j);
+  }
+}
+
 static __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const PromptArgs g) {
   __shared__ int at[2][kBuckets];
-  __shared__ int used, want;
-  const int tid = threadIdx.x;
+  __shared__ int used, want, many, cuts;
+  let_next_start();
+  const int tid = threadIdx.x, lane = tid & 31;
   if (tid < kBuckets) at[0][tid] = at[1][tid] = 0;
-  if (tid == 0) used = want = 0;
+  if (tid == 0) used = want = many = cuts = 0;
   __syncthreads();
   for (int s = tid; s < g.a.n; s += kPlanThreads) {
     const Cut c(g, s, true);
-    if (c.pieces > 1) atomicAdd(&want, c.pieces);
+    if (c.pieces > 1) {
+      atomicAdd(&want, c.pieces);
+      atomicAdd(&many, 1);
+    }
   }
   __syncthreads();
   // starts that do not ascend could ask for more than the workspace has room for
-  const bool split = want <= g.entries;
-  for (int s = tid; s < g.a.n; s += kPlanThreads) {
-    const Cut c(g, s, split);
-    for (int j = 0; j < c.pieces; ++j) {
+  const bool split = want <= g.entries && many <= g.splits;
+  for (int s0 = tid - lane; s0 < g.a.n; s0 += kPlanThreads)
+    each_piece(Cut(g, s0 + lane, split), 0, [&](const Cut& c, int, int, int j) {
       const int b = c.bucket(g, j);
       atomicAdd(&at[1][b], 1);
       if (j + 1 < c.pieces) atomicAdd(&at[0][b], 1);
+    });
+  __syncthreads();
+  if (tid < 64) {  // where each bucket starts
+    static_assert(kBuckets == 64, "two of a lane");
+    int* mine = at[tid >> 5];
+    const int n0 = mine[2 * lane], n1 = mine[2 * lane + 1];
+    int inc = n0 + n1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    mine[2 * lane] = inc - n0 - n1;
+    mine[2 * lane + 1] = inc - n1;
+    if (lane == 31) {
+      g.head->count[tid >> 5] = inc;
+      g.head->next[tid >> 5] = 0;
     }
   }
   __syncthreads();
-  if (tid < 2) {
-    int sum = 0;
-    for (int b = 0; b < kBuckets; ++b) {
-      const int n = at[tid][b];
-      at[tid][b] = sum;
-      sum += n;
-    }
-    g.head->count[tid] = sum;
-    g.head->next[tid] = 0;
-  }
-  __syncthreads();
-  for (int s = tid; s < g.a.n; s += kPlanThreads) {
-    const Cut c(g, s, split);
+  for (int s0 = tid - lane; s0 < g.a.n; s0 += kPlanThreads) {
+    const Cut c(g, s0 + lane, split);
     int base = 0;
-    if (c.pieces > 1) base = atomicAdd(&used, c.pieces);
-    for (int j = 0; j < c.pieces; ++j) {
-      const int first = j * c.each * kC;
-      const Piece piece{s, c.r0 + first, min(c.len - first, c.each * kC), j, c.pieces, base};
-      const int b = c.bucket(g, j);
-      g.pieces[1][atomicAdd(&at[1][b], 1)] = piece;
-      if (j + 1 < c.pieces) g.pieces[0][atomicAdd(&at[0][b], 1)] = piece;
+    if (c.pieces > 1) {
+      base = atomicAdd(&used, c.pieces);
+      g.cuts[atomicAdd(&cuts, 1)] = CutSeq{base, c.pieces};
     }
+    each_piece(c, base, [&](const Cut& d, int b, int from, int j) {
+      const int first = j * d.each * kC;
+      const Piece piece{s0 + from, d.r0 + first, min(d.len - first, d.each * kC), j, d.pieces, b};
+      const int k = d.bucket(g, j);
+      g.pieces[1][atomicAdd(&at[1][k], 1)] = piece;
+      if (j + 1 < d.pieces) g.pieces[0][atomicAdd(&at[0][k], 1)] = piece;
+    });
+  }
+  __syncthreads();
+  if (tid == 0) g.head->cuts = cuts;
+}
+
+// ---------------------------------------------------------------------------
+// the states that enter pieces
+// ---------------------------------------------------------------------------
+// Entry base is the state that enters the first piece, base + 1 the one that leaves
+// it, base + j + 1 what piece j adds; from the third on they become what enters
+// piece j: E_j = decay of piece j - 1 E_(j - 1) + what it adds.
+constexpr int kJoinThreads = 256;
+
+static __global__ void __launch_bounds__(kJoinThreads) linattn_join_kernel(const PromptArgs g) {
+  let_next_start();
+  launch_before_ended();
+  if ((int)blockIdx.y >= g.head->cuts) return;
+  const CutSeq c = g.cuts[blockIdx.y];
+  const int64_t per = (int64_t)g.p.dv * g.p.dk / 4, all = per * g.p.H;  // of an entry
+  const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  if (i >= all || c.of < 3) return;
+  const int h = (int)(i / per);
+  float4* e = reinterpret_cast<float4*>(g.state) + (int64_t)(c.base + 1) * all + i;
+  const float* by = g.decay + (int64_t)(c.base + 1) * g.p.H + h;
+  float4 s = *e;
+#pragma unroll 4
+  for (int j = 2; j < c.of; ++j) {
+    e += all;
+    const float d = *by;
+    by += g.p.H;
+    const float4 v = *e;
+    s.x = fmaf(s.x, d, v.x);
+    s.y = fmaf(s.y, d, v.y);
+    s.z = fmaf(s.z, d, v.z);
+    s.w = fmaf(s.w, d, v.w);
+    *e = s;
   }
 }
 
@@ -541,6 +645,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if constexpr (!FULL) let_next_start();
+  launch_before_ended();
   const uint32_t tmem = sm.tmem;
   const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes
 
@@ -1113,19 +1219,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int i = 0; i < HALF; ++i) S[i] = 0.0f;
         total = 1.0f;
         if (FULL && pc.of > 1) {
-          // the entry behind the last piece before this one, from the first on
-          const int e0 = pc.j > 0 ? 1 : 0;
-          for (int e = e0; e <= pc.j; ++e) {
-            const float by = e > e0 ? g.decay[(int64_t)(pc.base + e - 1) * p.H + h] : 0.0f;
-            const float4* from = entry(pc.base + e, h);
+          const float4* from = entry(pc.base + pc.j, h);
 #pragma unroll
-            for (int i = 0; i < HALF / 4; ++i) {
-              const float4 v = from[i * ROWS];
-              S[4 * i] = fmaf(S[4 * i], by, v.x);
-              S[4 * i + 1] = fmaf(S[4 * i + 1], by, v.y);
-              S[4 * i + 2] = fmaf(S[4 * i + 2], by, v.z);
-              S[4 * i + 3] = fmaf(S[4 * i + 3], by, v.w);
-            }
+          for (int i = 0; i < HALF / 4; ++i) {
+            const float4 v = from[i * ROWS];
+            S[4 * i] = v.x;
+            S[4 * i + 1] = v.y;
+            S[4 * i + 2] = v.z;
+            S[4 * i + 3] = v.w;
           }
         } else if (pc.j == 0) {
           const Slot from = load_slot(g.a.src, pc.seq, 0, g.a.idx64);

@@ -19,8 +19,7 @@ cudaError_t launch_chunks(const PromptArgs& g, int ctas, cudaStream_t stream) {
   e = cudaFuncGetAttributes(&fa, kernel);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != 80) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)ctas, kPromptThreads, ask, stream>>>(g);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3((unsigned)ctas), kPromptThreads, ask, stream, g);
 }
 
 template <class IT, int PARTS, bool FULL>
