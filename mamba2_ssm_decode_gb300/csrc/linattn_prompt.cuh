@@ -317,11 +317,11 @@ struct PromptSmem {
   Chunk chunk[kStages];
   // fp16 (two parts) alone
   static constexpr int kScaled = PARTS == 2 ? 128 : 1;
-  float row_max[2][kScaled];    // the largest value of half a row of S
+  float row_max[2][2][kScaled];  // the largest value of half a row of S
   float row_scale[2][kScaled];  // what a row of S was divided by
   float p_scale[2][kScaled];    // ... a token's row of P
   float v_scale[kStages];       // ... w V
-  uint32_t v_max[4];
+  uint32_t v_max[kStages][4];   // the largest of w V, by warp
   int bad[kStages][128];    // the first token of the chunk whose v is not finite
   int any_bad[kStages];
   uint64_t full[kStages], empty[kStages], v_ready[kStages], sc_full[2], sc_free[2];
@@ -1057,28 +1057,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if constexpr (!kBF16) {
         // the largest |w v| of the chunk comes to 2^14
         float m = 0.0f;
-#pragma unroll 1
-        for (int s = lane; s < min(rows, kC); s += 32) {
+#pragma unroll
+        for (int s = lane; s < kC; s += 32) {
           __half2 top{};
-#pragma unroll 2
-          for (int i = w4; i < DV / 8; i += 4) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(v + tile_at(s, i));
+#pragma unroll
+          for (int i = 0; i < DV / 32; ++i) {
+            const uint4 raw = *reinterpret_cast<const uint4*>(v + tile_at(s, 4 * i + w4));
             const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               top = __hmax2(top, __habs2(*reinterpret_cast<const __half2*>(&u[e])));
           }
-          m = fmaxf(m, sm.tab[st].w[s] * fmaxf(__low2float(top), __high2float(top)));
+          if (s < rows) m = fmaxf(m, sm.tab[st].w[s] * fmaxf(__low2float(top), __high2float(top)));
         }
         const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-        if (n > 0 && !warp_wait(sm, g.err, &sm.wv_free[0], (n - 1) & 1)) dead = true;
-        if (lane == 0) sm.v_max[w4] = most;
+        if (lane == 0) sm.v_max[st][w4] = most;
         if (!meet(sm, g.err, &sm.v_warps, met)) dead = true;
-        m = __uint_as_float(max(max(sm.v_max[0], sm.v_max[1]), max(sm.v_max[2], sm.v_max[3])));
+        m = __uint_as_float(max(max(sm.v_max[st][0], sm.v_max[st][1]),
+                                max(sm.v_max[st][2], sm.v_max[st][3])));
         float back;
         by = toward(m, 14, &back);
+        // D of the chunk that had this stage before is read: the products two chunks on are done
+        if (n > 0 && !warp_wait(sm, g.err, &sm.wv_free[0], (n - 1) & 1)) dead = true;
         if (w4 == 0 && lane == 0) sm.v_scale[st] = back;
-        if (!meet(sm, g.err, &sm.v_warps, met)) dead = true;  // v_max is written again
       }
 #pragma unroll 1
       for (int hh = 0; hh < 2; ++hh) {
@@ -1181,13 +1182,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < HALF; ++i) m = fmaxf(m, fabsf(S[i]));
-        if (lane < ROWS) sm.row_max[half][row] = m;
+        if (lane < ROWS) sm.row_max[n & 1][half][row] = m;
         state_warps_meet();
-        m = fmaxf(sm.row_max[0][row], sm.row_max[1][row]);
+        m = fmaxf(sm.row_max[n & 1][0][row], sm.row_max[n & 1][1][row]);
         float back;
         by = toward(m, 10, &back);
         if (half == 0 && lane < ROWS) sm.row_scale[n & 1][row] = back;
-        state_warps_meet();  // row_max is written again in the next chunk
       }
 #pragma unroll
       for (int c = 0; c < HALF; c += 16) operand(c, by);
