@@ -60,33 +60,54 @@ __device__ __forceinline__ int64_t context_of(const Args& a, int s) {
   return c > 0 ? c : 0;
 }
 
+// Its place within its chunk.
+__device__ __forceinline__ int offset_of(const Args& a, int64_t context) {
+  // a 64-bit remainder takes a hundred instructions
+  return (int)(context >> 32 ? context % a.chunk : (uint32_t)context % (uint32_t)a.chunk);
+}
+
 // Starts cu[0 .. n] (cut at `rows`) and chunk ends end[0 .. n) of every
-// sequence, to shared memory; the CTA's threads share the work.
+// sequence, to shared memory; kPer sequences a thread.
+constexpr int kPer = 4;
+
 __device__ __forceinline__ void plan(const Args& a, int* cu, int* end) {
   __shared__ long long warps[kThreads / 32];
   long long rows = 0, chunks = 0;
   if (threadIdx.x == 0) cu[0] = 0;
-  for (int s0 = 0; s0 < a.n; s0 += kThreads) {
-    const int s = s0 + threadIdx.x;
-    long long len = s < a.n ? load_int(a.lens, s, a.is64) : 0;
-    len = len > 0 ? (len < a.rows ? len : a.rows) : 0;  // more than `rows` is cut all the same
-    long long total;
-    const long long inc = rows + block_scan<kThreads>(len, warps, &total);
-    const long long to = inc < a.rows ? inc : a.rows, from = inc - len < a.rows ? inc - len : a.rows;
+  for (int s0 = 0; s0 < a.n; s0 += kPer * kThreads) {
+    const int s = s0 + kPer * threadIdx.x;
+    long long len[kPer], sum = 0, total;
+    int off[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      len[i] = s + i < a.n ? load_int(a.lens, s + i, a.is64) : 0;
+      off[i] = s + i < a.n ? offset_of(a, context_of(a, s + i)) : 0;
+      len[i] = len[i] > 0 ? (len[i] < a.rows ? len[i] : a.rows) : 0;  // more is cut all the same
+      sum += len[i];
+    }
+    long long from = rows + block_scan<kThreads>(sum, warps, &total) - sum;
     rows += total;
     // a sequence's chunks end at multiples of the chunk size of its own positions; it has one
     // at least, which carries its state through
-    long long many = 0;
-    if (s < a.n) {
-      const long long off = context_of(a, s) % a.chunk;
-      many = (off + (to - from) + a.chunk - 1) / a.chunk;
-      if (to == from) many = 1;
+    int many[kPer], all = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = (int)(from < a.rows ? from : a.rows);
+      from += len[i];
+      const int e = (int)(from < a.rows ? from : a.rows);
+      many[i] = e == b ? 1 : (int)(((uint32_t)off[i] + (uint32_t)(e - b) + (uint32_t)a.chunk - 1u) /
+                                   (uint32_t)a.chunk);
+      if (s + i >= a.n) continue;
+      cu[s + i + 1] = e;
+      all += many[i];
     }
-    const long long e = chunks + block_scan<kThreads>(many, warps, &total);
+    long long c = chunks + block_scan<kThreads>((long long)all, warps, &total) - all;
     chunks += total;
-    if (s < a.n) {
-      cu[s + 1] = (int)to;
-      end[s] = (int)e;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (s + i >= a.n) continue;
+      c += many[i];
+      end[s + i] = (int)c;
     }
   }
   __syncthreads();
@@ -94,11 +115,11 @@ __device__ __forceinline__ void plan(const Args& a, int* cu, int* end) {
 
 // The first of n ascending values that is above v (n: none).
 __device__ __forceinline__ int first_above(const int* values, int n, int v) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (values[mid] > v) hi = mid;
-    else lo = mid + 1;
+  int lo = 0;
+  for (int left = n; left > 0;) {  // as many steps whatever v is
+    const int half = left >> 1;
+    if (values[lo + half] <= v) lo += left - half, left = half;
+    else left = half;
   }
   return lo;
 }
@@ -111,17 +132,30 @@ __device__ __forceinline__ void write_chunk(const Args& a, const int* cu, const 
   if (c < chunks) {
     const int nth = c - (s > 0 ? end[s - 1] : 0);
     at = cu[s];
-    if (nth > 0) at += (int64_t)nth * a.chunk - context_of(a, s) % a.chunk;
+    if (nth > 0) at += (int64_t)nth * a.chunk - offset_of(a, context_of(a, s));
   }
   store_int(a.cu_chunk, c, a.is64, at);
   if (c < a.most) store_int(a.seq_idx, c, a.is64, s > 0 ? s : 0);
 }
 
-__device__ __forceinline__ void write_row(const Args& a, const int* cu, int r) {
-  const int s = first_above(cu + 1, a.n, r);
-  const bool inside = s < a.n;
-  if (a.row_seq) store_int(a.row_seq, r, a.is64, inside ? s : -1);
-  if (a.row_pos) store_int(a.row_pos, r, a.is64, inside ? context_of(a, s) + r - cu[s] : -1);
+// Rows r, r + step, ...: kRows of them at a time, whose searches and loads overlap.
+constexpr int kRows = 4;
+
+__device__ __forceinline__ void write_rows(const Args& a, const int* cu, int64_t r, int64_t step) {
+  int s[kRows];
+  int64_t pos[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    s[i] = r + i * step < a.rows ? first_above(cu + 1, a.n, (int)(r + i * step)) : a.n;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    pos[i] = s[i] < a.n ? context_of(a, s[i]) + r + i * step - cu[s[i]] : -1;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (r + i * step >= a.rows) continue;
+    if (a.row_seq) store_int(a.row_seq, r + i * step, a.is64, s[i] < a.n ? s[i] : -1);
+    if (a.row_pos) store_int(a.row_pos, r + i * step, a.is64, pos[i]);
+  }
 }
 
 __device__ __forceinline__ void write_sequence(const Args& a, const int* cu, const int* end, int s) {
@@ -143,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) prompt_maps_kernel(const Args a) {
   for (int s = t; s <= a.n; s += step) write_sequence(a, cu, end, s);
   for (int c = t; c <= a.most; c += step) write_chunk(a, cu, end, c);
   if (a.row_seq || a.row_pos)
-    for (int64_t r = t; r < a.rows; r += step) write_row(a, cu, (int)r);
+    for (int64_t r = t; r < a.rows; r += (int64_t)kRows * step) write_rows(a, cu, r, step);
 }
 
 // ---------------------------------------------------------------------------
@@ -161,6 +195,22 @@ struct AssignArgs {
 };
 
 constexpr int kAssignThreads = 1024;
+constexpr int kEntries = 8;  // of a thread at a time
+
+// Bit k (from 0) of those set in v.
+__device__ __forceinline__ int nth_bit(unsigned long long v, int k) {
+  int at = 0;
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) {
+    const int low = __popcll(v & ((1ull << w) - 1));
+    if (k >= low) {
+      k -= low;
+      at += w;
+      v >>= w;
+    }
+  }
+  return at;
+}
 
 // One CTA: a bitmap of the slots that are kept, the free ones before each of its
 // words, and then, in the table's order, the k-th place without a slot takes the
@@ -177,16 +227,25 @@ __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const Assi
   __syncthreads();
   if (threadIdx.x == 0 && a.pad >= 0 && a.pad < a.slots)
     atomicOr(&held[a.pad >> 6], 1ull << (a.pad & 63));  // never handed out
-  const int64_t entries = (int64_t)a.n * a.steps;
-  auto entry = [&](int64_t e, bool* wanted) {
-    const int s = (int)(e / a.steps);
-    *wanted = e - (int64_t)s * a.steps < load_int(a.counts, s, a.is64);
+  const int entries = a.n * a.steps;  // at most 2^24
+  // the table's entry e; `wanted`: its row is to hold it
+  auto entry = [&](int e, bool* wanted) {
+    const uint32_t s = (uint32_t)e / (uint32_t)a.steps;
+    *wanted = (int64_t)(e - (int)s * a.steps) < load_int(a.counts, s, a.is64);
     return load_int(a.table, e, a.is64);
   };
-  for (int64_t e = threadIdx.x; e < entries; e += kAssignThreads) {
-    bool wanted;
-    const int64_t v = entry(e, &wanted);
-    if (wanted && slot_ok(v, a.pad, a.slots)) atomicOr(&held[v >> 6], 1ull << (v & 63));
+  for (int e0 = threadIdx.x; e0 < entries; e0 += kEntries * kAssignThreads) {
+    int64_t v[kEntries];
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i) {
+      const int e = e0 + i * kAssignThreads;
+      bool wanted = false;
+      v[i] = e < entries ? entry(e, &wanted) : 0;
+      if (!wanted) v[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i)
+      if (slot_ok(v[i], a.pad, a.slots)) atomicOr(&held[v[i] >> 6], 1ull << (v[i] & 63));
   }
   __syncthreads();
   int free = 0;
@@ -199,33 +258,43 @@ __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const Assi
     free += total;
   }
   __syncthreads();
-  int64_t given = 0;
-  for (int64_t e0 = 0; e0 < entries; e0 += kAssignThreads) {
-    const int64_t e = e0 + threadIdx.x;
-    bool wanted = false;
-    const int64_t v = e < entries ? entry(e, &wanted) : 0;
-    const bool kept = wanted && slot_ok(v, a.pad, a.slots);
-    const int need = wanted && !kept;
-    int total;
-    const int64_t rank = given + block_scan<kAssignThreads>(need, warps, &total) - need;
-    given += total;
-    if (e >= entries) continue;
-    int64_t got = a.pad;
-    if (need && rank < free) {
-      int lo = 0, hi = words;  // the last word with no more than `rank` free ones before it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (before[mid] <= rank) lo = mid;
-        else hi = mid;
-      }
-      unsigned long long open = ~held[lo];
-      for (int k = (int)rank - before[lo]; k > 0; --k) open &= open - 1;
-      got = lo * 64 + __ffsll((long long)open) - 1;
+  int given = 0;
+  for (int e0 = 0; e0 < entries; e0 += kEntries * kAssignThreads) {
+    const int first = e0 + kEntries * threadIdx.x;
+    int64_t v[kEntries];
+    uint32_t kept = 0, need = 0;
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i) {
+      bool wanted = false;
+      v[i] = first + i < entries ? entry(first + i, &wanted) : 0;
+      if (!wanted) continue;
+      if (slot_ok(v[i], a.pad, a.slots)) kept |= 1u << i;
+      else need |= 1u << i;
     }
-    store_int(a.out, e, a.is64, kept ? v : got);
-    store_int(a.fresh, e, a.is64, got);
+    int total;
+    int rank = given + block_scan<kAssignThreads>(__popc(need), warps, &total) - __popc(need);
+    given += total;
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i) {
+      if (first + i >= entries) continue;
+      int64_t got = a.pad;
+      if (need >> i & 1) {
+        if (rank < free) {
+          int lo = 0, hi = words;  // the last word with no more than `rank` free ones before it
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= rank) lo = mid;
+            else hi = mid;
+          }
+          got = lo * 64 + nth_bit(~held[lo], rank - before[lo]);
+        }
+        ++rank;
+      }
+      store_int(a.out, first + i, a.is64, kept >> i & 1 ? v[i] : got);
+      store_int(a.fresh, first + i, a.is64, got);
+    }
   }
-  if (threadIdx.x == 0) *a.missing = (int)(given > free ? given - free : 0);
+  if (threadIdx.x == 0) *a.missing = given > free ? given - free : 0;
 }
 
 static ssu_status prompt_maps(const ssu_prompt_maps_params* c, cudaStream_t stream) {

@@ -35,11 +35,13 @@ struct Args {
   int64_t o_ss;
   void* count;
   int count64;
-  int p_vec, q_vec;  // every row of p (q) starts on a boundary of four elements
 };
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kVec = 4;
+constexpr int kEach = 16;           // elements a lane has under way at once
+constexpr int kStep = 32 * kEach;   // ... a warp
+
+constexpr int kRows = 4;            // rows of a greedy sequence that are looked at together
 
 // (value, index) of the largest value; the lowest index of equal ones; NaN never
 struct Best {
@@ -48,49 +50,94 @@ struct Best {
   __device__ __forceinline__ void take(float w, int j) {
     if (w > v || (w == v && j < i)) v = w, i = j;
   }
+  // a number that is larger for what is better, above 0; 0 where nothing was taken
+  __device__ __forceinline__ unsigned long long key() const {
+    if (i == 0x7fffffff) return 0;
+    const uint32_t b = __float_as_uint(v + 0.0f);  // one zero
+    return (unsigned long long)(b >> 31 ? ~b : b | 0x80000000u) << 32 | (0x7fffffffu - (uint32_t)i);
+  }
 };
 
 struct Shared {
   unsigned long long sum[kWarps];  // weights of each warp's share
-  Best best[kWarps];
+  unsigned long long best[kRows][kWarps];  // ... best of each row, as Best::key
   // of the CTA, read by the others of its cluster
   unsigned long long total;
-  Best top[2];
+  unsigned long long top[2][kRows];
 };
 
-// What is left of four consecutive probabilities.
-template <class T>
+// What is left of kStep consecutive probabilities, kEach a lane.  VEC: every row
+// starts on a boundary of four elements, and a lane takes them four at a time; else
+// one at a time, which leaves a warp's accesses as long: rows of an odd vocabulary
+// start anywhere.
+template <class T, bool VEC>
 struct Row {
+  static constexpr int E = VEC ? 4 : 1, U = kEach / E;
   const T* p;
   const T* q;  // nullptr: nothing is taken off, but for token `drop`
   int drop;
-  bool p_vec, q_vec;
 
-  __device__ __forceinline__ void load(int i, int end, float* r) const {
-    if (i + kVec <= end) {
-      load_floats<T, kVec>(p + i, p_vec, r);
-      if (q) {
-        float s[kVec];
-        load_floats<T, kVec>(q + i, q_vec, s);
+  // element e of part u of the kStep from `base` on
+  static __device__ __forceinline__ int place(int base, int u, int e) {
+    return base + (u * 32 + (threadIdx.x & 31)) * E + e;
+  }
+  static __device__ __forceinline__ void read(const T* row, int base, int end, float none,
+                                              float (&r)[kEach]) {
+    if (base + kStep <= end) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) r[e] -= s[e];
-      }
+      for (int u = 0; u < U; ++u) load_floats<T, E>(row + place(base, u, 0), true, r + u * E);
     } else {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        r[e] = i + e < end ? to_f(p[i + e]) : 0.0f;
-        if (q && i + e < end) r[e] -= to_f(q[i + e]);
-      }
-    }
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      if (i + e == drop) r[e] = 0.0f;
+        for (int e = 0; e < E; ++e) {
+          const int i = place(base, u, e);
+          r[u * E + e] = i < end ? to_f(row[i]) : none;
+        }
+    }
+  }
+  // zeros from `end` on
+  __device__ __forceinline__ void load(int base, int end, float (&r)[kEach]) const {
+    read(p, base, end, 0.0f, r);
+    if (q) {
+      float s[kEach];
+      read(q, base, end, 0.0f, s);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) r[i] -= s[i];
+    }
+    if (drop >= base && drop < base + kStep) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (place(base, i / E, i % E) == drop) r[i] = 0.0f;
+    }
   }
 };
 
-// in units of 2^-44; NaN and what is below zero weigh nothing
+// Weights in units of 2^-44; NaN and what is below zero weigh nothing.  A weight is
+// h 2^22 + l, h the nearest integer of r 2^22 and l the one of what that leaves times
+// 2^22: sums of fp32 numbers and a power of two, whose low bits are the integers.
+// Conversions to 64-bit integers took 26 of 92 us (256 sequences, 128257 tokens).
+struct Weights {
+  uint32_t h = 0, l = 0;
+  int n = 0;
+  __device__ __forceinline__ void add(float r) {  // at most 2^9 times
+    const float t = fminf(fmaxf(r, 0.0f), 1.0f) * 0x1p22f;
+    const float a = t + 0x1p23f;
+    const float b = fmaf(t - (a - 0x1p23f), 0x1p22f, 0x1.8p23f);
+    h += __float_as_uint(a);
+    l += __float_as_uint(b);
+    ++n;
+  }
+  __device__ __forceinline__ unsigned long long sum() const {
+    return ((unsigned long long)(h - (uint32_t)n * 0x4b000000u) << 22) +
+           (long long)(int32_t)(l - (uint32_t)n * 0x4b400000u);
+  }
+};
+
 __device__ __forceinline__ unsigned long long weight(float r) {
-  return (unsigned long long)__float2ll_rn(fminf(fmaxf(r, 0.0f), 1.0f) * 0x1p44f);
+  Weights w;
+  w.add(r);
+  return w.sum();
 }
 
 template <class T>
@@ -107,8 +154,8 @@ __device__ __forceinline__ void store_int(void* p, int64_t i, int is64, int64_t 
 
 // A cluster per sequence; its CTAs, and their warps, have consecutive shares of
 // the vocabulary.
-template <class T>
-__global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
+template <class T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) drafts_verify_kernel(const Args a) {
   __shared__ Shared sm;
   cg::cluster_group cluster = cg::this_cluster();
   const int s = blockIdx.y, rank = cluster.block_rank(), ctas = cluster.num_blocks();
@@ -123,42 +170,59 @@ __global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
   if (n >= 0) {
     const bool greedy = a.greedy && a.greedy[s];
     // the warp's share [i0, i1) of the vocabulary
-    const int share = ((a.V + ctas * kWarps - 1) / (ctas * kWarps) + kVec - 1) / kVec * kVec;
+    const int share = ((a.V + ctas * kWarps - 1) / (ctas * kWarps) + kStep - 1) / kStep * kStep;
     const int64_t at = (int64_t)share * (rank * kWarps + warp);
     const int i0 = (int)min(at, (int64_t)a.V), i1 = (int)min(at + share, (int64_t)a.V);
     auto row_of = [&](int j) { return static_cast<const T*>(a.p) + (int64_t)(r0 + j) * a.p_rs; };
     auto draft = [&](int j) { return load_int(a.drafts, s * a.d_ss + j, a.tok64); };
 
     if (greedy) {
-      for (int j = 0;; ++j) {
-        const T* row = row_of(j);
-        Best b{-INFINITY, 0x7fffffff};
-        for (int i = i0 + lane * kVec; i < i1; i += 32 * kVec) {
-          float r[kVec];
-          if (i + kVec <= i1) load_floats<T, kVec>(row + i, a.p_vec, r);
-          else
-            for (int e = 0; e < kVec; ++e) r[e] = i + e < i1 ? to_f(row[i + e]) : NAN;
+      // Blocks of kStep of the next kRows rows, dealt to all of the cluster's warps: row
+      // after row would wait for a meeting of the CTAs each time.
+      const int blocks = (a.V + kStep - 1) / kStep;
+      for (int j0 = 0, odd = 0;; j0 += kRows, odd ^= 1) {
+        const int rows = min(kRows, n + 1 - j0);
+        int id = rank * kWarps + warp;
+        for (int j = 0; j < rows; ++j) {
+          using R = Row<T, VEC>;
+          Best b{-INFINITY, 0x7fffffff};
+          const T* row = row_of(j0 + j);
+          for (; id < (j + 1) * blocks; id += ctas * kWarps) {
+            float r[kEach];
+            const int base = (id - j * blocks) * kStep;
+            R::read(row, base, a.V, NAN, r);
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) b.take(r[e], i + e);
+            for (int i = 0; i < kEach; ++i) b.take(r[i], R::place(base, i / R::E, i % R::E));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            b.take(__shfl_xor_sync(0xffffffffu, b.v, o), __shfl_xor_sync(0xffffffffu, b.i, o));
+          if (lane == 0) sm.best[j][warp] = b.key();
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          b.take(__shfl_xor_sync(0xffffffffu, b.v, o), __shfl_xor_sync(0xffffffffu, b.i, o));
-        if (lane == 0) sm.best[warp] = b;
         __syncthreads();
-        if (threadIdx.x == 0) {
-          for (int w = 1; w < kWarps; ++w) b.take(sm.best[w].v, sm.best[w].i);
-          sm.top[j & 1] = b;
+        static_assert(kRows <= kWarps && kWarps <= 32, "a warp a row");
+        if (warp < rows) {
+          unsigned long long b = lane < kWarps ? sm.best[warp][lane] : 0;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const unsigned long long v = __shfl_xor_sync(0xffffffffu, b, o);
+            b = v > b ? v : b;
+          }
+          if (lane == 0) sm.top[odd][warp] = b;
         }
         cluster.sync();
-        Best top{-INFINITY, 0x7fffffff};
-        for (int c = 0; c < ctas; ++c) {
-          const Best o = *cluster.map_shared_rank(&sm.top[j & 1], c);
-          top.take(o.v, o.i);
+        bool more = true;
+        for (int j = 0; j < rows && more; ++j) {
+          unsigned long long best = 0;
+          for (int c = 0; c < ctas; ++c) {
+            const unsigned long long b = *cluster.map_shared_rank(&sm.top[odd][j], c);
+            best = b > best ? b : best;
+          }
+          token = best ? (int64_t)(0x7fffffffu - (uint32_t)best) : -1;
+          more = j0 + j < n && token >= 0 && draft(j0 + j) == token;
+          count += more;
         }
-        token = top.i < a.V ? top.i : -1;
-        if (j == n || token < 0 || draft(j) != token) break;
-        ++count;
+        if (!more) break;
       }
     } else {
       // the first draft that is turned down, by every warp for itself
@@ -179,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
         if (no) break;
       }
       count = min(count, n);
-      Row<T> row{row_of(count), nullptr, -1, a.p_vec != 0, a.q_vec != 0};
+      Row<T, VEC> row{row_of(count), nullptr, -1};
       if (count < n) {
         if (a.q) row.q = static_cast<const T*>(a.q) + s * a.q_ss + count * a.q_ts;
         else {
@@ -191,11 +255,13 @@ __global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
       // a second time, from the whole row, where nothing is left of it
       for (int pass = 0; pass < 2; ++pass) {
         unsigned long long sum = 0;
-        for (int i = i0 + lane * kVec; i < i1; i += 32 * kVec) {
-          float r[kVec];
-          row.load(i, i1, r);
+        for (int base = i0; base < i1; base += kStep) {
+          float r[kEach];
+          row.load(base, i1, r);
+          Weights w;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) sum += weight(r[e]);
+          for (int i = 0; i < kEach; ++i) w.add(r[i]);
+          sum += w.sum();
         }
         sum = warp_sum(sum);
         if (lane == 0) sm.sum[warp] = sum;
@@ -220,33 +286,43 @@ __global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
           // the warp whose share holds it finds the token
           if (mark >= before && mark - before < sum) {
             unsigned long long run = before;
-            for (int base = i0; base < i1; base += 32 * kVec) {
-              const int i = base + lane * kVec;
-              float r[kVec];
-              unsigned long long w[kVec], mine = 0;
-              if (i < i1) row.load(i, i1, r);
+            for (int base = i0; base < i1; base += kStep) {
+              constexpr int E = Row<T, VEC>::E;
+              float r[kEach];
+              row.load(base, i1, r);
+              Weights w;
 #pragma unroll
-              for (int e = 0; e < kVec; ++e) {
-                w[e] = i < i1 ? weight(r[e]) : 0;
-                mine += w[e];
+              for (int i = 0; i < kEach; ++i) w.add(r[i]);
+              unsigned long long mine = w.sum();
+              const unsigned long long here = warp_sum(mine);
+              if (mark >= run + here) {
+                run += here;
+                continue;
               }
-              unsigned long long inc = mine;
 #pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const unsigned long long v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-              }
-              const unsigned long long all = __shfl_sync(0xffffffffu, inc, 31);
-              if (mark < run + all) {
+              for (int u = 0; u < kEach / E; ++u) {
+                mine = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) mine += weight(r[u * E + e]);
+                unsigned long long inc = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                  const unsigned long long v = __shfl_up_sync(0xffffffffu, inc, o);
+                  if (lane >= o) inc += v;
+                }
                 unsigned long long c = run + inc - mine;
                 if (mark >= c && mark < c + mine) {
-                  int e = 0;
-                  while (mark >= c + w[e]) c += w[e++];
-                  store_int(a.out, s * a.o_ss + count, a.tok64, i + e);
+#pragma unroll
+                  for (int e = 0; e < E; ++e) {
+                    const unsigned long long w = weight(r[u * E + e]);
+                    if (mark >= c && mark < c + w)
+                      store_int(a.out, s * a.o_ss + count, a.tok64, row.place(base, u, e));
+                    c += w;
+                  }
                 }
-                break;
+                run += __shfl_sync(0xffffffffu, inc, 31);
               }
-              run += all;
+              break;
             }
           }
           token = -2;  // another thread writes it
@@ -273,10 +349,14 @@ __global__ void __launch_bounds__(kThreads) drafts_verify_kernel(const Args a) {
   cluster.sync();  // no CTA leaves while another may read its shared memory
 }
 
-template <class T>
+template <class T, bool VEC>
 static cudaError_t launch(const Args& a, cudaStream_t stream) {
+  // More CTAs while a warp has more than one step, up to four CTAs an SM in all: for one
+  // sequence of 50288 tokens 1, 2, 4 and 8 take 25, 12, 9.6 and 8.2 us, for 256 of 128257
+  // 2, 4 and 8 take 65, 66 and 87 us.
   int ctas = 1;
-  while (ctas < 8 && a.V > ctas * 16384) ctas *= 2;
+  while (ctas < 8 && a.V > ctas * kWarps * kStep && (int64_t)a.n * ctas < 4LL * ssu::sm_count())
+    ctas *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)a.n);
   cfg.blockDim = dim3(kThreads);
@@ -287,7 +367,7 @@ static cudaError_t launch(const Args& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, drafts_verify_kernel<T>, a);
+  return cudaLaunchKernelEx(&cfg, drafts_verify_kernel<T, VEC>, a);
 }
 
 static ssu_status verify(const ssu_drafts_params* c, cudaStream_t stream) {
@@ -350,13 +430,17 @@ static ssu_status verify(const ssu_drafts_params* c, cudaStream_t stream) {
   a.o_ss = c->out_seq_stride;
   a.count = c->num_accepted;
   a.count64 = c->count_dtype == SSU_I64;
-  a.p_vec = aligned(c->target_probs, kVec * es) && c->target_row_stride % kVec == 0;
-  a.q_vec = c->draft_probs && aligned(c->draft_probs, kVec * es) &&
-            c->draft_seq_stride % kVec == 0 && c->draft_step_stride % kVec == 0;
+  auto fours = [&](const void* p, int64_t stride, int64_t more) {
+    return aligned(p, 4 * es) && stride % 4 == 0 && more % 4 == 0;
+  };
+  const bool vec = fours(c->target_probs, c->target_row_stride, 0) &&
+                   (!c->draft_probs ||
+                    fours(c->draft_probs, c->draft_seq_stride, c->draft_step_stride));
   switch (c->probs_dtype) {
-    case SSU_F32: return launched(launch<float>(a, stream));
-    case SSU_BF16: return launched(launch<__nv_bfloat16>(a, stream));
-    default: return launched(launch<__half>(a, stream));
+    case SSU_F32: return launched((vec ? launch<float, true> : launch<float, false>)(a, stream));
+    case SSU_BF16:
+      return launched((vec ? launch<__nv_bfloat16, true> : launch<__nv_bfloat16, false>)(a, stream));
+    default: return launched((vec ? launch<__half, true> : launch<__half, false>)(a, stream));
   }
 }
 

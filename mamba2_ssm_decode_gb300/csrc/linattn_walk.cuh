@@ -22,7 +22,8 @@ struct WalkLayout {
 
 constexpr int kWalkWarps = 4;
 
-template <class ST, class IT, int DK>
+// ONE: a row a sequence, which is that of its number.
+template <class ST, class IT, int DK, bool ONE>
 __global__ void __launch_bounds__(kWalkWarps * 32)
     linattn_walk_kernel(const Args p, const Seqs a, int tiles) {
   using L = WalkLayout<ST, DK>;
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
   const int h = blockIdx.y / tiles, g = h / p.hr;
   const int p0 = (blockIdx.y - h * tiles) * kWalkWarps * L::ROWS + warp * L::ROWS + lane / LPR;
 
-  const Item it = packed_item(a, s, p.pad, p.slots);
+  const Item it = packed_item<ONE>(a, s, p.pad, p.slots);
   if (it.len == 0) return;
   const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
 
@@ -121,8 +122,11 @@ cudaError_t launch_walk_dk(const Args& p, const Seqs& a, cudaStream_t stream) {
   constexpr int per = kWalkWarps * WalkLayout<ST, DK>::ROWS;
   const int tiles = (p.dv + per - 1) / per;
   // sequences along x, which has room for them all; heads and row tiles along y
-  linattn_walk_kernel<ST, IT, DK>
-      <<<dim3((unsigned)a.n, (unsigned)(p.H * tiles)), kWalkWarps * 32, 0, stream>>>(p, a, tiles);
+  const dim3 grid((unsigned)a.n, (unsigned)(p.H * tiles));
+  if (!a.cu && !a.na && a.steps == 1 && !p.prompt)
+    linattn_walk_kernel<ST, IT, DK, true><<<grid, kWalkWarps * 32, 0, stream>>>(p, a, tiles);
+  else
+    linattn_walk_kernel<ST, IT, DK, false><<<grid, kWalkWarps * 32, 0, stream>>>(p, a, tiles);
   return cudaGetLastError();
 }
 
