@@ -68,8 +68,7 @@ __device__ __forceinline__ int offset_of(const Args& a, int64_t context) {
 
 // Starts cu[0 .. n] (cut at `rows`) and chunk ends end[0 .. n) of every
 // sequence, to shared memory; kPer sequences a thread.
-constexpr int kPer = 4;
-
+template <int kPer>
 __device__ __forceinline__ void plan(const Args& a, int* cu, int* end) {
   __shared__ long long warps[kThreads / 32];
   long long rows = 0, chunks = 0;
@@ -138,9 +137,8 @@ __device__ __forceinline__ void write_chunk(const Args& a, const int* cu, const 
   if (c < a.most) store_int(a.seq_idx, c, a.is64, s > 0 ? s : 0);
 }
 
-// Rows r, r + step, ...: kRows of them at a time, whose searches and loads overlap.
-constexpr int kRows = 4;
-
+// Rows r, r + step, ...: kRows of them, whose searches and loads overlap.
+template <int kRows>
 __device__ __forceinline__ void write_rows(const Args& a, const int* cu, int64_t r, int64_t step) {
   int s[kRows];
   int64_t pos[kRows];
@@ -167,17 +165,20 @@ __device__ __forceinline__ void write_sequence(const Args& a, const int* cu, con
   a.has_init[s] = context_of(a, s) > 0;
 }
 
-// Every CTA plans for itself and writes its share.
+// Every CTA plans for itself and writes its share.  MANY: more than a sequence (S) or
+// a row (R) a thread; one at a time is 2 us faster where there are few.
+template <bool MANY_S, bool MANY_R>
 __global__ void __launch_bounds__(kThreads) prompt_maps_kernel(const Args a) {
+  constexpr int kRows = MANY_R ? 4 : 1;
   extern __shared__ int plan_smem[];
   int* cu = plan_smem;
   int* end = plan_smem + a.n + 1;
-  plan(a, cu, end);
+  plan<MANY_S ? 4 : 1>(a, cu, end);
   const int t = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
   for (int s = t; s <= a.n; s += step) write_sequence(a, cu, end, s);
   for (int c = t; c <= a.most; c += step) write_chunk(a, cu, end, c);
   if (a.row_seq || a.row_pos)
-    for (int64_t r = t; r < a.rows; r += (int64_t)kRows * step) write_rows(a, cu, r, step);
+    for (int64_t r = t; r < a.rows; r += (int64_t)kRows * step) write_rows<kRows>(a, cu, r, step);
 }
 
 // ---------------------------------------------------------------------------
@@ -195,8 +196,6 @@ struct AssignArgs {
 };
 
 constexpr int kAssignThreads = 1024;
-constexpr int kEntries = 8;  // of a thread at a time
-
 // Bit k (from 0) of those set in v.
 __device__ __forceinline__ int nth_bit(unsigned long long v, int k) {
   int at = 0;
@@ -214,7 +213,8 @@ __device__ __forceinline__ int nth_bit(unsigned long long v, int k) {
 
 // One CTA: a bitmap of the slots that are kept, the free ones before each of its
 // words, and then, in the table's order, the k-th place without a slot takes the
-// k-th free one.
+// k-th free one.  kEntries of the table a thread at a time.
+template <int kEntries>
 __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const AssignArgs a) {
   extern __shared__ unsigned long long held[];
   __shared__ int warps[kAssignThreads / 32];
@@ -258,40 +258,50 @@ __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const Assi
     free += total;
   }
   __syncthreads();
+  // a warp has kEntries times 32 consecutive entries, 32 at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int given = 0;
   for (int e0 = 0; e0 < entries; e0 += kEntries * kAssignThreads) {
-    const int first = e0 + kEntries * threadIdx.x;
+    const int first = e0 + warp * kEntries * 32 + lane;
     int64_t v[kEntries];
-    uint32_t kept = 0, need = 0;
+    unsigned need[kEntries], kept = 0;
+    int mine = 0;  // of the warp
 #pragma unroll
     for (int i = 0; i < kEntries; ++i) {
+      const int e = first + i * 32;
       bool wanted = false;
-      v[i] = first + i < entries ? entry(first + i, &wanted) : 0;
-      if (!wanted) continue;
-      if (slot_ok(v[i], a.pad, a.slots)) kept |= 1u << i;
-      else need |= 1u << i;
+      v[i] = e < entries ? entry(e, &wanted) : 0;
+      const bool keeps = wanted && slot_ok(v[i], a.pad, a.slots);
+      kept |= (unsigned)keeps << i;
+      need[i] = __ballot_sync(0xffffffffu, wanted && !keeps);
+      mine += __popc(need[i]);
     }
-    int total;
-    int rank = given + block_scan<kAssignThreads>(__popc(need), warps, &total) - __popc(need);
+    __syncthreads();  // `warps` may still be read
+    if (lane == 0) warps[warp] = mine;
+    __syncthreads();
+    static_assert(kAssignThreads / 32 == 32, "a lane a warp");
+    const int theirs = warps[lane];
+    const int total = __reduce_add_sync(0xffffffffu, theirs);
+    int rank = given + __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0);
     given += total;
 #pragma unroll
     for (int i = 0; i < kEntries; ++i) {
-      if (first + i >= entries) continue;
+      const int e = first + i * 32;
+      const int k = rank + __popc(need[i] & ((1u << lane) - 1));
+      rank += __popc(need[i]);
+      if (e >= entries) continue;
       int64_t got = a.pad;
-      if (need >> i & 1) {
-        if (rank < free) {
-          int lo = 0, hi = words;  // the last word with no more than `rank` free ones before it
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (before[mid] <= rank) lo = mid;
-            else hi = mid;
-          }
-          got = lo * 64 + nth_bit(~held[lo], rank - before[lo]);
+      if ((need[i] >> lane & 1) && k < free) {
+        int lo = 0, hi = words;  // the last word with no more than k free ones before it
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (before[mid] <= k) lo = mid;
+          else hi = mid;
         }
-        ++rank;
+        got = lo * 64 + nth_bit(~held[lo], k - before[lo]);
       }
-      store_int(a.out, first + i, a.is64, kept >> i & 1 ? v[i] : got);
-      store_int(a.fresh, first + i, a.is64, got);
+      store_int(a.out, e, a.is64, kept >> i & 1 ? v[i] : got);
+      store_int(a.fresh, e, a.is64, got);
     }
   }
   if (threadIdx.x == 0) *a.missing = given > free ? given - free : 0;
@@ -360,16 +370,20 @@ static ssu_status prompt_maps(const ssu_prompt_maps_params* c, cudaStream_t stre
   a.row_seq = c->row_seq;
   a.row_pos = c->row_pos;
   const int smem = (2 * a.n + 1) * (int)sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        prompt_maps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return launched(e);
-  }
   const int64_t rows = a.row_seq || a.row_pos ? a.rows : 0;
   const int64_t items = rows > a.most ? rows : a.most;
   const int64_t fit = ssu::sm_count();
-  const int64_t ctas = items / (4 * kThreads) + 1;
-  prompt_maps_kernel<<<(unsigned)(ctas < fit ? ctas : fit), kThreads, smem, stream>>>(a);
+  int64_t ctas = items / kThreads + 1;
+  const bool many_s = a.n > kThreads, many_r = ctas > fit;
+  if (many_r) ctas = fit;
+  auto kernel = many_s ? (many_r ? prompt_maps_kernel<true, true> : prompt_maps_kernel<true, false>)
+                       : (many_r ? prompt_maps_kernel<false, true> : prompt_maps_kernel<false, false>);
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return launched(e);
+  }
+  kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(a);
   return launched(cudaGetLastError());
 }
 
@@ -403,12 +417,13 @@ static ssu_status assign(const void* table, const void* counts, ssu_dtype index_
   AssignArgs a{table, counts, out, fresh, missing, index_dtype == SSU_I64, (int)nseqs, (int)steps,
                (int)slots, pad};
   const int smem = (a.slots + 63) / 64 * 12;
+  auto kernel = entries <= kAssignThreads ? slots_assign_kernel<1> : slots_assign_kernel<8>;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        slots_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return launched(e);
   }
-  slots_assign_kernel<<<1, kAssignThreads, smem, stream>>>(a);
+  kernel<<<1, kAssignThreads, smem, stream>>>(a);
   return launched(cudaGetLastError());
 }
 
