@@ -312,7 +312,6 @@ struct PromptSmem {
   unsigned char wv[PARTS][Z::kV];
   unsigned char p[2][Z::kP];
   unsigned char out[Z::kOut ? Z::kOut : 16];
-  unsigned char turn[8][DV / 4 * 48];  // rows of S on their way from and to global memory
   Tables tab[kStages];
   Chunk chunk[kStages];
   // fp16 (two parts) alone
@@ -528,65 +527,66 @@ __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Eight values of this thread's row of a state in global memory, columns [c, c +
-// 8): loaded (or stored) by the warp in whole rows, 16 bytes a lane, and turned
-// through `buf`, ROWS rows of 48 bytes.  Row = lane % ROWS.  ST is the state's type.
-template <class ST, int DK, int ROWS>
-__device__ __forceinline__ void load_rows8(const ST* tile, int c, unsigned char* buf, float* v) {
-  constexpr int PER = 8 * (int)sizeof(ST) / 16;  // lanes of a row
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < (ROWS * PER + 31) / 32; ++i) {
-    const int row = (i * 32 + lane) / PER, piece = lane % PER;
-    if (row < ROWS)
-      *reinterpret_cast<uint4*>(buf + row * 48 + piece * 16) =
-          *reinterpret_cast<const uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST)));
+// 32 bytes of global memory, in one access where `wide` says that they start on such
+// a boundary: a whole sector a lane.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&r)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+    r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
   }
-  __syncwarp();
-  const unsigned char* mine = buf + (lane % ROWS) * 48;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const uint4 w = *reinterpret_cast<const uint4*>(mine + i * 16);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (sizeof(ST) == 4) v[i * 4 + k] = __uint_as_float(u[k]);
-      else {
-        const float2 f = unpack2<ST>(u[k]);
-        v[2 * k] = f.x;
-        v[2 * k + 1] = f.y;
-      }
-    }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&r)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
   }
-  __syncwarp();
 }
 
-template <class ST, int DK, int ROWS>
-__device__ __forceinline__ void store_rows8(ST* tile, int c, unsigned char* buf, const float* v) {
-  constexpr int PER = 8 * (int)sizeof(ST) / 16;
-  const int lane = threadIdx.x & 31;
-  if (lane < ROWS) {
-    unsigned char* mine = buf + lane * 48;
+// N values of this thread's row of a state; ST is the state's type.
+template <class ST, int N>
+__device__ __forceinline__ void load_row(const ST* row, bool wide, float* v) {
+  constexpr int E = 32 / (int)sizeof(ST);
+  uint32_t r[N / E][8];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      uint32_t u[4];
+  for (int i = 0; i < N / E; ++i) load32(row + i * E, wide, r[i]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(ST) == 4) u[k] = __float_as_uint(v[i * 4 + k]);
-        else u[k] = pack2<ST>(v[2 * k], v[2 * k + 1]);
+  for (int i = 0; i < N / E; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (sizeof(ST) == 4) {
+        v[i * E + k] = __uint_as_float(r[i][k]);
+      } else {
+        const float2 f = unpack2<ST>(r[i][k]);
+        v[i * E + 2 * k] = f.x;
+        v[i * E + 2 * k + 1] = f.y;
       }
-      *reinterpret_cast<uint4*>(mine + i * 16) = make_uint4(u[0], u[1], u[2], u[3]);
     }
-  }
-  __syncwarp();
+}
+
+template <class ST, int N>
+__device__ __forceinline__ void store_row(ST* row, bool wide, const float* v) {
+  constexpr int E = 32 / (int)sizeof(ST);
 #pragma unroll
-  for (int i = 0; i < (ROWS * PER + 31) / 32; ++i) {
-    const int row = (i * 32 + lane) / PER, piece = lane % PER;
-    if (row < ROWS)
-      *reinterpret_cast<uint4*>(tile + (int64_t)row * DK + c + piece * (16 / sizeof(ST))) =
-          *reinterpret_cast<const uint4*>(buf + row * 48 + piece * 16);
+  for (int i = 0; i < N / E; ++i) {
+    uint32_t r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (sizeof(ST) == 4) r[k] = __float_as_uint(v[i * E + k]);
+      else r[k] = pack2<ST>(v[i * E + 2 * k], v[i * E + 2 * k + 1]);
+    }
+    store32(row + i * E, wide, r);
   }
-  __syncwarp();
 }
 
 // FULL: the outputs and final states.  Else: what the pieces add to the state.
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float a0 = tab.a[t0], a1 = tab.a[t1];
         const bool mild = tab.mild;
         if (!warp_wait(sm, g.err, &sm.sc_full[n & 1], (n >> 1) & 1)) break;
-        if (n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
+        if (kBF16 && n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
         tc::fence_after_sync();
         // 16 columns: scale e^(a_t - a_s) q_t . k_s, 0 above the diagonal
         auto weighed = [&](int b, float2 (&y)[4]) {
@@ -923,6 +923,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           float back0, back1;
           const float by0 = toward(m0, 10, &back0), by1 = toward(m1, 10, &back1);
+          if (n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
           if ((lane & 3) == 0) {
             sm.p_scale[n & 1][t0] = back0;
             sm.p_scale[n & 1][t1] = back1;
@@ -1147,13 +1148,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // ---- S ---------------------------------------------------------------
     const int half = wg - 2, st_tid = tid - 256;  // 0 .. 255
     const int row = ROWS * (warp & 3) + lane % ROWS;
-    unsigned char* buf = sm.turn[warp - 8];
     float S[HALF];
     float total = 1.0f;
     uint32_t met = 0;
     bool dead = false;
-    auto state_warps_meet = [&] {
-      if (!meet(sm, g.err, &sm.state_warps, met)) dead = true;
+    // fp16: the largest value of this thread's half of a row, left for the other half's
+    // threads; the warps meet when it is looked at
+    auto measure = [&](int n) {
+      float m[4] = {};
+#pragma unroll
+      for (int i = 0; i < HALF; i += 4)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], fabsf(S[i + k]));
+      if (lane < ROWS) sm.row_max[n & 1][half][row] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.state_warps);
     };
     // S as a chunk's operand: columns [c, c + 16), divided by a power of two
     auto operand = [&](int c, float by) {
@@ -1179,12 +1188,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       float by = 1.0f;
       if constexpr (!kBF16) {
         // fp16 has no room for a large S: each row is brought to about 2^10 by a power of two
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < HALF; ++i) m = fmaxf(m, fabsf(S[i]));
-        if (lane < ROWS) sm.row_max[n & 1][half][row] = m;
-        state_warps_meet();
-        m = fmaxf(sm.row_max[n & 1][0][row], sm.row_max[n & 1][1][row]);
+        if (!warp_wait(sm, g.err, &sm.state_warps, met)) dead = true;
+        met ^= 1;
+        const float m = fmaxf(sm.row_max[n & 1][0][row], sm.row_max[n & 1][1][row]);
         float back;
         by = toward(m, 10, &back);
         if (half == 0 && lane < ROWS) sm.row_scale[n & 1][row] = back;
@@ -1193,9 +1199,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int c = 0; c < HALF; c += 16) operand(c, by);
       given();
     };
-    auto rows_of_state = [&](auto* pool, int64_t slot, int h) {
-      return pool + ((slot * p.H + h) * DV + ROWS * (warp & 3)) * DK + half * HALF;
+    auto row_of_state = [&](auto* pool, int64_t slot, int h) {
+      return pool + ((slot * p.H + h) * DV + row) * DK + half * HALF;
     };
+    const bool wide = ((uintptr_t)p.state & 31) == 0;
     auto entry = [&](int e, int h) {  // of the workspace's states; this thread's first four values
       return reinterpret_cast<float4*>(g.state) + ((int64_t)e * p.H + h) * (DV * DK / 4) +
              (half * 4 + (warp & 3)) * (HALF / 4 * ROWS) + lane % ROWS;
@@ -1233,16 +1240,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int64_t slot = from.id(pc.seq, g.a.idx64);
           if (from.found && slot_ok(slot, p.pad, p.slots) && (!p.has_init || p.has_init[pc.seq])) {
 #pragma unroll
-            for (int c = 0; c < HALF; c += 8) {
+            for (int c = 0; c < HALF; c += 32) {
               if (p.state_dtype == SSU_F32)
-                load_rows8<float, DK, ROWS>(rows_of_state(static_cast<const float*>(p.state), slot, h),
-                                             c, buf, S + c);
+                load_row<float, 32>(row_of_state(static_cast<const float*>(p.state), slot, h) + c,
+                                    wide, S + c);
               else if (p.state_dtype == SSU_BF16)
-                load_rows8<__nv_bfloat16, DK, ROWS>(
-                    rows_of_state(static_cast<const __nv_bfloat16*>(p.state), slot, h), c, buf, S + c);
+                load_row<__nv_bfloat16, 32>(
+                    row_of_state(static_cast<const __nv_bfloat16*>(p.state), slot, h) + c, wide, S + c);
               else
-                load_rows8<__half, DK, ROWS>(
-                    rows_of_state(static_cast<const __half*>(p.state), slot, h), c, buf, S + c);
+                load_row<__half, 32>(row_of_state(static_cast<const __half*>(p.state), slot, h) + c,
+                                     wide, S + c);
             }
           }
           if (!FULL && lane < ROWS) {  // the second launch finds it here, whatever is in the slot then
@@ -1252,6 +1259,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               to[i * ROWS] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
           }
         }
+        if constexpr (FULL && !kBF16) measure(n);
       }
       if constexpr (FULL) {
         // o2 of the chunk before has read its S
@@ -1285,7 +1293,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.d_free);
-      if (!last) continue;
+      if (!last) {
+        if constexpr (FULL && !kBF16) measure(n + 1);
+        continue;
+      }
       if constexpr (!FULL) {
         if (lane < ROWS) {
           float4* to = entry(pc.base + pc.j + 1, h);
@@ -1298,20 +1309,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const Slot from = load_slot(g.a.src, pc.seq, 0, g.a.idx64);
         int64_t to;
         if (from.found && slot_ok(from.id(pc.seq, g.a.idx64), p.pad, p.slots) &&
-            write_slot(g.a, pc.seq, 0, p.pad, p.slots, &to)) {
-#pragma unroll
-          for (int c = 0; c < HALF; c += 8) {
-            if (p.state_dtype == SSU_F32)
-              store_rows8<float, DK, ROWS>(rows_of_state(static_cast<float*>(p.state), to, h), c,
-                                            buf, S + c);
-            else if (p.state_dtype == SSU_BF16)
-              store_rows8<__nv_bfloat16, DK, ROWS>(
-                  rows_of_state(static_cast<__nv_bfloat16*>(p.state), to, h), c, buf, S + c);
-            else
-              store_rows8<__half, DK, ROWS>(rows_of_state(static_cast<__half*>(p.state), to, h), c,
-                                             buf, S + c);
-          }
+            write_slot(g.a, pc.seq, 0, p.pad, p.slots, &to) && lane < ROWS) {
+          if (p.state_dtype == SSU_F32)
+            store_row<float, HALF>(row_of_state(static_cast<float*>(p.state), to, h), wide, S);
+          else if (p.state_dtype == SSU_BF16)
+            store_row<__nv_bfloat16, HALF>(row_of_state(static_cast<__nv_bfloat16*>(p.state), to, h),
+                                           wide, S);
+          else
+            store_row<__half, HALF>(row_of_state(static_cast<__half*>(p.state), to, h), wide, S);
         }
+        __syncwarp();
       }
     }
   }
