@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;  // this warp's lanes
 
   if (wg == 5) {
-    regs_dec<64>();
+    regs_dec<48>();
     // ---- the products: scores, D and the outputs' two from a warp each, so that none
     // waits for what only another one needs
     if (warp == 20 || warp == 22 || warp == 23) {
@@ -1144,7 +1144,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (dead) break;
     }
   } else {
-    regs_inc<112>();
+    regs_inc<120>();
     // ---- S ---------------------------------------------------------------
     const int half = wg - 2, st_tid = tid - 256;  // 0 .. 255
     const int row = ROWS * (warp & 3) + lane % ROWS;
