@@ -3,7 +3,7 @@
 
 namespace linattn {
 
-// H * tiles is the grid's second dimension
+// heads are the grid's second dimension, items of a prompt call are counted in 32 bits
 constexpr int64_t kMostHeads = 4096, kMostDim = 256;
 
 static ssu_status check(const ssu_linattn_params* c, int64_t rows, bool pool_needed, Args* p) {

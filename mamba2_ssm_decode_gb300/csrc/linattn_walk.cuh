@@ -8,15 +8,17 @@ namespace linattn {
 
 // A state row is dk elements; a lane owns 16 of them, as 16-byte chunks that
 // alternate with those of the row's other lanes, so that a warp's load covers
-// whole 128-byte lines.  A lane owns the same chunks of U rows.
-template <class ST, int DK>
+// whole 128-byte lines.  A lane owns the same chunks of U rows.  ONE: a row a
+// sequence; sequences of several rows wait for one's operands after the other's, and
+// more warps, of fewer state rows each, cover that.
+template <class ST, int DK, bool ONE>
 struct WalkLayout {
   static constexpr int E = 16;                      // elements a lane owns of a row
   static constexpr int VEC = 16 / (int)sizeof(ST);  // elements of a chunk
   static constexpr int CPL = E / VEC;               // chunks a lane owns of a row
   static constexpr int LPR = DK / E;                // lanes of a row
   static constexpr int RPW = 32 / LPR;              // rows of a warp's load
-  static constexpr int U = LPR >= 8 ? 4 : LPR == 4 ? 2 : 1;
+  static constexpr int U = LPR >= 8 ? (ONE ? 4 : 2) : LPR == 4 && ONE ? 2 : 1;
   static constexpr int ROWS = RPW * U;              // rows of a warp
 };
 
@@ -25,21 +27,21 @@ constexpr int kWalkWarps = 4;
 // ONE: a row a sequence, which is that of its number.
 template <class ST, class IT, int DK, bool ONE>
 __global__ void __launch_bounds__(kWalkWarps * 32)
-    linattn_walk_kernel(const Args p, const Seqs a, int tiles) {
-  using L = WalkLayout<ST, DK>;
+    linattn_walk_kernel(const Args p, const Seqs a) {
+  using L = WalkLayout<ST, DK, ONE>;
   constexpr int U = L::U, E = L::E, VEC = L::VEC, CPL = L::CPL, LPR = L::LPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ql = lane % LPR;
   const int s = blockIdx.x;
-  const int h = blockIdx.y / tiles, g = h / p.hr;
-  const int p0 = (blockIdx.y - h * tiles) * kWalkWarps * L::ROWS + warp * L::ROWS + lane / LPR;
+  const int h = blockIdx.y, g = h / p.hr;
+  const int p0 = blockIdx.z * kWalkWarps * L::ROWS + warp * L::ROWS + lane / LPR;
 
   const Item it = packed_item<ONE>(a, s, p.pad, p.slots);
   if (it.len == 0) return;
   const bool from = it.read_ok && (!p.has_init || p.has_init[s]);
 
   // state rows p0 + u RPW; what a row does not have stays zero and is not stored
-  float S[U][E];
+  float2 S[U][E / 2];  // in pairs: an instruction for two
   const int64_t head = (int64_t)p.dv * DK;
   const ST* src = static_cast<const ST*>(p.state) + (it.src * p.H + h) * head;
 #pragma unroll
@@ -51,7 +53,8 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
       if (from && row < p.dv)
         w = load_pack<ST, VEC>(src + (int64_t)row * DK + (c * LPR + ql) * VEC);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) S[u][c * VEC + e] = to_f(w.v[e]);
+      for (int e = 0; e < VEC; e += 2)
+        S[u][(c * VEC + e) / 2] = make_float2(to_f(w.v[e]), to_f(w.v[e + 1]));
     }
   }
 
@@ -68,19 +71,21 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
       load_floats<IT, VEC>(kp + (c * LPR + ql) * VEC, p.qk_vec, k + c * VEC);
       load_floats<IT, VEC>(qp + (c * LPR + ql) * VEC, p.qk_vec, q + c * VEC);
     }
-    const float d = lp ? expf(*lp) : 1.0f;
+    const float decay = lp ? expf(*lp) : 1.0f;
+    const float2 d = make_float2(decay, decay);
     float y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = p0 + u * L::RPW;
-      const float v = row < p.dv ? to_f(vp[row]) : 0.0f;
-      float sum = 0.0f;
+      const float one = row < p.dv ? to_f(vp[row]) : 0.0f;
+      const float2 v = make_float2(one, one);
+      float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        S[u][e] = fmaf(v, k[e], S[u][e] * d);
-        sum = fmaf(S[u][e], q[e], sum);
+      for (int e = 0; e < E / 2; ++e) {
+        S[u][e] = __ffma2_rn(v, make_float2(k[2 * e], k[2 * e + 1]), __fmul2_rn(S[u][e], d));
+        sum = __ffma2_rn(S[u][e], make_float2(q[2 * e], q[2 * e + 1]), sum);
       }
-      y[u] = sum;
+      y[u] = sum.x + sum.y;
     }
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1)
@@ -104,7 +109,12 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
         for (int c = 0; c < CPL; ++c) {
           Pack<ST, VEC> w;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) w.v[e] = from_f<ST>(S[u][c * VEC + e]);
+          for (int e = 0; e < VEC; e += 2) {
+            const float2 f = S[u][(c * VEC + e) / 2];
+            Words<ST, 2> two;
+            two.set(&f);
+            two.store(&w.v[e]);
+          }
           store_pack<ST, VEC>(dst + (int64_t)row * DK + (c * LPR + ql) * VEC, w);
         }
       }
@@ -117,17 +127,21 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
   }
 }
 
+template <class ST, class IT, int DK, bool ONE>
+cudaError_t launch_walk_form(const Args& p, const Seqs& a, cudaStream_t stream) {
+  constexpr int per = kWalkWarps * WalkLayout<ST, DK, ONE>::ROWS;
+  const int tiles = (p.dv + per - 1) / per;
+  // sequences along x, which has room for them all
+  linattn_walk_kernel<ST, IT, DK, ONE>
+      <<<dim3((unsigned)a.n, (unsigned)p.H, (unsigned)tiles), kWalkWarps * 32, 0, stream>>>(p, a);
+  return cudaGetLastError();
+}
+
 template <class ST, class IT, int DK>
 cudaError_t launch_walk_dk(const Args& p, const Seqs& a, cudaStream_t stream) {
-  constexpr int per = kWalkWarps * WalkLayout<ST, DK>::ROWS;
-  const int tiles = (p.dv + per - 1) / per;
-  // sequences along x, which has room for them all; heads and row tiles along y
-  const dim3 grid((unsigned)a.n, (unsigned)(p.H * tiles));
   if (!a.cu && !a.na && a.steps == 1 && !p.prompt)
-    linattn_walk_kernel<ST, IT, DK, true><<<grid, kWalkWarps * 32, 0, stream>>>(p, a, tiles);
-  else
-    linattn_walk_kernel<ST, IT, DK, false><<<grid, kWalkWarps * 32, 0, stream>>>(p, a, tiles);
-  return cudaGetLastError();
+    return launch_walk_form<ST, IT, DK, true>(p, a, stream);
+  return launch_walk_form<ST, IT, DK, false>(p, a, stream);
 }
 
 template <class ST, class IT>
