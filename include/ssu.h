@@ -717,7 +717,11 @@ int64_t ssu_linattn_workspace_bytes(int64_t rows, int64_t nseqs, int64_t nheads,
  * Prompt form; arguments and rules as in ssu_conv_fwd_varlen (state may be
  * NULL).  workspace: device memory of ssu_linattn_workspace_bytes(...) bytes,
  * 16-byte aligned; nothing in it need be kept between calls, and calls that
- * share it must not overlap.
+ * share it must not overlap.  One launch where rows are taken one by one (fp32,
+ * dk or dv other than 64 and 128, rows off 16-byte boundaries), else two, or four
+ * where a sequence may be long enough to be cut into pieces.  A value that is not
+ * finite makes outputs of its own row and of later ones NaN where it takes part
+ * (of v: its channel), no others.
  */
 ssu_status ssu_linattn_fwd_varlen(const ssu_linattn_params* p, int64_t nseqs, int64_t rows,
                                   const void* cu_seqlens, ssu_dtype meta_dtype,
