@@ -2,7 +2,9 @@
 // the GPU from its lengths: sequence starts, the chunks of the SSD prefill, each
 // row's sequence and position; and slot tables, filled with the lowest free slots.
 //
-// Integers only, a few bytes a row: what the calls cost is latency.
+// Integers only, a few bytes a row: what the calls cost is latency.  16 sequences 6 us,
+// 2048 sequences of 524288 rows 10.3 us; 20 entries 6 us, 8000 entries of a pool of 16384
+// 18 us (one CTA: its searches).
 #include "layer_common.cuh"
 
 namespace maps {

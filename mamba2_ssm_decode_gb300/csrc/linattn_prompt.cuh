@@ -34,6 +34,12 @@
 // (the fourth product alone) and its decay, a second one adds them up to the state
 // that enters each piece.  Every launch but the first is set up while the one before
 // runs (programmatic dependent launch).
+//
+// 20634 tokens of 16 prompts, 32 heads of 128 x 128 in bf16: 202 us (HBM's floor 108,
+// the tensor pipe's 62).  A chunk takes some 4000 cycles; what bounds it is the issue of
+// instructions (48 % of the slots) and their supply (2.8 cycles an instruction: six roles
+// share each scheduler's instruction cache), so fewer instructions count, and neither more
+// stages (210 us) nor fewer waits (204).
 #pragma once
 
 #include <cuda.h>

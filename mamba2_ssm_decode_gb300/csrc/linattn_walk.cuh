@@ -1,5 +1,11 @@
 // linattn_walk.cuh -- the recurrent form of linear attention (linattn.cuh):
 // tokens, drafted tokens, and the prompts that the tensor cores do not take.
+//
+// A state is read and written once and bounds the call: 256 tokens of 32 heads of 128 x
+// 128 fp32, 163 us (1082 MB, 98 % of a copy's rate).  128 sequences of 1 to 4 drafted
+// tokens, 80 heads of 64 x 128 bf16, where the state is written after each: 123 us (595
+// MB; 71 % of issue slots).  With the next row's operands in registers meanwhile they
+// took 187 and 148 us: warps cover the loads better than registers do.
 #pragma once
 
 #include "linattn.cuh"
