@@ -33,9 +33,8 @@ struct Args {
   int o_vec;   // ... and of out
   int disable;
   int64_t pad;
-  // prompt form: the state is written once, after the last row
-  int prompt;
-  const uint8_t* has_init;  // per sequence, or NULL: every valid slot is read
+  int prompt;  // the state is written once, after the last row
+  const uint8_t* has_init;  // prompts: per sequence, or NULL: every valid slot is read
 };
 
 // Rows [r0, r0 + len) of a sequence from the slot it reads; one launch.
