@@ -678,7 +678,8 @@ ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, c
  * v, out     [rows, nheads, dv], likewise; out must not overlap an operand.
  * log_decay  ld, fp32, element (r, h) at r * log_decay_row_stride +
  *            h * log_decay_head_stride (a row stride of 0: one value per head),
- *            or NULL: no decay.  -infinity forgets what came before.
+ *            or NULL: no decay.  -infinity forgets what came before.  Above 0 a
+ *            state grows; prompts want e^(the sum over 64 rows) within fp32.
  * disable_state_update  1: no slot is written (decode form).
  */
 typedef struct ssu_linattn_params {

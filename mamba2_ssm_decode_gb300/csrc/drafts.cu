@@ -406,10 +406,35 @@ static ssu_status verify(const ssu_drafts_params* c, cudaStream_t stream) {
   const Rows out = rows_of(c->out, c->out_seq_stride, c->drafts + 1, c->token_dtype);
   if (overlap(out, rows_of(c->draft_tokens, c->draft_tokens_seq_stride, c->drafts, c->token_dtype),
               c->nseqs) ||
-      overlap(out, rows_of(c->uniform, c->uniform_seq_stride, c->drafts + 1, SSU_F32), c->nseqs) ||
-      overlap(out, rows_of(c->num_accepted, 1, 1, c->count_dtype), c->nseqs))
-    return fail(SSU_ERR_INVALID_ARGUMENT,
-                "out must not overlap draft_tokens, uniform or num_accepted");
+      overlap(out, rows_of(c->uniform, c->uniform_seq_stride, c->drafts + 1, SSU_F32), c->nseqs))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not overlap draft_tokens or uniform");
+  // the results against each other and the other operands, which other sequences' CTAs still
+  // read: the bytes from an operand's first to its last
+  struct Span {
+    const char* name;
+    const void* p;
+    int64_t bytes;
+  };
+  auto span = [](const char* name, const void* p, int64_t rows, int64_t stride, int64_t n, int64_t s) {
+    return Span{name, p, rows > 0 && n > 0 && p ? ((rows - 1) * stride + n) * s : 0};
+  };
+  const int64_t S = c->nseqs, K = c->drafts;
+  const Span all[] = {
+      span("out", c->out, S, c->out_seq_stride, K + 1, ts),
+      span("num_accepted", c->num_accepted, 1, 0, S, size_of(c->count_dtype)),
+      span("target_probs", c->target_probs, c->rows, c->target_row_stride, c->vocab, es),
+      span("draft_probs", c->draft_probs, S, c->draft_seq_stride,
+           K > 0 ? (K - 1) * c->draft_step_stride + c->vocab : 0, es),
+      span("cu_seqlens", c->cu_seqlens, 1, 0, S + 1, c->cu_seqlens ? size_of(c->meta_dtype) : 0),
+      span("greedy", c->greedy, 1, 0, S, 1),
+      span("draft_tokens", c->draft_tokens, S, c->draft_tokens_seq_stride, K, ts),
+      span("uniform", c->uniform, S, c->uniform_seq_stride, K + 1, 4)};
+  constexpr int kAll = (int)(sizeof(all) / sizeof(all[0]));
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < (i ? kAll : kAll - 2); ++j)  // out's rows may lie beside the last two's
+      if (all[i].bytes > 0 && all[j].bytes > 0 &&
+          overlap(Rows{all[i].p, 0, all[i].bytes}, Rows{all[j].p, 0, all[j].bytes}, 1))
+        return fail(SSU_ERR_INVALID_ARGUMENT, "%s must not overlap %s", all[i].name, all[j].name);
   if (c->nseqs == 0) return ok();
   Args a{};
   a.p = c->target_probs;

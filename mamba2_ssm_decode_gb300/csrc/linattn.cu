@@ -99,6 +99,13 @@ static ssu_status check_out(const ssu_linattn_params* c, int64_t rows) {
   for (const auto& v : in)
     if (overlap(out, v.rows, rows))
       return fail(SSU_ERR_INVALID_ARGUMENT, "out must not overlap %s", v.name);
+  // ... and against the pool, from out's first byte to its last
+  const int64_t last = (rows - 1) * c->out_row_stride + (c->nheads - 1) * c->out_head_stride + c->dv;
+  const int64_t pool = c->slots * c->nheads * c->dv * c->dk;
+  if (rows > 0 && c->state && pool > 0 &&
+      overlap(Rows{c->out, 0, last * size_of(c->io_dtype)},
+              Rows{c->state, 0, pool * size_of(c->state_dtype)}, 1))
+    return fail(SSU_ERR_INVALID_ARGUMENT, "out must not overlap state");
   return SSU_OK;
 }
 

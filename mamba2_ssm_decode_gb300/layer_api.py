@@ -287,7 +287,8 @@ def linattn_fwd_varlen(q, k, v, cu_seqlens, log_decay=None, scale=None, state=No
     which must not overlap an operand."""
     if out is None:
         out = result(stream, v.shape, v.dtype, v.device)
-    if workspace is None and v.dim() == 3 and q.dim() == 3 and v.dtype in _IO:
+    if (workspace is None and cu_seqlens is not None and v.dim() == 3 and q.dim() == 3
+            and v.dtype in _IO):
         need = linattn_workspace_bytes(v.shape[0], max(cu_seqlens.numel() - 1, 0), v.shape[1],
                                        v.shape[2], q.shape[2], v.dtype)
         if need > 0:

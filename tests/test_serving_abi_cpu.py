@@ -87,6 +87,8 @@ REFUSED = [
     (dict(q=FAR + (1 << 30), k=FAR + 64), INVALID, "out must not overlap k"),
     (dict(v=FAR - 2), INVALID, "out must not overlap v"),
     (dict(log_decay=FAR + 4, log_decay_head_stride=1), INVALID, "out must not overlap log_decay"),
+    (dict(state=FAR - 16), INVALID, "out must not overlap state"),
+    (dict(state=FAR + 4 * 512 - 16), INVALID, "out must not overlap state"),
 ]
 
 
@@ -186,6 +188,11 @@ def drafts(**over):
     (dict(draft_tokens=FAR + 4), INVALID, "must not overlap"),
     (dict(uniform=FAR + 20), INVALID, "must not overlap"),
     (dict(num_accepted=FAR + 8), INVALID, "must not overlap"),
+    (dict(target_probs=FAR - 4), INVALID, "out must not overlap target_probs"),
+    (dict(draft_probs=FAR + 20), INVALID, "out must not overlap draft_probs"),
+    (dict(cu_seqlens=FAR + 20), INVALID, "out must not overlap cu_seqlens"),
+    (dict(greedy=FAR + 23), INVALID, "out must not overlap greedy"),
+    (dict(num_accepted=FAKE + 4), INVALID, "num_accepted must not overlap"),
 ])
 def test_verify_refusals(lib, over, code, needle):  # noqa: F811
     assert lib.ssu_drafts_verify(ctypes.byref(drafts(**over)), None) == code

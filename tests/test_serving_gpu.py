@@ -495,6 +495,42 @@ def test_linattn_launches_graphs_and_streams():
     same_bits(got, want[0])
 
 
+@pytest.mark.parametrize("io,dv", [(BF16, 128), (F16, 64)])
+def test_linattn_captured_prompts_in_pieces(io, dv):
+    """Launches that are set up while the one before runs, replayed: four kernel nodes, the
+    bits of the eager call, also when the inputs change and when two graphs run at once."""
+    lens, H = [2500, 40], 2
+    i = lin_inputs(sum(lens), H, H, 64, dv, 2, io, F32, seed=17)
+    d, cu = on_gpu(i), cu_of(lens).to(DEV)
+    size = ssu.linattn_workspace_bytes(sum(lens), 2, H, dv, 64, io)
+
+    def call(pool, ws, out):
+        ssu.linattn_fwd_varlen(d["q"], d["k"], d["v"], cu, log_decay=d["log_decay"], state=pool,
+                               out=out, workspace=ws)
+
+    sets = [(d["pool"].clone(), torch.empty(size, dtype=torch.uint8, device=DEV),
+             torch.empty(sum(lens), H, dv, dtype=io, device=DEV)) for _ in range(3)]
+    assert graph_kernel_nodes(lambda: call(*sets[0])) == 4
+    sets[0][0].copy_(d["pool"])
+    graphs = []
+    for s in sets[1:]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(*s)
+    side = torch.cuda.Stream()
+    for step in range(3):
+        call(*sets[0])
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for s in sets[1:]:
+            same_bits(s[2], sets[0][2])
+            same_bits(s[0], sets[0][0])
+        d["v"].mul_(-0.5)
+
+
 def test_linattn_empty_and_refused():
     i = lin_inputs(6, 4, 2, 64, 64, 3)
     d = on_gpu(i)
@@ -511,6 +547,10 @@ def test_linattn_empty_and_refused():
         ssu.linattn_fwd_varlen(q, k, v, cu_of([1] * 6).to(DEV), state=pool)
     with pytest.raises(ValueError, match="slots need the state pool"):
         ssu.linattn_fwd_varlen(q, k, v, cu, state_batch_indices=cu[:2])
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        ssu.linattn_fwd_varlen(q, k, v, None)
+    with pytest.raises(ValueError, match="overlap state"):
+        ssu.linattn_update(pool, q[:3], k[:3], v[:3], out=pool.view(BF16)[0, 0].view(-1)[:768].view(3, 4, 64))
     with pytest.raises(ValueError, match="workspace"):
         ssu.linattn_fwd_varlen(q, k, v, cu, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="share the v dtype"):
