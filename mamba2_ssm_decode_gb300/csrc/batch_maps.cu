@@ -4,7 +4,7 @@
 //
 // Integers only, a few bytes a row: what the calls cost is latency.  16 sequences 6 us,
 // 2048 sequences of 524288 rows 10.3 us; 20 entries 6 us, 8000 entries of a pool of 16384
-// 18 us (one CTA: its searches).
+// 14.3 us (one CTA: its two passes over the table).
 #include "layer_common.cuh"
 
 namespace maps {
@@ -215,8 +215,12 @@ __device__ __forceinline__ int nth_bit(unsigned long long v, int k) {
 
 // One CTA: a bitmap of the slots that are kept, the free ones before each of its
 // words, and then, in the table's order, the k-th place without a slot takes the
-// k-th free one.  kEntries of the table a thread at a time.
-template <int kEntries>
+// k-th free one.  kEntries of the table a thread at a time.  LIST: the free slots are
+// listed in shared memory, where there is room for kListed of them; else each place
+// searches the words (8000 entries of a pool of 16384: 14.3 and 18 us).
+constexpr int kListed = 1 << 15;
+
+template <int kEntries, bool LIST>
 __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const AssignArgs a) {
   extern __shared__ unsigned long long held[];
   __shared__ int warps[kAssignThreads / 32];
@@ -260,6 +264,17 @@ __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const Assi
     free += total;
   }
   __syncthreads();
+  int* list = before + words;
+  if constexpr (LIST) {
+    for (int i = threadIdx.x; i < 4 * words; i += kAssignThreads) {  // 16 slots a thread
+      const int w = i >> 2, part = (i & 3) * 16;
+      const unsigned long long open = ~held[w];
+      int k = before[w] + __popcll(open & ((1ull << part) - 1));
+      for (unsigned m = (unsigned)(open >> part) & 0xffffu; m; m &= m - 1)
+        list[k++] = w * 64 + part + __ffs((int)m) - 1;
+    }
+    __syncthreads();
+  }
   // a warp has kEntries times 32 consecutive entries, 32 at a time
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int given = 0;
@@ -294,13 +309,17 @@ __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const Assi
       if (e >= entries) continue;
       int64_t got = a.pad;
       if ((need[i] >> lane & 1) && k < free) {
-        int lo = 0, hi = words;  // the last word with no more than k free ones before it
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (before[mid] <= k) lo = mid;
-          else hi = mid;
+        if constexpr (LIST) {
+          got = list[k];
+        } else {
+          int lo = 0, hi = words;  // the last word with no more than k free ones before it
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] <= k) lo = mid;
+            else hi = mid;
+          }
+          got = lo * 64 + nth_bit(~held[lo], k - before[lo]);
         }
-        got = lo * 64 + nth_bit(~held[lo], k - before[lo]);
       }
       store_int(a.out, e, a.is64, kept >> i & 1 ? v[i] : got);
       store_int(a.fresh, e, a.is64, got);
@@ -418,8 +437,11 @@ static ssu_status assign(const void* table, const void* counts, ssu_dtype index_
                 "overlap");
   AssignArgs a{table, counts, out, fresh, missing, index_dtype == SSU_I64, (int)nseqs, (int)steps,
                (int)slots, pad};
-  const int smem = (a.slots + 63) / 64 * 12;
-  auto kernel = entries <= kAssignThreads ? slots_assign_kernel<1> : slots_assign_kernel<8>;
+  const bool list = a.slots <= kListed;
+  const int smem = (a.slots + 63) / 64 * 12 + (list ? a.slots * 4 : 0);
+  const bool few = entries <= kAssignThreads;
+  auto kernel = list ? (few ? slots_assign_kernel<1, true> : slots_assign_kernel<8, true>)
+                     : (few ? slots_assign_kernel<1, false> : slots_assign_kernel<8, false>);
   if (smem > 40 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

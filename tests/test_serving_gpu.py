@@ -816,7 +816,8 @@ def test_maps_drive_the_ssd_prefill():
 
 @pytest.mark.parametrize("ints", [I32, I64])
 @pytest.mark.parametrize("S,T,slots", [(0, 4, 9), (5, 1, 3), (20, 1, 48), (300, 4, 900), (1500, 5, 9000),
-                                       (7, 0, 4), (9, 3, 0), (64, 1, 64), (70, 300, 70000)])
+                                       (7, 0, 4), (9, 3, 0), (64, 1, 64), (70, 300, 70000),
+                                       (300, 4, 32768), (300, 4, 32769), (2, 2, 40000)])
 @pytest.mark.parametrize("pad", [-1, 0, 5])
 def test_slots_assign(ints, S, T, slots, pad):
     r = np.random.default_rng(S + T + pad)
