@@ -18,8 +18,8 @@
 // P, S and w V are computed, not given, and enter the products as 16-bit parts
 // that add up to them: P and S as a high part and a remainder (to 2^-17 of each
 // with bf16, 2^-22 with fp16, where one part alone would be as far off as the
-// output's own rounding), w V as three of bf16 where the state is kept in 32 bits
-// (2^-26; two leave 2^-17, which shows in it), else two.  fp16 has no room for what
+// output's own rounding), w V as three of bf16 (all of an fp32 number; two leave
+// 2^-17, which shows in an fp32 state) or two of fp16.  fp16 has no room for what
 // is large or small: there the rows of P and S and all of a chunk's w V are brought
 // to the middle of its range by powers of two, which are taken out of the products.
 //
