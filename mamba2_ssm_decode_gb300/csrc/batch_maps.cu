@@ -219,6 +219,7 @@ __device__ __forceinline__ int nth_bit(unsigned long long v, int k) {
 // listed in shared memory, where there is room for kListed of them; else each place
 // searches the words (8000 entries of a pool of 16384: 14.3 and 18 us).
 constexpr int kListed = 1 << 15;
+constexpr int kMostSlots = 1 << 20;
 
 template <int kEntries, bool LIST>
 __global__ void __launch_bounds__(kAssignThreads) slots_assign_kernel(const AssignArgs a) {
@@ -390,7 +391,8 @@ static ssu_status prompt_maps(const ssu_prompt_maps_params* c, cudaStream_t stre
   a.has_init = c->has_initial_state;
   a.row_seq = c->row_seq;
   a.row_pos = c->row_pos;
-  const int smem = (2 * a.n + 1) * (int)sizeof(int);
+  auto smem_of = [](int n) { return (2 * n + 1) * (int)sizeof(int); };
+  const int smem = smem_of(a.n);
   const int64_t rows = a.row_seq || a.row_pos ? a.rows : 0;
   const int64_t items = rows > a.most ? rows : a.most;
   const int64_t fit = ssu::sm_count();
@@ -400,8 +402,9 @@ static ssu_status prompt_maps(const ssu_prompt_maps_params* c, cudaStream_t stre
   auto kernel = many_s ? (many_r ? prompt_maps_kernel<true, true> : prompt_maps_kernel<true, false>)
                        : (many_r ? prompt_maps_kernel<false, true> : prompt_maps_kernel<false, false>);
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the most of any call: the limit is the kernel's, and another thread's call sets it too
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               smem_of(SSU_PROMPT_MAPS_MAX_SEQS));
     if (e != cudaSuccess) return launched(e);
   }
   kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(a);
@@ -415,7 +418,7 @@ static ssu_status assign(const void* table, const void* counts, ssu_dtype index_
     return fail(SSU_ERR_INVALID_ARGUMENT, "the slot table and counts must be int32 or int64");
   if (nseqs < 0 || steps < 0 || slots < 0)
     return fail(SSU_ERR_INVALID_ARGUMENT, "nseqs, steps and slots must be >= 0");
-  if (slots > (1 << 20)) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
+  if (slots > kMostSlots) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
   if (nseqs > 0x7fffffffLL || steps > 0x7fffffffLL || (steps > 0 && nseqs > (1 << 24) / steps))
     return fail(SSU_ERR_UNSUPPORTED, "the table must not exceed 2^24 entries");
   const int64_t entries = nseqs * steps;
@@ -438,13 +441,14 @@ static ssu_status assign(const void* table, const void* counts, ssu_dtype index_
   AssignArgs a{table, counts, out, fresh, missing, index_dtype == SSU_I64, (int)nseqs, (int)steps,
                (int)slots, pad};
   const bool list = a.slots <= kListed;
-  const int smem = (a.slots + 63) / 64 * 12 + (list ? a.slots * 4 : 0);
+  auto smem_of = [list](int n) { return (n + 63) / 64 * 12 + (list ? n * 4 : 0); };
+  const int smem = smem_of(a.slots);
   const bool few = entries <= kAssignThreads;
   auto kernel = list ? (few ? slots_assign_kernel<1, true> : slots_assign_kernel<8, true>)
                      : (few ? slots_assign_kernel<1, false> : slots_assign_kernel<8, false>);
-  if (smem > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > 40 * 1024) {  // the most of any call, as above
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               smem_of(list ? kListed : kMostSlots));
     if (e != cudaSuccess) return launched(e);
   }
   kernel<<<1, kAssignThreads, smem, stream>>>(a);
