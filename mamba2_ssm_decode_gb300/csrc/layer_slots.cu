@@ -9,6 +9,7 @@
 namespace layer {
 
 constexpr int kMaxPools = SSU_SLOTS_MAX_POOLS;
+constexpr int kMostSlots = 1 << 20;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
 constexpr int kChunk = kCopyThreads * kCopyUnroll * 16;  // bytes of a slot per work item
@@ -249,7 +250,7 @@ static ssu_status check_pools(const ssu_pool* pools, int npools, int64_t slots, 
     return fail(SSU_ERR_INVALID_ARGUMENT, "npools and slots must be >= 0");
   if (npools > kMaxPools)
     return fail(SSU_ERR_UNSUPPORTED, "at most %d pools per call, got %d", kMaxPools, npools);
-  if (slots > (1 << 20)) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
+  if (slots > kMostSlots) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
   if (npools > 0 && !pools) return fail(SSU_ERR_INVALID_ARGUMENT, "pools must not be NULL");
   *ps = Pools<MOST>{};
   int64_t chunks = 0;
@@ -361,7 +362,9 @@ static ssu_status compact_as(const ssu_pool* pools, int npools, int64_t slots, c
   const int smem = plan_smem(slots);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(slots_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the most of any call: the limit is the kernel's, and another thread's call sets it too
+    e = cudaFuncSetAttribute(slots_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             plan_smem(kMostSlots));
     if (e != cudaSuccess) return launched(e);
   }
   slots_plan_kernel<<<1, kPlanThreads, smem, stream>>>(

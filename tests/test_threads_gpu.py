@@ -90,3 +90,23 @@ def test_maps_of_two_batches_at_once():
     for n, t in results:
         assert torch.equal(t["cu_seqlens"].cpu(), torch.arange(0, 2 * n + 1, 2, dtype=torch.int32))
         assert int(t["num_chunks"]) == n
+
+
+def test_compaction_of_two_pools_at_once():
+    """2^20 and 300000 slots."""
+    lib, keep, jobs, results = _abi.lib(), [], [], []
+    for slots in (1 << 20, 300000):
+        pool = torch.arange(slots, dtype=torch.int32, device=DEV)
+        table, out, live = ints(8), ints(8), ints(1, fill=7)
+        table.copy_(torch.arange(8, dtype=torch.int32) + slots - 8)
+        pools = (_abi.Pool * 1)(_abi.Pool(pool.data_ptr(), 4, 4))
+        size = lib.ssu_slots_compact_workspace_bytes(slots, 8, 0)
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        keep.append((pool, table, pools, ws))
+        results.append((out, live))
+        args = [pools, 1, slots, table.data_ptr(), out.data_ptr(), _abi.SSU_I32, 8, -1,
+                live.data_ptr(), ws.data_ptr(), size]
+        jobs.append(lambda stream, args=args: lib.ssu_slots_compact(*args, stream))
+    assert at_once(jobs) == []
+    for out, live in results:
+        assert sorted(out.tolist()) == list(range(8)) and int(live) == 8
