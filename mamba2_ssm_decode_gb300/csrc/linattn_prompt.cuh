@@ -85,7 +85,7 @@ struct PromptArgs {
   Header* head;
   Piece* pieces[2];
   CutSeq* cuts;
-  float* decay;  // [entries][H]: what a piece decays the state by
+  float* decay;  // [entries][H]: log2 of what a piece decays the state by
   float* state;  // [entries][H][dv * dk], in the threads' order
   int fair, cut;  // chunks: more than `fair` of them are cut into pieces of about `cut`
   int entries, splits;  // room: states, sequences in pieces
@@ -235,6 +235,25 @@ static __global__ void __launch_bounds__(kPlanThreads) linattn_plan_kernel(const
 // piece j: E_j = decay of piece j - 1 E_(j - 1) + what it adds.
 constexpr int kJoinThreads = 256;
 
+// 2^l as a factor: near 1 as 1 + add, as a chunk's decay is, and in three equal steps where
+// fp32 has no room for it, though it may have for the product (nothing stays nothing).
+struct Factor {
+  float step, last;
+  bool near;
+  __device__ __forceinline__ explicit Factor(float l) {
+    near = fabsf(l) < 1.0f;
+    const float m = l > 360.0f && l < INFINITY ? 360.0f : l;  // beyond, all but zero is infinite
+    const bool inside = fabsf(m) < 126.0f;
+    step = inside ? 1.0f : ex2(m * (1.0f / 3.0f));
+    last = near ? expm1f(l * 0.693147181f) : inside ? ex2(m) : step;
+  }
+  // v + 2^l s
+  __device__ __forceinline__ float times(float s, float v) const {
+    s = s * step * step;
+    return fmaf(s, last, near ? s + v : v);
+  }
+};
+
 static __global__ void __launch_bounds__(kJoinThreads) linattn_join_kernel(const PromptArgs g) {
   let_next_start();
   launch_before_ended();
@@ -250,13 +269,13 @@ static __global__ void __launch_bounds__(kJoinThreads) linattn_join_kernel(const
 #pragma unroll 4
   for (int j = 2; j < c.of; ++j) {
     e += all;
-    const float d = *by;
+    const Factor d(*by);
     by += g.p.H;
     const float4 v = *e;
-    s.x = fmaf(s.x, d, v.x);
-    s.y = fmaf(s.y, d, v.y);
-    s.z = fmaf(s.z, d, v.z);
-    s.w = fmaf(s.w, d, v.w);
+    s.x = d.times(s.x, v.x);
+    s.y = d.times(s.y, v.y);
+    s.z = d.times(s.z, v.z);
+    s.w = d.times(s.w, v.w);
     *e = s;
   }
 }
@@ -272,14 +291,13 @@ struct Chunk {
   Piece piece;
 };
 
-struct Tables {        // of a chunk, in units of log2
+struct alignas(16) Tables {  // of a chunk, in units of log2; read in pairs
   float a[kC];         // a_t
   float x[kC];         // e^(r - a_s), r the a of the last token of s's 16
   float ea[kC];        // scale e^(a_t)
   float w[kC];         // e^(a_C - a_s); 0 behind the last row
   float r[kC / 16];    // the four r
   float keep, add;     // e^(a_C) = keep + add, keep 0 or 1
-  float decay;         // e^(a_C)
   int mild;            // e^(a_t - r) and e^(r - a_s) stay within 2^60 inside the 16 of an r
 };
 
@@ -317,14 +335,14 @@ struct PromptSmem {
   unsigned char stage[kStages][Z::kStage];  // Q, K, V
   unsigned char wv[PARTS][Z::kV];
   unsigned char p[2][Z::kP];
-  unsigned char out[Z::kOut ? Z::kOut : 16];
+  alignas(16) unsigned char out[Z::kOut ? Z::kOut : 16];
   Tables tab[kStages];
   Chunk chunk[kStages];
   // fp16 (two parts) alone
   static constexpr int kScaled = PARTS == 2 ? 128 : 1;
   float row_max[2][2][kScaled];  // the largest value of half a row of S
   float row_scale[2][kScaled];  // what a row of S was divided by
-  float p_scale[2][kScaled];    // ... a token's row of P
+  alignas(16) float p_scale[2][kScaled];  // ... a token's row of P, read in pairs
   float v_scale[kStages];       // ... w V
   uint32_t v_max[kStages][4];   // the largest of w V, by warp
   int bad[kStages][128];    // the first token of the chunk whose v is not finite
@@ -748,6 +766,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                        : 0.0f;
         };
         float l0 = decay_at(2 * lane), l1 = decay_at(2 * lane + 1);
+        double whole = 0.0;  // log2 of what the piece decays a state by
         for (int c = 0; c < chunks; ++c, ++n) {
           const int st = n % kStages;
           const int t0 = c * kC, rows = min(kC, piece.len - t0);
@@ -765,6 +784,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // 2^-44 (sums of doubles took this warp twice the time of a chunk's products), or
           // as doubles where the batch has something that these do not hold
           float a0, a1, x0, x1, w0, w1, end;  // a_t; r - a_t; a_C - a_t; a_C
+          [[maybe_unused]] double exact;      // a_C
           auto sums = [&](auto e0, auto e1, float unit) {
             auto inc = e0 + e1;
 #pragma unroll
@@ -782,6 +802,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             w0 = (float)(all - before) * unit;
             w1 = (float)(all - inc) * unit;
             end = (float)all * unit;
+            if constexpr (!FULL) exact = (double)all * (double)unit;
           };
           if (__all_sync(0xffffffffu, d0 <= 4096.0f && d1 <= 4096.0f))
             sums(__float2ll_rn(d0 * 0x1p44f), __float2ll_rn(d1 * 0x1p44f), 0x1p-44f);
@@ -797,6 +818,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // near 1 the decay is 1 + add: rounded by itself it would be off by the same
           // 2^-25 chunk after chunk
           const float e = ex2(end);
+          if constexpr (!FULL) {
+            // summed before the exponential is taken: a product of the chunks' decays would be
+            // off by each one's rounding.  What fp32 forgets here it does not remember, whatever
+            // a state grows by behind it.
+            whole += exact;
+            if (e == 0.0f || whole < -320.0) whole = -INFINITY;
+            if (c == chunks - 1 && lane == 0)
+              g.decay[(int64_t)(piece.base + piece.j) * p.H + h] = (float)whole;
+          }
           const float keep = e > 0.5f ? 1.0f : 0.0f;
           const float add = e > 0.5f ? expm1f(end * 0.693147181f) : e;
           if (n >= kStages && !warp_wait(sm, g.err, &sm.empty[st], (n / kStages - 1) & 1)) {
@@ -824,7 +854,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           *reinterpret_cast<float2*>(tab.w + t) = w;
           if ((lane & 7) == 7) tab.r[lane / 8] = a1;
           if (lane == 0) {
-            tab.decay = e;
             tab.keep = keep;
             tab.add = add;
             tab.mild = mild;
@@ -1152,10 +1181,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else {
     regs_inc<120>();
     // ---- S ---------------------------------------------------------------
-    const int half = wg - 2, st_tid = tid - 256;  // 0 .. 255
+    const int half = wg - 2;
     const int row = ROWS * (warp & 3) + lane % ROWS;
     float S[HALF];
-    float total = 1.0f;
     uint32_t met = 0;
     bool dead = false;
     // fp16: the largest value of this thread's half of a row, left for the other half's
@@ -1217,7 +1245,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       const int st = n % kStages;
       if (!warp_wait(sm, g.err, &sm.full[st], (n / kStages) & 1) || sm.chunk[st].stop) break;
       const Tables& tab = sm.tab[st];
-      const float keep = tab.keep, add = tab.add, decay = tab.decay;
+      const float keep = tab.keep, add = tab.add;
       const bool first = sm.chunk[st].first, last = sm.chunk[st].last;
       Piece pc{};
       int h = 0;
@@ -1230,7 +1258,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (first) {
 #pragma unroll
         for (int i = 0; i < HALF; ++i) S[i] = 0.0f;
-        total = 1.0f;
         if (FULL && pc.of > 1) {
           const float4* from = entry(pc.base + pc.j, h);
 #pragma unroll
@@ -1273,7 +1300,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc::fence_after_sync();
         give(n);
       }
-      total *= decay;
       if (!warp_wait(sm, g.err, &sm.d_full, n & 1)) break;
       tc::fence_after_sync();
       float back = 1.0f;
@@ -1310,7 +1336,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           for (int i = 0; i < HALF / 4; ++i)
             to[i * ROWS] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
         }
-        if (st_tid == 0) g.decay[(int64_t)(pc.base + pc.j) * p.H + h] = total;
       } else if (pc.j == pc.of - 1) {
         const Slot from = load_slot(g.a.src, pc.seq, 0, g.a.idx64);
         int64_t to;
