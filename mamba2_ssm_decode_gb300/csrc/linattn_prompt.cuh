@@ -291,14 +291,29 @@ struct Chunk {
   Piece piece;
 };
 
+// a - b
+__device__ __forceinline__ float between(float2 a, float2 b) { return (a.x - b.x) + (a.y - b.y); }
+// A sum of log decays as two floats: in units of 2^-44 its multiples of 2^-8, whole below
+// 2^16, and the rest to 2^-32; of a double what fp32 takes and what that leaves.
+__device__ __forceinline__ float2 in_two(long long v) {
+  return make_float2((float)(int)(v >> 36) * 0x1p-8f, (float)(uint32_t)(v >> 4) * 0x1p-40f);
+}
+__device__ __forceinline__ float2 in_two(double v) {
+  const float high = (float)v;
+  return make_float2(high, (float)(v - (double)high));
+}
+
 struct alignas(16) Tables {  // of a chunk, in units of log2; read in pairs
   float a[kC];         // a_t
+  float2 two[kC];      // a_t as the sum of two, which gives a difference its own rounding
+                       // however large the sums are
   float x[kC];         // e^(r - a_s), r the a of the last token of s's 16
   float ea[kC];        // scale e^(a_t)
   float w[kC];         // e^(a_C - a_s); 0 behind the last row
   float r[kC / 16];    // the four r
   float keep, add;     // e^(a_C) = keep + add, keep 0 or 1
-  int mild;            // e^(a_t - r) and e^(r - a_s) stay within 2^60 inside the 16 of an r
+  int mild;            // e^(a_t - r) and e^(r - a_s) stay within 2^60 inside the 16 of an r, and
+                       // a_t within 128, so that a_t - r is off by 2^-17 at most
 };
 
 // A tile: 64 rows (tokens) of 128 bytes, one after the other, the 16-byte pieces
@@ -783,7 +798,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // a_t in 64 bits, so that differences of large sums keep their digits: in units of
           // 2^-44 (sums of doubles took this warp twice the time of a chunk's products), or
           // as doubles where the batch has something that these do not hold
-          float a0, a1, x0, x1, w0, w1, end;  // a_t; r - a_t; a_C - a_t; a_C
+          float2 two0, two1;            // a_t
+          float x0, x1, w0, w1, end;    // r - a_t; a_C - a_t; a_C
           [[maybe_unused]] double exact;      // a_C
           auto sums = [&](auto e0, auto e1, float unit) {
             auto inc = e0 + e1;
@@ -795,8 +811,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const auto all = __shfl_sync(0xffffffffu, inc, 31);
             const auto ref = __shfl_sync(0xffffffffu, inc, lane | 7);
             const auto before = inc - e1;
-            a0 = (float)before * unit;
-            a1 = (float)inc * unit;
+            two0 = in_two(before);
+            two1 = in_two(inc);
             x0 = (float)(ref - before) * unit;
             x1 = (float)(ref - inc) * unit;
             w0 = (float)(all - before) * unit;
@@ -811,10 +827,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           // all of it before the stage is free
           const int t = 2 * lane;
           const float2 x = make_float2(ex2(x0), ex2(x1));
+          const float a0 = two0.x + two0.y, a1 = two1.x + two1.y;
           const float2 ea = make_float2(p.scale * ex2(a0), p.scale * ex2(a1));
           const float2 w = make_float2(t < rows ? ex2(w0) : 0.0f, t + 1 < rows ? ex2(w1) : 0.0f);
-          const bool mild =
-              __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f);
+          const bool mild = __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f &&
+                                                        fabsf(a0) <= 128.0f && fabsf(a1) <= 128.0f);
           // near 1 the decay is 1 + add: rounded by itself it would be off by the same
           // 2^-25 chunk after chunk
           const float e = ex2(end);
@@ -849,6 +866,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           Tables& tab = sm.tab[st];
           *reinterpret_cast<float2*>(tab.a + t) = make_float2(a0, a1);
+          *reinterpret_cast<float4*>(tab.two + t) = make_float4(two0.x, two0.y, two1.x, two1.y);
           *reinterpret_cast<float2*>(tab.x + t) = x;
           *reinterpret_cast<float2*>(tab.ea + t) = ea;
           *reinterpret_cast<float2*>(tab.w + t) = w;
@@ -891,23 +909,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (kBF16 && n > 0 && !warp_wait(sm, g.err, &sm.p_free, (n - 1) & 1)) break;
         tc::fence_after_sync();
         // 16 columns: scale e^(a_t - a_s) q_t . k_s, 0 above the diagonal
-        auto weighed = [&](int b, float2 (&y)[4]) {
+        auto weighed = [&](auto mild, int b, float2 (&y)[4]) {
           float s[8];
           ld_frag2(tmem + quad + Z::kSc + (n & 1) * 64 + 16 * b, s);
-          const float u0 = p.scale * ex2(a0 - tab.r[b]), u1 = p.scale * ex2(a1 - tab.r[b]);
+          float u0, u1;
+          float2 r0, r1;
+          if constexpr (mild) {
+            u0 = p.scale * ex2(a0 - tab.r[b]), u1 = p.scale * ex2(a1 - tab.r[b]);
+          } else {
+            r0 = tab.two[t0], r1 = tab.two[t1];
+          }
           tc::wait_ld();
 #pragma unroll
           for (int f = 0; f < 2; ++f) {  // 8 columns
             const int c = 16 * b + 8 * f + cc;
             float2 e0, e1;
-            if (mild) {
+            if constexpr (mild) {
               const float2 x = *reinterpret_cast<const float2*>(tab.x + c);
               e0 = __fmul2_rn(x, make_float2(u0, u0));
               e1 = __fmul2_rn(x, make_float2(u1, u1));
             } else {
-              const float2 x = *reinterpret_cast<const float2*>(tab.a + c);
-              e0 = make_float2(p.scale * ex2(a0 - x.x), p.scale * ex2(a0 - x.y));
-              e1 = make_float2(p.scale * ex2(a1 - x.x), p.scale * ex2(a1 - x.y));
+              const float4 x = *reinterpret_cast<const float4*>(tab.two + c);
+              const float2 c0 = make_float2(x.x, x.y), c1 = make_float2(x.z, x.w);
+              e0 = make_float2(p.scale * ex2(between(r0, c0)), p.scale * ex2(between(r0, c1)));
+              e1 = make_float2(p.scale * ex2(between(r1, c0)), p.scale * ex2(between(r1, c1)));
             }
             float2 &y0 = y[2 * f], &y1 = y[2 * f + 1];
             y0 = __fmul2_rn(make_float2(s[4 * f], s[4 * f + 1]), e0);
@@ -935,22 +960,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 1
           for (int b = 0; b <= warp; ++b) {
             float2 y[4];
-            weighed(b, y);
+            if (mild) weighed(std::true_type{}, b, y);
+            else weighed(std::false_type{}, b, y);
             leave(b, y);
           }
         } else {
           float2 y[4][4];
           float m0 = 0.0f, m1 = 0.0f;
+          auto all = [&](auto kind) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            if (b > warp) continue;
-            weighed(b, y[b]);
+            for (int b = 0; b < 4; ++b) {
+              if (b > warp) continue;
+              weighed(kind, b, y[b]);
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              m0 = fmaxf(m0, fmaxf(fabsf(y[b][2 * f].x), fabsf(y[b][2 * f].y)));
-              m1 = fmaxf(m1, fmaxf(fabsf(y[b][2 * f + 1].x), fabsf(y[b][2 * f + 1].y)));
+              for (int f = 0; f < 2; ++f) {
+                m0 = fmaxf(m0, fmaxf(fabsf(y[b][2 * f].x), fabsf(y[b][2 * f].y)));
+                m1 = fmaxf(m1, fmaxf(fabsf(y[b][2 * f + 1].x), fabsf(y[b][2 * f + 1].y)));
+              }
             }
-          }
+          };
+          if (mild) all(std::true_type{});
+          else all(std::false_type{});
 #pragma unroll
           for (int o = 1; o < 4; o <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
