@@ -785,11 +785,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < chunks; ++c, ++n) {
           const int st = n % kStages;
           const int t0 = c * kC, rows = min(kC, piece.len - t0);
-          // A log decay below -160 (in units of log2) is a decay of zero in fp32 and is held
-          // there.
+          // A log decay below -320 (in units of log2) is held there: a decay of zero in fp32,
+          // also where the chunk's other rows grow by all that fp32 has room for.
           auto held = [](float l) {
             l *= kLog2e;
-            asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-160.0f));
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(l) : "f"(-320.0f));
             return l;
           };
           const float d0 = held(l0), d1 = held(l1);

@@ -63,3 +63,28 @@ def test_weights_after_what_was_forgotten(io, d, forgotten, at):
     for r in (at, 64 + at):
         size = float((q[r, 0].double() * k[r, 0].double()).sum()) * d ** -0.5 * v[r].abs().double()
         assert bool((out[r].cpu().double().abs() <= ROOM[io] * size + 2.0 ** -25).all()), r
+
+
+@pytest.mark.parametrize("io", [F16, BF16])
+@pytest.mark.parametrize("last", [-math.inf, -1e4, -230.0])
+@pytest.mark.parametrize("form", ["prompt", "tokens"])
+def test_growth_brings_nothing_forgotten_back(io, last, form):
+    """A state and rows that are forgotten, then growth by e^80 over the chunk's other rows:
+    what is left of them is zero (e^-230 e^80 is below fp32's range)."""
+    g, H, d, rows = gen(3), 2, 64, 64
+    q, k = (torch.randn(rows, H, d, generator=g).to(io) for _ in range(2))
+    v = torch.randn(rows, H, d, generator=g).to(io)
+    v[10:] = 0.0
+    ld = torch.full((rows, H), 80.0 / 53)
+    ld[:10], ld[10] = 0.0, last
+    pool = torch.randn(1, H, d, d, generator=g).to(DEV)
+    args = [t.to(DEV) for t in (q, k, v)]
+    cu = cu_of([rows]).to(DEV)
+    if form == "prompt":
+        out = ssu.linattn_fwd_varlen(*args, cu, log_decay=ld.to(DEV), state=pool)
+    else:
+        out = ssu.linattn_update_varlen(pool, *args, log_decay=ld.to(DEV), cu_seqlens=cu,
+                                        state_batch_indices=torch.zeros(1, rows, dtype=torch.int32,
+                                                                        device=DEV))
+    assert bool(out[:10].any()) and not bool(out[10:].any())
+    assert not bool(pool.any())
