@@ -1121,7 +1121,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool dead = false;
       float by = 1.0f;
       if constexpr (!kBF16) {
-        // the largest |w v| of the chunk comes to 2^14
+        // the largest finite |w v| of the chunk comes to 2^14
         float m = 0.0f;
 #pragma unroll
         for (int s = lane; s < kC; s += 32) {
@@ -1136,7 +1136,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           if (s < rows) m = fmaxf(m, sm.tab[st].w[s] * fmaxf(__low2float(top), __high2float(top)));
         }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (most == 0x7f800000u) {
+          // the channel of an infinite value is lost (below); the others keep their scale
+          m = 0.0f;
+#pragma unroll 1
+          for (int j = lane; j < rows * (DV / 4); j += 32) {
+            const int s = j / (DV / 4), i = j % (DV / 4);
+            const float x = fabsf(__half2float(*reinterpret_cast<const __half*>(
+                v + tile_at(s, 4 * (i / 8) + w4) + i % 8 * 2)));
+            if (x < INFINITY) m = fmaxf(m, sm.tab[st].w[s] * x);
+          }
+          most = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        }
         if (lane == 0) sm.v_max[st][w4] = most;
         if (!meet(sm, g.err, &sm.v_warps, met)) dead = true;
         m = __uint_as_float(max(max(sm.v_max[st][0], sm.v_max[st][1]),

@@ -1,0 +1,69 @@
+"""Linear attention over fp16 prompts, whose products are brought to the middle of
+fp16's range by powers of two: values that are not finite."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import mamba2_ssm_decode_gb300 as ssu
+
+from .test_layer_gpu import BF16, F16, F32, same_bits
+from .test_serving_gpu import lin_inputs, lin_prompt
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mamba2_ssm_decode_gb300 import build
+    build.build()
+    yield
+    assert ssu.ssu_device_error() == 0
+
+
+def copied(i, rows, G, dk, H, dv):
+    """The inputs on a projection of their own."""
+    wide = i["q"].as_strided((rows, 2 * G * dk + H * dv), (i["q"].stride(0), 1), 0).clone()
+    cut = lambda a, n, d: wide[:, a:a + n * d].unflatten(1, (n, d))  # noqa: E731
+    return dict(i, q=cut(0, G, dk), k=cut(G * dk, G, dk), v=cut(2 * G * dk, H, dv),
+                log_decay=i["log_decay"].clone())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("name,at", [("q", 70), ("k", 70), ("v", 70), ("v", 5), ("v", 100), ("v", 129)])
+@pytest.mark.parametrize("io,dk,dv", [(F16, 64, 64), (F16, 128, 128), (F16, 128, 64), (BF16, 64, 128)])
+@pytest.mark.parametrize("lens,H", [([30, 100, 40], 4), ([30, 1500], 2)])
+def test_bad_values_leave_the_rest_alone(name, at, bad, io, dk, dv, lens, H):
+    """Rows before the value, the other sequences, and the heads (of v: the channels) that
+    it does not touch have the bits of a call with a zero in its place; small values
+    beside an fp32 state, in whole sequences and in pieces."""
+    T, G = sum(lens), 2
+    i = lin_inputs(T, H, G, dk, dv, len(lens), io, F32, seed=12)
+    i["v"].mul_(2.0 ** -10)
+    i["pool"].mul_(2.0 ** -10)
+    i[name][at, 0 if name != "v" else 1, 17] = 0.0
+    want, want_pool = lin_prompt(i, lens)
+    j = copied(i, T, G, dk, H, dv)
+    j[name][at, 0 if name != "v" else 1, 17] = bad
+    got, pool = lin_prompt(j, lens)
+    s = 0 if at < 30 else 1
+    end = sum(lens[:s + 1])
+    heads = [1] if name == "v" else list(range(H // G))
+    clean = torch.ones(T, H, dv, dtype=torch.bool)
+    state = torch.ones_like(pool.cpu(), dtype=torch.bool)
+    for h in heads:
+        if name == "v":
+            clean[at:end, h, 17] = state[s, h, 17] = False
+        elif name == "k":
+            clean[at:end, h] = state[s, h] = False
+        else:
+            clean[at, h] = False
+    same_bits(got.cpu()[clean], want.cpu()[clean])
+    same_bits(pool.cpu()[state], want_pool.cpu()[state])
+    assert not bool(torch.isfinite(got.cpu()[~clean]).any())
+    if name == "v":
+        assert not bool(torch.isfinite(pool[s, 1, 17]).any())
