@@ -533,11 +533,12 @@ __device__ __forceinline__ uint32_t part_cut(float2& v) {
 }
 
 // The power of two that brings m to [2^to, 2^(to + 1)), and its reciprocal; 1 where m
-// is 0 or not finite.  Held so that both are fp32 numbers.
+// is 0 or not finite.  Held so that both are normal fp32 numbers: an m below 2^(to - 126)
+// stays lower.
 __device__ __forceinline__ float toward(float m, int to, float* back) {
   const int field = (int)(__float_as_uint(m) >> 23) & 255;
   int e = field - 127 - to;
-  e = field == 255 || !(m > 0.0f) ? 0 : e < -100 ? -100 : e > 110 ? 110 : e;
+  e = field == 255 || !(m > 0.0f) ? 0 : e < -126 ? -126 : e;
   *back = __uint_as_float((uint32_t)(127 + e) << 23);
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }

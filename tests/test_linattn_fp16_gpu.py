@@ -67,3 +67,22 @@ def test_bad_values_leave_the_rest_alone(name, at, bad, io, dk, dv, lens, H):
     assert not bool(torch.isfinite(got.cpu()[~clean]).any())
     if name == "v":
         assert not bool(torch.isfinite(pool[s, 1, 17]).any())
+
+
+def test_weighed_values_over_the_whole_range():
+    """A value that grows to 2^127 before its product with k is added, and one that shrinks
+    to 2^-120: the state is the value within 2^-15 (an exponent of 111 to 136 is held to
+    2^-17, the parts of a value near the largest one to 2^-22)."""
+    rows, d = 64, 64
+    for v0, total, k0 in ((60000.0, 77.0, 2.0 ** -10), (2.0 ** -10, -76.0, 1.0)):
+        q, k, v = (torch.zeros(rows, 1, d, dtype=F16) for _ in range(3))
+        v[0], k[0] = v0, k0
+        v[0, 0, ::2] = v0 / 4
+        ld = torch.full((rows, 1), total / 63)
+        pool = torch.zeros(1, 1, d, d)
+        i = dict(q=q, k=k, v=v, log_decay=ld, pool=pool)
+        out, got = lin_prompt(i, [rows])
+        want = v[0, 0].double() * k0 * math.exp(float(ld[1:].double().sum()))
+        off = (got.cpu()[0, 0].double() / want[:, None] - 1.0).abs()
+        assert float(off.max()) <= 2.0 ** -15, float(off.max())
+        assert not bool(out.any())
