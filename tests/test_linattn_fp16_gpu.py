@@ -1,15 +1,18 @@
 """Linear attention over fp16 prompts, whose products are brought to the middle of
-fp16's range by powers of two: values that are not finite."""
+fp16's range by powers of two: values that are not finite, at the ends of the range,
+and decays there."""
 from __future__ import annotations
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import mamba2_ssm_decode_gb300 as ssu
+from oracle import serving
 
-from .test_layer_gpu import BF16, F16, F32, same_bits
+from .test_layer_gpu import BF16, F16, F32, cu_of, gen, same_bits, within
 from .test_serving_gpu import lin_inputs, lin_prompt
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +89,67 @@ def test_weighed_values_over_the_whole_range():
         off = (got.cpu()[0, 0].double() / want[:, None] - 1.0).abs()
         assert float(off.max()) <= 2.0 ** -15, float(off.max())
         assert not bool(out.any())
+
+
+def rows_check(i, lens, got, pool, init=None):
+    """As the tolerances of prompts in chunks have it, and nothing for the size of the
+    sums that an exponent comes from."""
+    o, bound, size, after, off, written = serving.linattn(
+        i["q"], i["k"], i["v"], i["log_decay"], i["q"].shape[2] ** -0.5, prompt=True,
+        eps=2.0 ** -18, pool=i["pool"], nseqs=len(lens), cu=cu_of(lens), init=init)
+    bound = bound + size * 2.0 ** -15
+    # from half a unit above the largest number on (65520 in fp16), a rounding gives infinity
+    most = torch.finfo(got.dtype).max * (1.0 + torch.finfo(got.dtype).eps / 4)
+    g = got.cpu().double().numpy()
+    beyond = np.abs(o) - bound >= most
+    assert (g[beyond] == np.copysign(np.inf, o[beyond])).all()
+    bound[np.abs(o) + bound >= most] = np.inf
+    within(got, o, bound, "out")
+    w = sorted(written)
+    within(pool[w], after[w], off[w], "state")
+
+
+@pytest.mark.parametrize("case", ["forget", "far", "tiny", "steep", "grow", "mixed", "most", "turns"])
+@pytest.mark.parametrize("io,dk,dv", [(F16, 64, 64), (F16, 128, 128), (F16, 64, 128), (BF16, 128, 64)])
+@pytest.mark.parametrize("lens,H", [([200, 33], 4), ([1500], 2)])
+def test_decays_at_the_ends_of_the_range(case, io, dk, dv, lens, H):
+    T = sum(lens)
+    i = lin_inputs(T, H, H, dk, dv, len(lens), io, F32, seed=7)
+    g = gen(10)
+    ld = i["log_decay"]
+    if case == "forget":            # everything before is gone
+        ld[torch.rand(T, H, generator=g) < 0.1] = -math.inf
+    elif case == "far":             # far below what fp32's exponential holds
+        ld[torch.rand(T, H, generator=g) < 0.1] = -1e30
+    elif case == "tiny":
+        ld.mul_(1e-7)
+    elif case == "steep":
+        ld.mul_(200.0)
+    elif case == "grow":            # a state that grows by e^2 over a chunk
+        ld.fill_(2.0 / 64)
+    elif case == "mixed":           # slow heads beside ones that forget at once
+        ld[:, 0], ld[:, 1] = 0.0, -math.inf
+        ld[::3, H - 2], ld[:, H - 1] = -90.0, -1e-9
+    elif case == "most":            # nearly every row forgotten, then slow ones
+        ld[:] = -math.inf
+        ld[torch.arange(T) % 64 > 55] = -1e-3
+    else:                           # growth by e^10 within 16 rows, and as much lost in the next
+        ld[:] = torch.where(torch.arange(T) % 32 < 16, 10.0 / 16, -10.0 / 16)[:, None]
+    got, pool = lin_prompt(i, lens)
+    rows_check(i, lens, got, pool)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("lens", [[150], [1500]])
+@pytest.mark.parametrize("state", ["large", "small"])
+def test_states_far_from_one(dk, dv, lens, state):
+    """A state beside which fp16 has no room, and values near its smallest, also in pieces."""
+    by = 1e6 if state == "large" else 1e-5
+    i = lin_inputs(lens[0], 2, 2, dk, dv, 1, F16, F32, "token", seed=11)
+    i["log_decay"] = i["log_decay"] / 16
+    i["pool"] = i["pool"] * by
+    i["q"] = (i["q"].float() * (1e-6 if state == "large" else 1.0)).to(F16)
+    if state == "small":
+        i["v"] = (i["v"].float() * 1e-3).to(F16)
+    got, pool = lin_prompt(i, lens)
+    rows_check(i, lens, got, pool)
