@@ -143,6 +143,18 @@ __device__ __forceinline__ unsigned long long weight(float r) {
   return w.sum();
 }
 
+// floor(u W), in whole numbers (u is m 2^-s with m below 2^24): a product in fp64 rounds up to
+// the next token's border once in some hundred.  Below W: 0 for NaN and below 0, W - 1 from 1 on.
+__device__ __forceinline__ unsigned long long mark_of(float u, unsigned long long W) {
+  if (!(u > 0.0f)) return 0;
+  if (u >= 1.0f) return W - 1;
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int s = 150 - (int)(e ? e : 1u);  // 24 to 149
+  const unsigned long long low = W * m, high = __umul64hi(W, m);
+  return s < 64 ? high << (64 - s) | low >> s : s < 128 ? high >> (s - 64) : 0;
+}
+
 template <class T>
 __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
@@ -282,10 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) drafts_verify_kernel(const Args a
         }
         for (int w = 0; w < warp; ++w) before += sm.sum[w];
         if (total > 0) {
-          // floor(u total), below total
-          const double m = floor(fmin(fmax((double)u, 0.0), 1.0) * (double)total);
-          unsigned long long mark = m < 9.2e18 ? (unsigned long long)m : total - 1;
-          mark = mark < total ? mark : total - 1;
+          const unsigned long long mark = mark_of(u, total);
           // the warp whose share holds it finds the token
           if (mark >= before && mark - before < sum) {
             unsigned long long run = before;

@@ -19,6 +19,9 @@ Pins: tests/test_oracle_serving.py.
 """
 from __future__ import annotations
 
+import math
+from fractions import Fraction
+
 import numpy as np
 
 from .layer import F32_MAX, _f64, _ints, sequences
@@ -119,7 +122,7 @@ def verify(p, drafts, u, q=None, cu=None, greedy=None):
             token = -1
             if total:
                 draw = float(u[s, K]) if u[s, K] == u[s, K] else 0.0
-                mark = min(int(np.floor(min(max(draw, 0.0), 1.0) * float(total))), total - 1)
+                mark = min(math.floor(Fraction(min(max(draw, 0.0), 1.0)) * total), total - 1)
                 run = 0
                 for i, x in enumerate(w):
                     run += x
