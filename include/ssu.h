@@ -709,8 +709,8 @@ ssu_status ssu_linattn_update(const ssu_linattn_params* p, int64_t nseqs, int64_
                               const ssu_slot_table* src, const ssu_slot_table* dst,
                               ssu_dtype index_dtype, struct CUstream_st* stream);
 
-/* Bytes of workspace ssu_linattn_fwd_varlen needs for these sizes (0: none; -1
- * for a negative size). */
+/* Bytes of workspace ssu_linattn_fwd_varlen needs for these sizes (0: none, also
+ * for sizes that it refuses; -1 for a negative size). */
 int64_t ssu_linattn_workspace_bytes(int64_t rows, int64_t nseqs, int64_t nheads, int64_t dv,
                                     int64_t dk, ssu_dtype io_dtype);
 

@@ -145,7 +145,9 @@ ssu_status ssu_linattn_update(const ssu_linattn_params* c, int64_t nseqs, int64_
 int64_t ssu_linattn_workspace_bytes(int64_t rows, int64_t nseqs, int64_t nheads, int64_t dv,
                                     int64_t dk, ssu_dtype io_dtype) {
   if (rows < 0 || nseqs < 0 || nheads < 0 || dv < 0 || dk < 0) return -1;
-  if (rows == 0 || nseqs == 0 ||
+  // sizes that the call refuses
+  if (rows > 0x7fffffffLL - 1024 || nseqs >= 1LL << 30 || nheads > linattn::kMostHeads) return 0;
+  if (rows == 0 || nseqs == 0 || nheads == 0 ||
       !linattn::takes_prompt(rows, nseqs, nheads, dv, dk, io_dtype))
     return 0;
   return linattn::prompt_workspace(rows, nseqs, nheads, dv, dk);

@@ -23,7 +23,8 @@ struct Layout {
     const int64_t sms = ssu::sm_count();
     const int64_t chunks = (rows + kC - 1) / kC;
     // every SM's share of the chunks; sequences beyond it are cut into pieces of a third of it
-    const int64_t share = (chunks * heads + sms - 1) / sms;
+    const int64_t all = (chunks * heads + sms - 1) / sms;
+    const int64_t share = all < 1 << 30 ? all : 1 << 30;  // (a single SM's of 2^31 rows)
     cut = (int)((share + 2) / 3 > 4 ? (share + 2) / 3 : 4);
     // ... where that saves more than the two launches it takes, some four chunks' time
     const int64_t worth = 2 * (int64_t)cut + 4;
