@@ -840,7 +840,7 @@ ssu_status ssu_prompt_maps(const ssu_prompt_maps_params* p, struct CUstream_st* 
  *   fresh        [nseqs, steps]: the slots newly given, pad_slot_id elsewhere
  *                (what ssu_slots_clear takes).
  *   num_missing  entries that got none because no slot was left (pad_slot_id).
- * Up to 2^20 slots and 2^24 entries.  One launch.
+ * pad_slot_id has to fit index_dtype.  Up to 2^20 slots and 2^24 entries.  One launch.
  */
 ssu_status ssu_slots_assign(const void* table, const void* counts, ssu_dtype index_dtype,
                             int64_t nseqs, int64_t steps, int64_t slots, int64_t pad_slot_id,

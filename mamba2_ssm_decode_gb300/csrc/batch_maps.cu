@@ -418,6 +418,10 @@ static ssu_status assign(const void* table, const void* counts, ssu_dtype index_
     return fail(SSU_ERR_INVALID_ARGUMENT, "the slot table and counts must be int32 or int64");
   if (nseqs < 0 || steps < 0 || slots < 0)
     return fail(SSU_ERR_INVALID_ARGUMENT, "nseqs, steps and slots must be >= 0");
+  // it is written into the tables
+  if (index_dtype == SSU_I32 && pad != (int32_t)pad)
+    return fail(SSU_ERR_INVALID_ARGUMENT, "pad_slot_id %lld is no int32, which the table holds",
+                (long long)pad);
   if (slots > kMostSlots) return fail(SSU_ERR_UNSUPPORTED, "slots must not exceed 2^20");
   if (nseqs > 0x7fffffffLL || steps > 0x7fffffffLL || (steps > 0 && nseqs > (1 << 24) / steps))
     return fail(SSU_ERR_UNSUPPORTED, "the table must not exceed 2^24 entries");

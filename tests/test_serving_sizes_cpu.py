@@ -6,6 +6,8 @@ import sys
 
 from mamba2_ssm_decode_gb300 import _abi
 
+from .test_layer_abi_cpu import FAKE, INVALID
+
 
 def test_linattn_workspace_of_any_sizes():
     """A query of sizes that no call takes is answered (a division by zero would end the
@@ -28,3 +30,15 @@ def test_linattn_workspace_of_refused_sizes():
     f = _abi.lib().ssu_linattn_workspace_bytes
     for rows, nseqs, heads in ((2 ** 31 - 1024, 1, 1), (64, 2 ** 30, 1), (64, 1, 4097), (64, 1, 0)):
         assert f(rows, nseqs, heads, 64, 64, _abi.SSU_BF16) == 0
+
+
+def test_assignment_refuses_a_pad_that_the_table_cannot_hold():
+    """2^32 would be written into an int32 table as 0: a valid slot."""
+    lib = _abi.lib()
+
+    def call(pad, idx):
+        return lib.ssu_slots_assign(FAKE, FAKE + 4096, idx, 0, 2, 8, pad, FAKE + 8192, FAKE + 12288,
+                                    FAKE + 16384, None)
+
+    for pad in (1 << 32, 1 << 31, -(1 << 31) - 1):
+        assert call(pad, _abi.SSU_I32) == INVALID and "int32" in lib.ssu_last_error().decode()
