@@ -3,9 +3,9 @@
 //
 // A state is read and written once and bounds the call: 256 tokens of 32 heads of 128 x
 // 128 fp32, 163 us (1082 MB, 98 % of a copy's rate).  128 sequences of 1 to 4 drafted
-// tokens, 80 heads of 64 x 128 bf16, where the state is written after each: 134 us (595
-// MB; 70 % of issue slots).  With the next row's operands in registers meanwhile they
-// took 187 and 148 us: warps cover the loads better than registers do.
+// tokens, 80 heads of 64 x 128 bf16, where the state is written after each: 128 us (595
+// MB).  With the next row's operands in registers meanwhile they took 187 and 148 us:
+// warps cover the loads better than registers do.
 #pragma once
 
 #include "linattn.cuh"
@@ -96,9 +96,18 @@ struct WalkState {
   }
 };
 
+// CTAs an SM that a sequence of several rows is bounded to: warps cover what its rows wait
+// for.  128 sequences of 1 to 4 rows, 32 heads of 128 x dk: fp32 and dk 32 56.9 us for 59.8
+// unbounded, dk 64 53.7 for 57.5; bf16 and dk 64 76.5 at ten and 80.3 at eight.  From dk 128
+// on nine fit; bounded to that, other code spilled (80 heads of 64 x 128 bf16: 133 -> 141 us).
+template <class ST, int DK, bool ONE>
+constexpr int walk_ctas() {
+  return ONE || DK >= 128 ? 0 : DK == 64 && sizeof(ST) == 2 ? 10 : 8;
+}
+
 // Tokens.  ONE: a row a sequence, which is that of its number.
 template <class ST, class IT, int DK, bool ONE>
-__global__ void __launch_bounds__(kWalkWarps * 32)
+__global__ void __launch_bounds__(kWalkWarps * 32, (walk_ctas<ST, DK, ONE>()))
     linattn_walk_kernel(const Args p, const Seqs a) {
   using L = WalkLayout<ST, DK, ONE>;
   constexpr int U = L::U, E = L::E, VEC = L::VEC, CPL = L::CPL, LPR = L::LPR;
@@ -114,16 +123,25 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
   WalkState<ST, DK, ONE> state;
   state.load(static_cast<const ST*>(p.state) + (it.src * p.H + h) * head, it.read_ok, p0, p.dv, ql);
 
-  const IT* qp = static_cast<const IT*>(p.q) + (int64_t)it.r0 * p.q_rs + (int64_t)g * p.q_gs;
-  const IT* kp = static_cast<const IT*>(p.k) + (int64_t)it.r0 * p.k_rs + (int64_t)g * p.k_gs;
-  const IT* vp = static_cast<const IT*>(p.v) + (int64_t)it.r0 * p.v_rs + (int64_t)h * p.v_hs;
-  IT* op = static_cast<IT*>(p.out) + (int64_t)it.r0 * p.o_rs + (int64_t)h * p.o_hs;
-  const float* lp = p.ld ? p.ld + (int64_t)it.r0 * p.ld_rs + (int64_t)h * p.ld_hs : nullptr;
+  const IT *qp, *kp, *vp;
+  IT* op;
+  const float* lp;
+  auto row_at = [&](int t) {
+    const int64_t r = it.r0 + t;
+    qp = static_cast<const IT*>(p.q) + r * p.q_rs + (int64_t)g * p.q_gs;
+    kp = static_cast<const IT*>(p.k) + r * p.k_rs + (int64_t)g * p.k_gs;
+    vp = static_cast<const IT*>(p.v) + r * p.v_rs + (int64_t)h * p.v_hs;
+    op = static_cast<IT*>(p.out) + r * p.o_rs + (int64_t)h * p.o_hs;
+    lp = p.ld ? p.ld + r * p.ld_rs + (int64_t)h * p.ld_hs : nullptr;
+  };
+  // Several rows of wide states: each one's addresses are worked out when it comes.  Kept along
+  // they take ten registers and a CTA an SM or three: 128 sequences of 1 to 4 rows, 32 heads of
+  // 128 x 128 fp32, take 223 us for 175 (narrow states: 63 for 54).
+  constexpr bool AGAIN = !ONE && DK >= 128;
+  row_at(0);
 
-  // counted down, so that a step's place in the slot table is worked out when it is needed:
-  // kept along, it and what hangs on it take six registers and 19 us of the drafts' time
-  for (int left = it.len; left > 0; --left) {
-    const int t = it.len - left;
+  for (int t = 0; t < it.len; ++t) {
+    if constexpr (AGAIN) row_at(t);
     float k[E], q[E], y[U];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
@@ -144,11 +162,13 @@ __global__ void __launch_bounds__(kWalkWarps * 32)
     int64_t to;
     if (it.read_ok && !p.disable && write_slot(a, s, t, p.pad, p.slots, &to))
       state.store(static_cast<ST*>(p.state) + (to * p.H + h) * head, p0, p.dv, ql);
-    qp += p.q_rs;
-    kp += p.k_rs;
-    vp += p.v_rs;
-    op += p.o_rs;
-    if (lp) lp += p.ld_rs;
+    if constexpr (!AGAIN) {
+      qp += p.q_rs;
+      kp += p.k_rs;
+      vp += p.v_rs;
+      op += p.o_rs;
+      if (lp) lp += p.ld_rs;
+    }
   }
 }
 
