@@ -312,8 +312,9 @@ struct alignas(16) Tables {  // of a chunk, in units of log2; read in pairs
   float w[kC];         // e^(a_C - a_s); 0 behind the last row
   float r[kC / 16];    // the four r
   float keep, add;     // e^(a_C) = keep + add, keep 0 or 1
-  int mild;            // e^(a_t - r) and e^(r - a_s) stay within 2^60 inside the 16 of an r, and
-                       // a_t within 128, so that a_t - r is off by 2^-17 at most
+  int mild;            // inside the 16 of an r, e^(a_t - r) stays below 2^60 and e^(r - a_s) below
+                       // 2 (it can lift nothing that e^(a_t - r) loses at 2^-126), and a_t stays
+                       // within 128, so that a_t - r is off by 2^-17 at most
 };
 
 // A tile: 64 rows (tokens) of 128 bytes, one after the other, the 16-byte pieces
@@ -831,8 +832,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const float a0 = two0.x + two0.y, a1 = two1.x + two1.y;
           const float2 ea = make_float2(p.scale * ex2(a0), p.scale * ex2(a1));
           const float2 w = make_float2(t < rows ? ex2(w0) : 0.0f, t + 1 < rows ? ex2(w1) : 0.0f);
-          const bool mild = __all_sync(0xffffffffu, fabsf(x0) <= 60.0f && fabsf(x1) <= 60.0f &&
-                                                        fabsf(a0) <= 128.0f && fabsf(a1) <= 128.0f);
+          const bool mild = __all_sync(0xffffffffu, x0 >= -60.0f && x0 <= 1.0f && x1 >= -60.0f &&
+                                                        x1 <= 1.0f && fabsf(a0) <= 128.0f &&
+                                                        fabsf(a1) <= 128.0f);
           // near 1 the decay is 1 + add: rounded by itself it would be off by the same
           // 2^-25 chunk after chunk
           const float e = ex2(end);

@@ -88,3 +88,20 @@ def test_growth_brings_nothing_forgotten_back(io, last, form):
                                                                         device=DEV))
     assert bool(out[:10].any()) and not bool(out[10:].any())
     assert not bool(pool.any())
+
+
+@pytest.mark.parametrize("io", [F16, BF16])
+def test_growth_that_is_lost_again(io):
+    """A value that grows by e^40 within 16 rows and shrinks by e^95 within the 46 after: what
+    is left, e^-55, counts where the scale says so.  An exponent of 137 is held to 2^-16."""
+    rows, d, scale = 64, 64, 2.0 ** 70
+    q, k, v = (torch.zeros(rows, 1, d, dtype=io) for _ in range(3))
+    q[:], k[0], v[0] = 0.125, 0.125, 1.0
+    ld = torch.zeros(rows, 1)
+    ld[1:16], ld[16:62] = 40.0 / 15, -95.0 / 46
+    out = ssu.linattn_fwd_varlen(q.to(DEV), k.to(DEV), v.to(DEV), cu_of([rows]).to(DEV),
+                                 log_decay=ld.to(DEV), scale=scale, state=torch.zeros(1, 1, d, d, device=DEV))
+    want = scale * torch.exp(ld.double().cumsum(0))[:, :, None].expand(rows, 1, d)
+    there = want < torch.finfo(io).max
+    off = (out.cpu().double() / want - 1.0).abs()[there]
+    assert there[61:].all() and float(off.max()) <= torch.finfo(io).eps / 2 + 2.0 ** -14
