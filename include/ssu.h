@@ -679,7 +679,8 @@ ssu_status ssu_slots_compact(const ssu_pool* pools, int npools, int64_t slots, c
  * log_decay  ld, fp32, element (r, h) at r * log_decay_row_stride +
  *            h * log_decay_head_stride (a row stride of 0: one value per head),
  *            or NULL: no decay.  -infinity forgets what came before.  Above 0 a
- *            state grows; prompts want e^(the sum over 64 rows) within fp32.
+ *            state grows.  Prompts want e^(the sum over up to 64 rows) within
+ *            fp32, and take it as zero below 2^-126.
  * disable_state_update  1: no slot is written (decode form).
  */
 typedef struct ssu_linattn_params {
@@ -806,7 +807,8 @@ ssu_status ssu_drafts_verify(const ssu_drafts_params* p, struct CUstream_st* str
  *   last_chunk_indices [nseqs]
  *   has_initial_state  [nseqs] bytes: context_lens > 0.
  *   row_seq, row_pos   [rows] or NULL: a row's sequence and position (context
- *                 included); -1 behind the last sequence.
+ *                 included); -1 behind the last sequence.  Positions have to fit
+ *                 index_dtype.
  * max_chunks must be at least rows / chunk_size + nseqs (2 nseqs with
  * context_lens), which no lengths exceed.  At most SSU_PROMPT_MAPS_MAX_SEQS
  * sequences, chunk_size at most 2^20.  One launch.

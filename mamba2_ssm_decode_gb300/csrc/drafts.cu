@@ -10,7 +10,7 @@
 // same inputs give the same token however the row is split.
 //
 // A chain of five loads and three meetings bounds one sequence (50288 tokens: 8.2 us),
-// and in 3.4 waves of CTAs a batch of 256 as well (128257 tokens, 230 MB: 64 us).
+// and in 3.4 waves of CTAs a batch of 256 as well (128257 tokens, 230 MB: 63 us).
 #include <cooperative_groups.h>
 
 #include "layer_common.cuh"
@@ -143,8 +143,8 @@ __device__ __forceinline__ unsigned long long weight(float r) {
   return w.sum();
 }
 
-// floor(u W), in whole numbers (u is m 2^-s with m below 2^24): a product in fp64 rounds up to
-// the next token's border once in some hundred.  Below W: 0 for NaN and below 0, W - 1 from 1 on.
+// floor(u W), in whole numbers (u is m 2^-s with m below 2^24): of 68 bits fp64 has 53, and may
+// round up to the whole number that is the next token's.  0 for NaN and below 0, W - 1 from 1 on.
 __device__ __forceinline__ unsigned long long mark_of(float u, unsigned long long W) {
   if (!(u > 0.0f)) return 0;
   if (u >= 1.0f) return W - 1;
@@ -363,9 +363,10 @@ __global__ void __launch_bounds__(kThreads, 2) drafts_verify_kernel(const Args a
 
 template <class T, bool VEC>
 static cudaError_t launch(const Args& a, cudaStream_t stream) {
-  // More CTAs while a warp has more than one step, up to four CTAs an SM in all: for one
-  // sequence of 50288 tokens 1, 2, 4 and 8 take 25, 12, 9.6 and 8.2 us, for 256 of 128257
-  // 2, 4 and 8 take 65, 66 and 87 us.
+  // Twice as many CTAs while a warp has more than one step and all sequences together have
+  // fewer than four CTAs an SM (so below eight in the end): for one sequence of 50288 tokens
+  // 1, 2, 4 and 8 take 25, 12, 9.6 and 8.2 us, for 256 of 128257 2, 4 and 8 take 65, 66 and
+  // 87 us.
   int ctas = 1;
   while (ctas < 8 && a.V > ctas * kWarps * kStep && (int64_t)a.n * ctas < 4LL * ssu::sm_count())
     ctas *= 2;

@@ -22,6 +22,11 @@
 // 2^-17, which shows in an fp32 state) or two of fp16.  fp16 has no room for what
 // is large or small: there the rows of P and S and all of a chunk's w V are brought
 // to the middle of its range by powers of two, which are taken out of the products.
+// (One power for all of w V: a channel whose largest value is below 2^-17 of the
+// chunk's keeps fewer than 22 bits in the state, 16 at 2^-23, down to fp16's last
+// subnormal.  A power for each channel would have every warp look at all tokens.)
+// Exponents are differences of 64-bit sums, or are taken so that 2^-17 is left of them
+// at most; e^ a sum counts as zero below 2^-126.
 //
 // One CTA of 24 warps works on a chunk of one head at a time, chunks of a
 // sequence in order: 4 warps turn scores into P, 4 write outputs, 8 update S (each
@@ -31,15 +36,16 @@
 // Items -- a sequence's, or a piece's, chunks of one head -- are handed out by a
 // counter, longest first.  A sequence of more chunks than every SM's fair share
 // is cut into pieces: a first launch computes what each piece adds to the state
-// (the fourth product alone) and its decay, a second one adds them up to the state
-// that enters each piece.  Every launch but the first is set up while the one before
+// (the fourth product alone) and the exponent of its decay, a second one adds them up
+// to the state that enters each piece.  Every launch but the first is set up while the one before
 // runs (programmatic dependent launch).
 //
-// 20634 tokens of 16 prompts, 32 heads of 128 x 128 in bf16: 202 us (HBM's floor 108,
-// the tensor pipe's 62).  A chunk takes some 4000 cycles; what bounds it is the issue of
-// instructions (48 % of the slots) and their supply (2.8 cycles an instruction: six roles
-// share each scheduler's instruction cache), so fewer instructions count, and neither more
-// stages (210 us) nor fewer waits (204).
+// 20634 tokens of 16 prompts, 32 heads of 128 x 128 in bf16: 204 us (HBM's floor 108,
+// the tensor pipe's 62).  A chunk takes some 4000 cycles, in which the roles wait for one
+// another: of a warp's cycles for each instruction 4.9 go to barriers and memory, 2.0 to
+// the next instruction (six roles share each scheduler's instruction cache), 1.4 to fixed
+// latencies, 1.2 to shared memory; 48 % of the issue slots are used.  More stages (210 us)
+// and fewer waits for them (204) took nothing off.
 #pragma once
 
 #include <cuda.h>

@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kWalkWarps * 32, (walk_ctas<ST, DK, ONE>()))
 }
 
 // Prompts: the same walk, with blocks of kBlock rows brought to shared memory as fp32
-// while the block before is computed.  A chain of rows bounds it: 16 prompts of 128 rows, 8
-// heads of 128 x 128 fp32, take 87 us, and 275 with a row's operands asked for in its turn;
-// 256 prompts of one or two rows 174 us against 222.
+// while the block before is computed.  The longest prompt's chain of rows bounds it: 16 prompts
+// of 128 rows on average and up to 197, 8 heads of 128 x 128 fp32, take 86 us, and 275 with a
+// row's operands asked for in its turn; 256 prompts of two rows on average 173 us against 222.
 constexpr int kBlock = 8;
 
 template <class ST, class IT, int DK>

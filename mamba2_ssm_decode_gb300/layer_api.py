@@ -349,9 +349,10 @@ def prompt_maps(lens, chunk_size, rows, context_lens=None, max_chunks=None, out=
 
     lens [S] int32/int64: each sequence's tokens in this call; ``rows``: the rows
     of the packed tensors, at least their sum (what is beyond is cut off);
-    context_lens [S]: tokens before this call; ``max_chunks``: room for chunks
-    (None: as many as there can be); ``out``: the PromptMaps of an earlier call
-    with the same sizes to write again.  Returns a PromptMaps."""
+    context_lens [S]: tokens before this call (positions have to fit lens' dtype);
+    ``max_chunks``: room for chunks (None: as many as there can be); ``out``: the
+    PromptMaps of an earlier call with the same sizes to write again.  Returns a
+    PromptMaps."""
     n = lens.numel()
     if max_chunks is None:
         if out is not None:
